@@ -13,7 +13,8 @@ past the last offset are padding, whose outputs are zero).
 
 8-bit activations: every channel's 16 consecutive tokens share one power of two 2^e,
 e = floor(log2(max |v|)), and each value is held as the whole number nearest to
-v * 2^(6 - e), at most 127 in magnitude.
+v * 2^(6 - e), at most 127 in magnitude.  The forward also keeps the state (float32) that
+enters every 64 tokens; a backward from 8 bits starts each such block from that state.
 
 A case's "op": "step" (one token for every row against a state pool), "fwd" (whole
 sequences), "train" (forward and backward), "train8" (the same with the backward reading
@@ -26,6 +27,7 @@ import torch
 own = False
 
 GROUP = 16     # tokens that share a power of two
+BLOCK = 64     # tokens between the states that a forward keeps
 DECAY = 8.0    # decay_scale
 
 
@@ -198,7 +200,15 @@ def _gates(x, r, i, lam, r_bias, i_bias):
     return rho, iota, kappa, log_a, torch.exp(log_a), torch.sqrt(-torch.expm1(2.0 * log_a))
 
 
+def _before(s, h, first, row):
+    """The state that each token continues."""
+    h0 = s["initial_state"]
+    start = torch.zeros(1, 1, h.shape[2], device="cuda") if h0 is None else h0[row]
+    return torch.where(first, start, torch.nn.functional.pad(h, (0, 0, 1, -1)))
+
+
 def _plain_fwd(s):
+    """The forward's outputs, and the state that each token continues."""
     x, r, i = s["x"].float(), s["r"].float(), s["i"].float()
     B, L, D = x.shape
     first, last, pad, row = _places(s, B, L)
@@ -220,21 +230,25 @@ def _plain_fwd(s):
             empty = (off[1:] == off[:-1])[:, None]
             zero = torch.zeros(off.numel() - 1, D, device="cuda") if h0 is None else h0
             out["last_state"] = torch.where(empty, zero, h[0][(off[1:] - 1).clamp(min=0)])
-    return out
+    return out, _before(s, h, first, row)
 
 
-def _plain_bwd(s, x, r, i, z):
-    """Gradients, the activations given apart (as they are, or as 8 bits stand for)."""
+def _plain_bwd(s, x, r, i, z, prev):
+    """Gradients.  The activations are given apart: as they are, with the states that the tokens
+    continue, or as 8 bits stand for, when those states are kept at the blocks' starts only."""
     x, r, i, dy = x.float(), r.float(), i.float(), s["dy"].float()
     B, L, D = x.shape
     first, last, pad, row = _places(s, B, L)
     rho, iota, kappa, log_a, a, m = _gates(x, r, i, s["lam"], s["r_bias"], s["i_bias"])
     u = iota * x
     h0 = s["initial_state"]
-    before = torch.zeros(1, 1, D, device="cuda") if h0 is None else h0[row]
     cut = torch.where(first, torch.zeros_like(a), a)
-    h = _scan(cut, torch.where(first, m * u + a * before, m * u))
-    prev = torch.where(first, before, torch.nn.functional.pad(h, (0, 0, 1, -1)))
+    if s["op"] == "train8":
+        kept = first | (torch.arange(L, device="cuda") % BLOCK == 0)[None, :, None]
+        b = torch.where(kept, m * u + a * prev, m * u)
+        h = _scan(torch.where(kept, torch.zeros_like(a), a), b)
+        prev = torch.where(kept, prev, torch.nn.functional.pad(h, (0, 0, 1, -1)))
+    h = a * prev + m * u
     gy, dz = dy, None
     if z is not None:
         z = z.float()
@@ -311,12 +325,12 @@ def _plain(s):
         return _plain_step(s)
     if s["op"] == "act8":
         return {"x": _plain_act8(s["x"]).to(s["dtype"])}
-    out = _plain_fwd(s)
+    out, prev = _plain_fwd(s)
     if s["op"] == "train":
-        out.update(_plain_bwd(s, s["x"], s["r"], s["i"], s["z"]))
+        out.update(_plain_bwd(s, s["x"], s["r"], s["i"], s["z"], prev))
     elif s["op"] == "train8":
         z = None if s["z"] is None else _plain_act8(s["z"])
-        out.update(_plain_bwd(s, _plain_act8(s["x"]), _plain_act8(s["r"]), _plain_act8(s["i"]), z))
+        out.update(_plain_bwd(s, _plain_act8(s["x"]), _plain_act8(s["r"]), _plain_act8(s["i"]), z, prev))
     return out
 
 
@@ -437,7 +451,8 @@ def exact(case, seed):
         """The state before sequence n: [D], or [B, D] for a dense batch, whose rows go together."""
         return (h0 if dense else h0[n]) if h0 is not None else (zero.expand(B, D) if dense else zero)
 
-    def states(x, r, i):
+    def states(x, r, i, kept=None):
+        """Gates and states; with `kept`, the states h of another run of them enter each block."""
         rho, iota, a, m = _exact_gates(p, x, r, i)
         b = m * iota * x
         h = torch.zeros_like(x)
@@ -445,6 +460,8 @@ def exact(case, seed):
         for n, (lo, hi) in enumerate(bounds):
             now = start(n)
             for t in range(lo, hi):
+                if kept is not None and t > lo and t % BLOCK == 0:
+                    now = kept[:, t - 1]
                 now = torch.addcmul(b[:, t], a[:, t], now)
                 h[:, t] = now
             ends.append(now.reshape(-1, D))
@@ -456,10 +473,10 @@ def exact(case, seed):
         out["last_state"] = ends
     if case["op"] == "fwd":
         return out
-    x, r, i, z = d["x"], d["r"], d["i"], d["z"]
+    x, r, i, z, kept = d["x"], d["r"], d["i"], d["z"], h
     if case["op"] == "train8":
         x, r, i, z = (None if v is None else _exact_act8(v) for v in (x, r, i, z))
-        rho, iota, a, m, h, ends = states(x, r, i)
+        rho, iota, a, m, h, ends = states(x, r, i, kept)
     gy = d["dy"]
     if z is not None:
         sz = 1.0 / (1.0 + torch.exp(-z))
@@ -477,6 +494,9 @@ def exact(case, seed):
         if hi > lo:
             prev[:, lo] = start(n)
             prev[:, lo + 1:hi] = h[:, lo:hi - 1]
+            if case["op"] == "train8":
+                at = torch.arange(-(-(lo + 1) // BLOCK) * BLOCK, hi, BLOCK, device="cuda")
+                prev[:, at] = kept[:, at - 1]
     # g is zero at padding, and with it every gradient but dz, which h makes zero there
     dlog_a = g * (a * prev - iota * x * a * a / m)
     out["dx"], out["di"] = g * m * iota, g * m * x * iota * (1.0 - iota)
