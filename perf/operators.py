@@ -329,8 +329,10 @@ def _plain(s):
     if s["op"] == "train":
         out.update(_plain_bwd(s, s["x"], s["r"], s["i"], s["z"], prev))
     elif s["op"] == "train8":
-        z = None if s["z"] is None else _plain_act8(s["z"])
-        out.update(_plain_bwd(s, _plain_act8(s["x"]), _plain_act8(s["r"]), _plain_act8(s["i"]), z, prev))
+        pad = _places(s, *s["x"].shape[:2])[2]
+        x, r, i, z = (None if v is None else _plain_act8(v if pad is None else torch.where(pad, torch.zeros_like(v), v))
+                      for v in (s["x"], s["r"], s["i"], s["z"]))
+        out.update(_plain_bwd(s, x, r, i, z, prev))
     return out
 
 
@@ -475,6 +477,9 @@ def exact(case, seed):
         return out
     x, r, i, z, kept = d["x"], d["r"], d["i"], d["z"], h
     if case["op"] == "train8":
+        for v in (x, r, i, z):
+            if v is not None and not dense:
+                v[:, bounds[-1][1]:] = 0.0            # padding is kept as zeros
         x, r, i, z = (None if v is None else _exact_act8(v) for v in (x, r, i, z))
         rho, iota, a, m, h, ends = states(x, r, i, kept)
     gy = d["dy"]
@@ -495,7 +500,8 @@ def exact(case, seed):
             prev[:, lo] = start(n)
             prev[:, lo + 1:hi] = h[:, lo:hi - 1]
             if case["op"] == "train8":
-                at = torch.arange(-(-(lo + 1) // BLOCK) * BLOCK, hi, BLOCK, device="cuda")
+                at = torch.arange(lo + 1, hi, device="cuda")
+                at = at[at % BLOCK == 0]
                 prev[:, at] = kept[:, at - 1]
     # g is zero at padding, and with it every gradient but dz, which h makes zero there
     dlog_a = g * (a * prev - iota * x * a * a / m)
