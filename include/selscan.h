@@ -39,6 +39,8 @@
  *  - dstate (N) must be in [1, SSCAN_MAX_DSTATE]; seqlen at most SSCAN_MAX_SEQLEN.
  *  - `flags` selects variants of the method (SSCAN_FLAG_*); 0 is the method
  *    as defined above.
+ * The gated linear recurrence and the 8-bit activations at the end of this header
+ * follow the same conventions, with shapes of their own and no flags.
  */
 #ifndef SELSCAN_H
 #define SELSCAN_H
@@ -50,7 +52,7 @@
 extern "C" {
 #endif
 
-#define SSCAN_VERSION 410
+#define SSCAN_VERSION 420
 #define SSCAN_MAX_DSTATE 16
 #define SSCAN_MAX_DCONV 4
 /* Longest sequence sscan_fwd* and sscan_bwd* accept (2^30 steps): the kernels count
@@ -355,6 +357,155 @@ sscan_status sscan_bwd_checkpointed(int64_t batch, int64_t seqlen, int64_t dim, 
                                     void* dx, void* ddelta, float* dA, void* dB, void* dC, float* dD,
                                     void* dz, float* ddelta_bias, float* dinitial_state, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/*
+ * The gated linear recurrence: one state per channel whose decay is a gate of the
+ * token, in place of the selective scan's step size and fixed A.  For channel d:
+ *
+ *   rho_t  = sigmoid(r_t + r_bias[d])      iota_t = sigmoid(i_t + i_bias[d])
+ *   a_t    = exp(-decay_scale softplus(lam[d]) rho_t)
+ *   h_t    = a_t h_{t-1} + sqrt(1 - a_t^2) (iota_t x_t)
+ *   y_t    = h_t, or h_t silu(z_t) with a gate z
+ *
+ * r and i are the pre-activations of the two gates (projections of the token), lam a
+ * parameter per channel, decay_scale > 0 a constant of the model.  The square root
+ * keeps the state at the size of the input whatever the decay; 1 - a^2 is formed
+ * without cancellation for decays near 1.
+ *
+ * Shapes.  Dense: x, r, i, z, y are [batch, seqlen, dim], every batch row a sequence.
+ * Packed (offsets given): batch is 1, and request s holds the tokens offsets[s] ..
+ * offsets[s + 1] - 1 of the seqlen tokens.  offsets is a device array of num_seqs + 1
+ * int32, non-decreasing, starting at 0 and ending at most at seqlen; equal neighbours
+ * are an empty request, whose last state is its initial one.  Tokens at or past
+ * offsets[num_seqs] are padding: y is zero there, and so are their gradients,
+ * whatever the inputs hold.  No state passes from one request to the next, infinities
+ * and NaN included.  The host does not read offsets; an array that breaks these rules
+ * gives unspecified results, with no access outside the tensors.  "Sequences" below
+ * are the batch rows, or the num_seqs requests.
+ *
+ * strides: host array of 4 token strides of x, r, i, z in elements (each at least
+ * dim), so that the inputs can be columns of one projection's output: token t of
+ * batch row b is at (b seqlen + t) stride.  NULL: all dense.  y and dy are dense.
+ */
+
+/* Tokens between the saved states of sscan_glr_fwd's checkpoints. */
+#define SSCAN_GLR_BLOCK 64
+
+/*
+ * Activations in 8 bits.  Every channel's 16 consecutive tokens of a batch row (the
+ * last group of a row may be shorter) share one power of two 2^e, e = floor(log2 max|v|)
+ * held as e + 127 in a byte (the exponent field of the largest magnitude), and each
+ * value is held as the whole number nearest to v 2^(6 - e) (ties to even), at most 127
+ * in magnitude: the error is at most 2^(e - 7), except for magnitudes within
+ * 2^(e - 7) of 2^(e + 1), where it is below 2^(e - 6).  Magnitudes below 2^-126 share
+ * e = -126.  A group with an infinity or NaN has the byte 255 and comes back as NaN.
+ *
+ * One packed tensor [batch, seqlen, dim] is sscan_act8_bytes bytes: the codes (int8)
+ * [batch][seqlen][dim], then, from the next multiple of 256 bytes, the exponent bytes
+ * [batch][ceil(seqlen / 16)][dim]; the total is a multiple of 256.
+ */
+#define SSCAN_ACT8_GROUP 16
+
+/* Bytes of one packed tensor (0 for an empty one, and for invalid sizes). */
+size_t sscan_act8_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+
+/*
+ * Pack x [batch, seqlen, dim] (dtype, token stride x_stride in elements, at least dim,
+ * 0 for dense) into `packed`, and back into a dense x.  The values that come back are
+ * rounded to dtype (bfloat16 holds every packed value exactly).  packed must be
+ * 256-byte aligned, of packed_bytes >= sscan_act8_bytes, and overlap no tensor.
+ */
+sscan_status sscan_act8_pack(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x,
+                             int64_t x_stride, void* packed, size_t packed_bytes, void* stream);
+sscan_status sscan_act8_unpack(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* packed,
+                               size_t packed_bytes, void* x, void* stream);
+
+/* Bytes of the state checkpoints (float32, [batch][ceil(seqlen / SSCAN_GLR_BLOCK)][dim]:
+ * the state entering each block of tokens) and of the activations saved in 8 bits
+ * (x, r, i and, if gated, z, each as one packed tensor of sscan_act8_bytes, in this order). */
+size_t sscan_glr_checkpoint_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+size_t sscan_glr_saved_bytes(int64_t batch, int64_t seqlen, int64_t dim, int gated);
+
+/* Workspace bytes of sscan_glr_fwd (0: none needed) and of sscan_glr_bwd. */
+size_t sscan_glr_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim);
+size_t sscan_glr_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim);
+
+/*
+ * Forward over whole sequences.
+ *
+ *   x, r, i, z     : as above (dtype); z NULL: no gate
+ *   lam, r_bias, i_bias : [dim] (float32); a NULL bias is zero
+ *   initial_state  : [sequences, dim] (float32), NULL: zero
+ *   y              : [batch, seqlen, dim] (dtype)
+ *   last_state     : [sequences, dim] (float32), NULL: not written; may be initial_state
+ *   checkpoints    : for a backward pass: sscan_glr_checkpoint_bytes, NULL: not written
+ *   saved          : for a backward pass from 8 bits: sscan_glr_saved_bytes, 256-byte
+ *                    aligned, NULL: not written
+ *   workspace      : sscan_glr_fwd_workspace_size, 256-byte aligned; scratch, nothing is
+ *                    kept in it between calls
+ * Results are bitwise reproducible.
+ */
+sscan_status sscan_glr_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x, const void* r,
+                           const void* i, const void* z, const int64_t* strides, const float* lam,
+                           const float* r_bias, const float* i_bias, float decay_scale,
+                           const float* initial_state, const int32_t* offsets, int64_t num_seqs, void* y,
+                           float* last_state, float* checkpoints, size_t checkpoint_bytes, void* saved,
+                           size_t saved_bytes, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward pass, given dy = dLoss/dy and optionally dlast_state = dLoss/d(last_state):
+ * with the reverse recurrence g_t = dy_t silu(z_t) + a_{t+1} g_{t+1} within a sequence,
+ *   dlog_a = g (a h_{t-1} - iota x a^2 / sqrt(1 - a^2))
+ *   dx = g sqrt(1 - a^2) iota             di = g sqrt(1 - a^2) x iota (1 - iota)
+ *   dr = -decay_scale softplus(lam) dlog_a rho (1 - rho)
+ *   dz = dy h silu'(z)                    dinitial_state = a g of the first token
+ *   dlam = -decay_scale sigmoid(lam) sum dlog_a rho     (bias gradients: sums of dr and di)
+ * Where a rounds to 1 the terms with 1 / sqrt(1 - a^2) take their limit for a vanishing
+ * decay rate, zero.
+ *
+ *   checkpoints    : what sscan_glr_fwd wrote for the same inputs (required)
+ *   x, r, i, z     : the forward's inputs, or all NULL with `saved`, what the forward
+ *                    wrote there; dz then says whether it was gated.  From `saved`,
+ *                    every gradient is the formula's at the values the 8 bits stand
+ *                    for, except that the states entering the blocks are the
+ *                    forward's own (those of the inputs as they were).
+ *   initial_state  : the forward's (read only with offsets; a dense forward's comes
+ *                    with the checkpoints), NULL: zero
+ *   dx, dr, di, dz : (dtype) token strides in grad_strides (host array of 4, NULL:
+ *                    dense); dz is required exactly when z is given
+ *   dlam, dr_bias, di_bias : [dim] (float32); the bias gradients may be NULL
+ *   dinitial_state : [sequences, dim] (float32), NULL: not written; an empty
+ *                    request's is its dlast_state
+ *   workspace      : sscan_glr_bwd_workspace_size, 256-byte aligned
+ * The remaining arguments as in sscan_glr_fwd.  Results are bitwise reproducible.
+ */
+sscan_status sscan_glr_bwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x, const void* r,
+                           const void* i, const void* z, const int64_t* strides, const void* saved,
+                           size_t saved_bytes, const float* lam, const float* r_bias, const float* i_bias,
+                           float decay_scale, const float* initial_state, const int32_t* offsets, int64_t num_seqs,
+                           const float* checkpoints, size_t checkpoint_bytes, const void* dy,
+                           const float* dlast_state, void* dx, void* dr, void* di, void* dz,
+                           const int64_t* grad_strides, float* dlam, float* dr_bias, float* di_bias,
+                           float* dinitial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for every row of a decode batch.
+ *
+ *   state          : [num_slots, dim] (float32), a pool of request states
+ *   slots          : device array [batch] of int32: row b continues state slots[b]; a row
+ *                    whose slot is outside [0, num_slots) holds no request: its y is zero
+ *                    and no state changes.  NULL: row b has slot b (batch <= num_slots).
+ *   slots_out      : device array [batch] of int32: where row b's new state goes (nowhere
+ *                    if outside [0, num_slots)); NULL: back to its own slot.  With other
+ *                    slots a state can be continued more than one way, or a drafted
+ *                    token taken back.  No two rows may write one slot, and no row may
+ *                    read a slot that another writes.
+ *   x, r, i, z     : [batch, dim] (dtype), strides as above; y [batch, dim] dense
+ */
+sscan_status sscan_glr_step(int64_t batch, int64_t dim, int dtype, float* state, int64_t num_slots,
+                            const int32_t* slots, const int32_t* slots_out, const void* x, const void* r,
+                            const void* i, const void* z, const int64_t* strides, const float* lam,
+                            const float* r_bias, const float* i_bias, float decay_scale, void* y, void* stream);
 
 #ifdef __cplusplus
 }

@@ -370,3 +370,272 @@ def sscan_bwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Te
                           _ptr(dlast_state), _ptr(dx), _ptr(ddelta), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD),
                           _ptr(dz), _ptr(dbias), _ptr(dh0), _ptr(workspace), wbytes, _stream(dev)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Gated linear recurrence, and activations in 8 bits
+# ---------------------------------------------------------------------------
+_F = ctypes.c_float
+_I = ctypes.c_int
+for _name, _args, _res in (
+        ("sscan_act8_bytes", [_I64] * 3, _SZ),
+        ("sscan_act8_pack", [_I64] * 3 + [_I, _P, _I64, _P, _SZ, _P], _I),
+        ("sscan_act8_unpack", [_I64] * 3 + [_I, _P, _SZ, _P, _P], _I),
+        ("sscan_glr_checkpoint_bytes", [_I64] * 3, _SZ),
+        ("sscan_glr_saved_bytes", [_I64] * 3 + [_I], _SZ),
+        ("sscan_glr_fwd_workspace_size", [_I64] * 3, _SZ),
+        ("sscan_glr_bwd_workspace_size", [_I64] * 3, _SZ),
+        ("sscan_glr_fwd", [_I64] * 3 + [_I] + [_P] * 8 + [_F, _P, _P, _I64] + [_P] * 3 + [_SZ, _P, _SZ, _P, _SZ, _P], _I),
+        ("sscan_glr_bwd", [_I64] * 3 + [_I] + [_P] * 6 + [_SZ] + [_P] * 3 + [_F, _P, _P, _I64, _P, _SZ] + [_P] * 12
+         + [_SZ, _P], _I),
+        ("sscan_glr_step", [_I64] * 2 + [_I, _P, _I64] + [_P] * 10 + [_F, _P, _P], _I)):
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _res
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Checks a token tensor whose rows may be columns of a wider one (last index dense,
+    tokens evenly spaced); returns its token stride in elements."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[-1]
+    st = t.stride()
+    step = st[-2]
+    even = t.dim() == 2 or shape[0] == 1 or st[0] == shape[1] * step
+    if t.dim() == 3 and shape[1] == 1:
+        step, even = st[0], True
+    if (st[-1] != 1 and shape[-1] != 1) or not even or step < shape[-1]:
+        raise ValueError(f"{name} must have a dense last dimension and evenly spaced tokens, got strides {st}")
+    return step
+
+
+def _strides(values, dim: int):
+    return None if all(v == dim for v in values) else (ctypes.c_int64 * 4)(*values)
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def act8_bytes(batch: int, seqlen: int, dim: int) -> int:
+    """Bytes of one activation tensor [batch, seqlen, dim] packed to 8 bits."""
+    return int(_lib.sscan_act8_bytes(batch, seqlen, dim))
+
+
+def sscan_act8_pack(x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [batch, seqlen, dim] (float32 or bfloat16, tokens evenly spaced) in 8 bits: every
+    channel's 16 consecutive tokens share a power of two.  Returns a byte tensor of
+    ``act8_bytes`` bytes (``out`` may supply it)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, dim]")
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    batch, seqlen, dim = x.shape
+    stride = _rows(x, "x", x.dtype, x.shape)
+    if out is None:
+        out = torch.empty(act8_bytes(batch, seqlen, dim), dtype=torch.uint8, device=x.device)
+    _dev(out, "out")
+    _check(_lib.sscan_act8_pack(batch, seqlen, dim, _DTYPES[x.dtype], _ptr(x), stride, _ptr(out), _nbytes(out),
+                                _stream(x.device)))
+    return out
+
+
+def sscan_act8_unpack(packed: torch.Tensor, shape, dtype=torch.bfloat16, out: Optional[torch.Tensor] = None
+                      ) -> torch.Tensor:
+    """The values of a tensor that ``sscan_act8_pack`` packed, as ``dtype`` of the given
+    shape [batch, seqlen, dim] (``out`` may supply the tensor)."""
+    if len(shape) != 3:
+        raise ValueError("shape must be [batch, seqlen, dim]")
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    _dev(packed, "packed")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=packed.device)
+    _dev(out, "out", dtype, shape)
+    _check(_lib.sscan_act8_unpack(shape[0], shape[1], shape[2], _DTYPES[dtype], _ptr(packed), _nbytes(packed), _ptr(out),
+                                  _stream(packed.device)))
+    return out
+
+
+def glr_checkpoint_bytes(batch: int, seqlen: int, dim: int) -> int:
+    """Bytes of the states ``sscan_glr_fwd`` keeps for the backward pass (one every 64
+    tokens, [batch, ceil(seqlen / 64), dim] float32)."""
+    return int(_lib.sscan_glr_checkpoint_bytes(batch, seqlen, dim))
+
+
+def glr_saved_bytes(batch: int, seqlen: int, dim: int, gated: bool = False) -> int:
+    """Bytes of the activations (x, r, i and, if gated, z) saved in 8 bits."""
+    return int(_lib.sscan_glr_saved_bytes(batch, seqlen, dim, int(gated)))
+
+
+def glr_workspace_size(batch: int, seqlen: int, dim: int, backward: bool = False) -> int:
+    fn = _lib.sscan_glr_bwd_workspace_size if backward else _lib.sscan_glr_fwd_workspace_size
+    return int(fn(batch, seqlen, dim))
+
+
+def _glr_params(dim, device, lam, r_bias, i_bias, offsets, batch):
+    """Checks the per-channel parameters and offsets; returns the number of sequences."""
+    _dev(lam, "lam", torch.float32, (dim,))
+    if r_bias is not None:
+        _dev(r_bias, "r_bias", torch.float32, (dim,))
+    if i_bias is not None:
+        _dev(i_bias, "i_bias", torch.float32, (dim,))
+    if offsets is None:
+        return batch
+    _dev(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be [sequences + 1]")
+    return offsets.numel() - 1
+
+
+def _glr_workspace(workspace, need, device):
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def sscan_glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor,
+                  r_bias: Optional[torch.Tensor] = None, i_bias: Optional[torch.Tensor] = None,
+                  z: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                  offsets: Optional[torch.Tensor] = None, decay_scale: float = 8.0, return_last_state: bool = False,
+                  out: Optional[torch.Tensor] = None, last_state: Optional[torch.Tensor] = None,
+                  checkpoints: Optional[torch.Tensor] = None, saved: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) (sigmoid(i_t + i_bias) x_t),
+    a_t = exp(-decay_scale softplus(lam) sigmoid(r_t + r_bias)); y = h, or h silu(z).
+
+    x, r, i, z: [batch, seqlen, dim] (all float32 or all bfloat16), each dense or columns of a
+    wider tensor; lam, r_bias, i_bias: [dim] float32.  offsets [sequences + 1] (int32, on the
+    GPU): batch is 1 and its tokens are packed requests, the rest padding.  initial_state,
+    last_state: [batch or sequences, dim] float32.  checkpoints (``glr_checkpoint_bytes``
+    bytes) and saved (``glr_saved_bytes`` bytes) are filled for ``sscan_glr_bwd``, the latter
+    with the activations in 8 bits.  Returns y, or (y, last_state)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, dim]")
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    batch, seqlen, dim = shape = x.shape
+    dev = x.device
+    strides = [_rows(x, "x", x.dtype, shape), _rows(r, "r", x.dtype, shape), _rows(i, "i", x.dtype, shape),
+               dim if z is None else _rows(z, "z", x.dtype, shape)]
+    nseq = _glr_params(dim, dev, lam, r_bias, i_bias, offsets, batch)
+    if initial_state is not None:
+        _dev(initial_state, "initial_state", torch.float32, (nseq, dim))
+    y = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else _dev(out, "out", x.dtype, shape)
+    if last_state is None and return_last_state:
+        last_state = torch.empty((nseq, dim), dtype=torch.float32, device=dev)
+    elif last_state is not None:
+        _dev(last_state, "last_state", torch.float32, (nseq, dim))
+    if checkpoints is not None:
+        _dev(checkpoints, "checkpoints")
+    if saved is not None:
+        _dev(saved, "saved")
+    workspace = _glr_workspace(workspace, _lib.sscan_glr_fwd_workspace_size(batch, seqlen, dim), dev)
+    _check(_lib.sscan_glr_fwd(batch, seqlen, dim, _DTYPES[x.dtype], _ptr(x), _ptr(r), _ptr(i), _ptr(z),
+                              _strides(strides, dim), _ptr(lam), _ptr(r_bias), _ptr(i_bias), decay_scale,
+                              _ptr(initial_state), _ptr(offsets), nseq, _ptr(y), _ptr(last_state), _ptr(checkpoints),
+                              _nbytes(checkpoints), _ptr(saved), _nbytes(saved), _ptr(workspace), _nbytes(workspace),
+                              _stream(dev)))
+    return (y, last_state) if return_last_state else y
+
+
+def sscan_glr_bwd(lam: torch.Tensor, dy: torch.Tensor, checkpoints: torch.Tensor,
+                  x: Optional[torch.Tensor] = None, r: Optional[torch.Tensor] = None,
+                  i: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                  saved: Optional[torch.Tensor] = None, gated: bool = False,
+                  r_bias: Optional[torch.Tensor] = None, i_bias: Optional[torch.Tensor] = None,
+                  initial_state: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                  decay_scale: float = 8.0, dlast_state: Optional[torch.Tensor] = None, want_dbias: bool = True,
+                  want_dinitial_state: bool = True, out: Optional[dict] = None,
+                  workspace: Optional[torch.Tensor] = None) -> dict:
+    """Backward pass of ``sscan_glr_fwd``, given dy and what the forward left in
+    ``checkpoints``, with either its inputs x, r, i (and z) or the activations it ``saved`` in
+    8 bits (``gated`` says whether z is among them).  initial_state is read with offsets only.
+    Returns a dict with dx, dr, di, dlam and, as applicable, dz, dr_bias, di_bias,
+    dinitial_state; ``out`` may supply tensors by name, the token gradients also as columns of
+    a wider tensor."""
+    if dy.dim() != 3:
+        raise ValueError("dy must be [batch, seqlen, dim]")
+    if dy.dtype not in _DTYPES:
+        raise ValueError("dy must be float32 or bfloat16")
+    batch, seqlen, dim = shape = dy.shape
+    dtype, dev = dy.dtype, dy.device
+    _dev(dy, "dy")
+    if saved is not None:
+        if x is not None or r is not None or i is not None or z is not None:
+            raise ValueError("give either saved or x, r, i and z")
+        _dev(saved, "saved")
+        strides = [dim] * 4
+    else:
+        if x is None or r is None or i is None:
+            raise ValueError("x, r and i are required without saved")
+        gated = z is not None
+        strides = [_rows(x, "x", dtype, shape), _rows(r, "r", dtype, shape), _rows(i, "i", dtype, shape),
+                   dim if z is None else _rows(z, "z", dtype, shape)]
+    nseq = _glr_params(dim, dev, lam, r_bias, i_bias, offsets, batch)
+    for t, name in ((initial_state, "initial_state"), (dlast_state, "dlast_state")):
+        if t is not None:
+            _dev(t, name, torch.float32, (nseq, dim))
+    _dev(checkpoints, "checkpoints")
+    out = dict(out or {})
+    grad_strides = []
+    for name in ("dx", "dr", "di", "dz"):
+        if name == "dz" and not gated:
+            grad_strides.append(dim)
+            continue
+        t = out.get(name)
+        if t is None:
+            out[name] = torch.empty(shape, dtype=dtype, device=dev)
+            grad_strides.append(dim)
+        else:
+            grad_strides.append(_rows(t, name, dtype, shape))
+    for name, want, size in (("dlam", True, (dim,)), ("dr_bias", want_dbias, (dim,)), ("di_bias", want_dbias, (dim,)),
+                             ("dinitial_state", want_dinitial_state, (nseq, dim))):
+        if name in out:
+            _dev(out[name], name, torch.float32, size)
+        elif want:
+            out[name] = torch.empty(size, dtype=torch.float32, device=dev)
+    workspace = _glr_workspace(workspace, _lib.sscan_glr_bwd_workspace_size(batch, seqlen, dim), dev)
+    _check(_lib.sscan_glr_bwd(batch, seqlen, dim, _DTYPES[dtype], _ptr(x), _ptr(r), _ptr(i), _ptr(z),
+                              _strides(strides, dim), _ptr(saved), _nbytes(saved), _ptr(lam), _ptr(r_bias),
+                              _ptr(i_bias), decay_scale, _ptr(initial_state), _ptr(offsets), nseq, _ptr(checkpoints),
+                              _nbytes(checkpoints), _ptr(dy), _ptr(dlast_state), _ptr(out["dx"]), _ptr(out["dr"]),
+                              _ptr(out["di"]), _ptr(out.get("dz")), _strides(grad_strides, dim), _ptr(out["dlam"]),
+                              _ptr(out.get("dr_bias")), _ptr(out.get("di_bias")), _ptr(out.get("dinitial_state")),
+                              _ptr(workspace), _nbytes(workspace), _stream(dev)))
+    return out
+
+
+def sscan_glr_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor,
+                   r_bias: Optional[torch.Tensor] = None, i_bias: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                   slots_out: Optional[torch.Tensor] = None, decay_scale: float = 8.0,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the gated linear recurrence for every row of a batch.  state: [slots, dim]
+    float32, a pool updated in place; x, r, i, z: [batch, dim]; slots [batch] (int32): row b
+    continues state slots[b] (none and y = 0 if negative), default slot b; slots_out [batch]
+    (int32): where its new state goes, default its own slot.  Returns y [batch, dim]."""
+    if x.dim() != 2:
+        raise ValueError("x must be [batch, dim]")
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    batch, dim = shape = x.shape
+    strides = [_rows(x, "x", x.dtype, shape), _rows(r, "r", x.dtype, shape), _rows(i, "i", x.dtype, shape),
+               dim if z is None else _rows(z, "z", x.dtype, shape)]
+    _glr_params(dim, x.device, lam, r_bias, i_bias, None, batch)
+    if state.dim() != 2:
+        raise ValueError("state must be [slots, dim]")
+    _dev(state, "state", torch.float32, (state.shape[0], dim))
+    for t, name in ((slots, "slots"), (slots_out, "slots_out")):
+        if t is not None:
+            _dev(t, name, torch.int32, (batch,))
+    y = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else _dev(out, "out", x.dtype, shape)
+    _check(_lib.sscan_glr_step(batch, dim, _DTYPES[x.dtype], _ptr(state), state.shape[0], _ptr(slots), _ptr(slots_out),
+                               _ptr(x), _ptr(r), _ptr(i), _ptr(z), _strides(strides, dim), _ptr(lam), _ptr(r_bias),
+                               _ptr(i_bias), decay_scale, _ptr(y), _stream(x.device)))
+    return y

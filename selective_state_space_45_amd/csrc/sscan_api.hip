@@ -5,34 +5,46 @@
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "selscan.h"
+#include "sscan_host.h"
 #include "sscan_internal.h"
 
 namespace {
+thread_local char g_last_error[512] = "";
+}  // namespace
 
-thread_local std::string g_last_error;
+namespace sscan {
 
 int fail(int code, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return code;
 }
 
 int ok() {
-  g_last_error.clear();
+  g_last_error[0] = '\0';
   return SSCAN_OK;
 }
 
 int hip_fail(hipError_t e, const char* what) {
   return fail(SSCAN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace sscan
+
+namespace {
+
+using sscan::Buf;
+using sscan::aligned;
+using sscan::fail;
+using sscan::hip_fail;
+using sscan::ok;
+using sscan::overlaps;
+using sscan::round256;
 
 // Compute units of the current device (cached per device); 256 if the query fails.
 int device_cus() {
@@ -165,20 +177,6 @@ SegPlan plan_segments(int64_t batch, int64_t seqlen, int64_t dim, int64_t N, int
   pl.nseg = static_cast<int>((seqlen + len - 1) / len);
   return pl;
 }
-
-bool overlaps(const void* a, size_t abytes, const void* b, size_t bbytes) {
-  if (!a || !b || abytes == 0 || bbytes == 0) return false;
-  const char* pa = static_cast<const char*>(a);
-  const char* pb = static_cast<const char*>(b);
-  return pa < pb + bbytes && pb < pa + abytes;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Buf {
-  const void* p;
-  size_t n;
-};
 
 int check_common(int64_t batch, int64_t dim, int64_t dstate, int dtype, unsigned flags) {
   if (dtype != SSCAN_F32 && dtype != SSCAN_BF16) return fail(SSCAN_ERR_UNSUPPORTED, "unknown dtype %d", dtype);
@@ -393,8 +391,6 @@ int fwd_impl(int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int dty
 // ---------------------------------------------------------------------------
 // Backward pass: workspace layout and host checks.
 // ---------------------------------------------------------------------------
-size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
-
 struct BwdLayout {
   size_t ckpt, gB, gC, gA, gD, gb, seg, rg, rs, gin, total;
   size_t total_saved;      // bytes needed when the checkpoints come from the caller
@@ -691,7 +687,7 @@ extern "C" {
 
 int sscan_version(void) { return SSCAN_VERSION; }
 
-const char* sscan_last_error(void) { return g_last_error.c_str(); }
+const char* sscan_last_error(void) { return g_last_error; }
 
 size_t sscan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int dtype) {
   (void)dtype;

@@ -1,0 +1,173 @@
+// The gated linear recurrence and 8-bit activations: parameters and device arithmetic
+// shared by their kernels.  The operations are defined in include/selscan.h.
+#pragma once
+
+#include "sscan_device.h"
+
+namespace sscan {
+
+constexpr int kGlrBlock = 64;   // tokens between saved states (SSCAN_GLR_BLOCK)
+constexpr int kActGroup = 16;   // tokens that share a power of two (SSCAN_ACT8_GROUP)
+
+struct GlrFwdParams {
+  const void* x;
+  const void* r;
+  const void* i;
+  const void* z;            // nullable
+  int64_t sx, sr, si, sz;   // token strides in elements
+  const float* lam;
+  const float* r_bias;      // nullable
+  const float* i_bias;      // nullable
+  float decay_scale;
+  const float* h0;          // nullable: [sequences][dim]
+  const int32_t* offsets;   // nullable: [num_seqs + 1]
+  void* y;
+  float* h_last;            // nullable
+  float* ckpt;              // nullable: [batch][ceil(L / kGlrBlock)][dim]
+  int8_t* codes;            // nullable: saved activations, one packed tensor after another
+  size_t saved_stride;      // bytes from one packed tensor to the next
+  size_t exps_at;           // bytes from a packed tensor's codes to its exponents
+  int64_t batch, L, dim, num_seqs;
+};
+
+struct GlrBwdParams {
+  const void* x;            // x, r, i, z null when the activations come from `codes`
+  const void* r;
+  const void* i;
+  const void* z;
+  int64_t sx, sr, si, sz;
+  const int8_t* codes;      // nullable
+  size_t saved_stride, exps_at;
+  const float* lam;
+  const float* r_bias;
+  const float* i_bias;
+  float decay_scale;
+  const float* h0;          // nullable, read with offsets only
+  const int32_t* offsets;   // nullable
+  const float* ckpt;
+  const void* dy;
+  const float* dlast;       // nullable
+  void* dx;
+  void* dr;
+  void* di;
+  void* dz;                 // nullable
+  int64_t gx, gr, gi, gz;   // token strides of the gradients
+  float* dlam;
+  float* dr_bias;           // nullable
+  float* di_bias;           // nullable
+  float* dh0;               // nullable
+  void* workspace;
+  int64_t batch, L, dim, num_seqs;
+};
+
+struct GlrStepParams {
+  float* state;
+  int64_t num_slots;
+  const int32_t* slots;     // nullable
+  const int32_t* slots_out; // nullable
+  const void* x;
+  const void* r;
+  const void* i;
+  const void* z;            // nullable
+  int64_t sx, sr, si, sz;
+  const float* lam;
+  const float* r_bias;
+  const float* i_bias;
+  float decay_scale;
+  void* y;
+  int64_t batch, dim;
+};
+
+hipError_t launch_glr_fwd(const GlrFwdParams& p, bool bf16, hipStream_t s);
+hipError_t launch_glr_bwd(const GlrBwdParams& p, bool bf16, hipStream_t s);
+hipError_t launch_glr_step(const GlrStepParams& p, bool bf16, hipStream_t s);
+hipError_t launch_act8_pack(const void* x, int64_t stride, void* packed, int64_t batch, int64_t L, int64_t dim,
+                            bool bf16, hipStream_t s);
+hipError_t launch_act8_unpack(const void* packed, void* x, int64_t batch, int64_t L, int64_t dim, bool bf16,
+                              hipStream_t s);
+size_t glr_bwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim);
+
+// Sizes of one packed tensor: codes, padded to 256 bytes, then exponents.
+inline size_t act8_exps_at(int64_t batch, int64_t L, int64_t dim) {
+  return (static_cast<size_t>(batch) * L * dim + 255) & ~size_t(255);
+}
+inline size_t act8_total(int64_t batch, int64_t L, int64_t dim) {
+  const size_t exps = static_cast<size_t>(batch) * ((L + kActGroup - 1) / kActGroup) * dim;
+  return act8_exps_at(batch, L, dim) + ((exps + 255) & ~size_t(255));
+}
+
+// sigmoid(v) = 1 / (1 + e^-v).  e^-v overflows to infinity for v below -88, whose
+// reciprocal is the right 0.
+__device__ __forceinline__ float sigmoid(float v) { return hw_rcp(1.f + hw_exp2(-v * kLog2e)); }
+
+// sigmoid(v) and its derivative sigmoid (1 - sigmoid), the latter without the
+// cancellation of 1 - sigmoid: with w = e^-|v| and q = 1 / (1 + w), sigmoid is q or
+// w q by the sign of v, and the derivative is w q^2.
+__device__ __forceinline__ float sigmoid_d(float v, float& deriv) {
+  const float w = hw_exp2(-fabsf(v) * kLog2e);
+  const float q = hw_rcp(1.f + w);
+  deriv = w * q * q;
+  return v >= 0.f ? q : (v < 0.f ? w * q : v);   // NaN stays NaN
+}
+
+// softplus(v) = max(v, 0) + log(1 + w), w = e^-|v|, to float32 accuracy at every v:
+// log(1 + w) = 2 atanh(s), s = w / (2 + w) <= 1/3, by its odd series through s^15
+// (the next term is below 2e-9 of the sum).
+__device__ __forceinline__ float softplus_acc(float v) {
+  const float w = hw_exp2(-fabsf(v) * kLog2e);
+  const float s = w * hw_rcp(2.f + w);
+  const float s2 = s * s;
+  float p = fmaf(s2, 1.f / 15.f, 1.f / 13.f);
+  p = fmaf(s2, p, 1.f / 11.f);
+  p = fmaf(s2, p, 1.f / 9.f);
+  p = fmaf(s2, p, 1.f / 7.f);
+  p = fmaf(s2, p, 1.f / 5.f);
+  p = fmaf(s2, p, 1.f / 3.f);
+  p = fmaf(s2, p, 1.f);
+  return (v > 0.f ? v : (v <= 0.f ? 0.f : v)) + 2.f * s * p;
+}
+
+// a = e^-q and v = 1 - a^2 for q = decay rate x gate >= 0.  1 - a^2 loses its leading
+// digits for a near 1, so for q < 1/2 it is 2 a sinh(q) with sinh by its series through
+// q^7 (the next term is below 1.1e-8 of it there); elsewhere a^2 <= e^-1 and the
+// difference is exact enough.
+__device__ __forceinline__ float decay_of(float q, float& one_minus_a2) {
+  const float a = hw_exp2(-q * kLog2e);
+  const float q2 = q * q;
+  float p = fmaf(q2, 1.f / 5040.f, 1.f / 120.f);
+  p = fmaf(q2, p, 1.f / 6.f);
+  p = fmaf(q2, p, 1.f);
+  const float near1 = (2.f * a) * (q * p);
+  const float far = fmaf(-a, a, 1.f);
+  one_minus_a2 = q < 0.5f ? near1 : far;
+  return a;
+}
+
+__device__ __forceinline__ float hw_sqrt(float v) { return __builtin_amdgcn_sqrtf(v); }
+
+// 1 / sqrt(v), and 0 below the smallest normal number, where the hardware's reciprocal
+// root is infinite: 1 - a^2 is that small only for decay rates below 1e-37, whose terms
+// with 1 / sqrt(1 - a^2), each times the rate, are below 1e-18 of the others.
+__device__ __forceinline__ float rsq_or_0(float v) { return v < 1.17549435e-38f ? 0.f : __builtin_amdgcn_rsqf(v); }
+
+// 8-bit codes.  `field` is the float32 exponent field (0 .. 255) of the group's largest
+// magnitude; 255 marks a group with an infinity or NaN.  Scaling by powers of two is
+// exact (ldexp reaches every exponent a field asks for), so the only rounding is to the
+// whole number.
+__device__ __forceinline__ uint32_t act8_field(float top) { return (__float_as_uint(top) >> 23) & 255u; }
+__device__ __forceinline__ int act8_shift(uint32_t field) { return (field < 1u ? 1 : static_cast<int>(field)) - 133; }
+__device__ __forceinline__ int act8_code(float v, int shift) {
+  const float c = rintf(__builtin_amdgcn_ldexpf(v, -shift));
+  return static_cast<int>(fminf(fmaxf(c, -127.f), 127.f));
+}
+__device__ __forceinline__ float act8_value(int code, uint32_t field) {
+  const float v = __builtin_amdgcn_ldexpf(static_cast<float>(code), act8_shift(field));
+  return field == 255u ? __uint_as_float(0x7fc00000u) : v;
+}
+// max |v| that keeps NaN: a NaN's magnitude bits are above infinity's.
+__device__ __forceinline__ uint32_t act8_top(uint32_t top, float v) {
+  const uint32_t m = __float_as_uint(v) & 0x7fffffffu;
+  return m > top ? m : top;
+}
+
+}  // namespace sscan
