@@ -13,7 +13,8 @@ SOURCES = ["csrc/sscan_api.hip", "csrc/sscan_fwd.hip", "csrc/sscan_fwd_zoh.hip",
            "csrc/sscan_fwd_row_struct.hip", "csrc/sscan_fwd_row_ckagg.hip",
            "csrc/sscan_fwd_conv.hip",
            "csrc/sscan_step.hip", "csrc/sscan_bwd.hip",
-           "csrc/sscan_glr_api.hip", "csrc/sscan_glr_fwd.hip", "csrc/sscan_glr_bwd.hip", "csrc/sscan_glr_step.hip"]
+           "csrc/sscan_glr_api.hip", "csrc/sscan_glr_fwd.hip", "csrc/sscan_glr_bwd.hip", "csrc/sscan_glr_step.hip",
+           "csrc/sscan_act8.hip"]
 
 # Packed-FP32 instructions are disabled on purpose: the VALU code is written for
 # plain fp32 issue.

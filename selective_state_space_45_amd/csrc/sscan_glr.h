@@ -27,6 +27,7 @@ struct GlrFwdParams {
   int8_t* codes;            // nullable: saved activations, one packed tensor after another
   size_t saved_stride;      // bytes from one packed tensor to the next
   size_t exps_at;           // bytes from a packed tensor's codes to its exponents
+  void* workspace;
   int64_t batch, L, dim, num_seqs;
 };
 
@@ -85,6 +86,7 @@ hipError_t launch_act8_pack(const void* x, int64_t stride, void* packed, int64_t
                             bool bf16, hipStream_t s);
 hipError_t launch_act8_unpack(const void* packed, void* x, int64_t batch, int64_t L, int64_t dim, bool bf16,
                               hipStream_t s);
+size_t glr_fwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim);
 size_t glr_bwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim);
 
 // Sizes of one packed tensor: codes, padded to 256 bytes, then exponents.
@@ -154,7 +156,6 @@ __device__ __forceinline__ float rsq_or_0(float v) { return v < 1.17549435e-38f 
 // magnitude; 255 marks a group with an infinity or NaN.  Scaling by powers of two is
 // exact (ldexp reaches every exponent a field asks for), so the only rounding is to the
 // whole number.
-__device__ __forceinline__ uint32_t act8_field(float top) { return (__float_as_uint(top) >> 23) & 255u; }
 __device__ __forceinline__ int act8_shift(uint32_t field) { return (field < 1u ? 1 : static_cast<int>(field)) - 133; }
 __device__ __forceinline__ int act8_code(float v, int shift) {
   const float c = rintf(__builtin_amdgcn_ldexpf(v, -shift));

@@ -44,6 +44,14 @@ int check_sizes(int64_t batch, int64_t seqlen, int64_t dim, int dtype) {
   return SSCAN_OK;
 }
 
+// The recurrence's launches count their tiles (64 tokens, at least 64 channels) in 31 bits.
+int check_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
+  const int64_t blocks = (seqlen + SSCAN_GLR_BLOCK - 1) / SSCAN_GLR_BLOCK, sets = (dim + 63) / 64;
+  if (batch > 0 && blocks > 0 && sets > 0 && (blocks > INT32_MAX / sets || batch > INT32_MAX / (blocks * sets)))
+    return fail(SSCAN_ERR_INVALID_ARG, "batch*seqlen*dim too large");
+  return SSCAN_OK;
+}
+
 // A token tensor: rows of dim elements, `stride` elements apart.
 struct Tok {
   const char* name;
@@ -124,6 +132,7 @@ int glr_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x
             float* last_state, float* checkpoints, size_t checkpoint_bytes, void* saved, size_t saved_bytes,
             void* workspace, size_t workspace_bytes, void* stream) {
   SSCAN_TRY(check_sizes(batch, seqlen, dim, dtype));
+  SSCAN_TRY(check_tiles(batch, seqlen, dim));
   SSCAN_TRY(check_offsets(batch, offsets, num_seqs));
   SSCAN_TRY(check_scale(decay_scale));
   if (batch == 0 || dim == 0) return ok();
@@ -172,6 +181,7 @@ int glr_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x
   p.codes = static_cast<int8_t*>(saved);
   p.saved_stride = sscan::act8_total(batch, seqlen, dim);
   p.exps_at = sscan::act8_exps_at(batch, seqlen, dim);
+  p.workspace = workspace;
   p.batch = batch; p.L = seqlen; p.dim = dim; p.num_seqs = num_seqs;
   const hipError_t e = sscan::launch_glr_fwd(p, dtype == SSCAN_BF16, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "gated recurrence launch");
@@ -185,6 +195,7 @@ int glr_bwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x
             const int64_t* grad_strides, float* dlam, float* dr_bias, float* di_bias, float* dinitial_state,
             void* workspace, size_t workspace_bytes, void* stream) {
   SSCAN_TRY(check_sizes(batch, seqlen, dim, dtype));
+  SSCAN_TRY(check_tiles(batch, seqlen, dim));
   SSCAN_TRY(check_offsets(batch, offsets, num_seqs));
   SSCAN_TRY(check_scale(decay_scale));
   if (dim == 0) return ok();
@@ -360,8 +371,7 @@ size_t sscan_glr_saved_bytes(int64_t batch, int64_t seqlen, int64_t dim, int gat
 }
 
 size_t sscan_glr_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim) {
-  (void)batch, (void)seqlen, (void)dim;
-  return 0;
+  return valid_sizes(batch, seqlen, dim) ? sscan::glr_fwd_workspace_bytes(batch, seqlen, dim) : 0;
 }
 
 size_t sscan_glr_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim) {

@@ -1,142 +1,314 @@
-// Gated linear recurrence, forward: one lane per (sequence, channel), token after token.
-#include "sscan_glr.h"
+// Gated linear recurrence, forward.
+#include "sscan_glr_tile.h"
 
 namespace sscan {
 
-template <typename Tin>
-__global__ __launch_bounds__(256) void glr_fwd_kernel(GlrFwdParams p) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t nseq = p.offsets ? p.num_seqs : p.batch;
-  if (id >= nseq * p.dim) return;
-  const int64_t s = id / p.dim, d = id - s * p.dim;
-  int64_t lo = s * p.L, hi = lo + p.L, row0 = lo;
-  if (p.offsets) {
-    lo = p.offsets[s], hi = p.offsets[s + 1], row0 = 0;
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > p.L ? p.L : hi;
+// Exponent field and codes of a wave's 16 tokens of one tensor, for V channels of a lane.
+// FULL: 16 tokens; otherwise the first `valid` of `rows` count, the others as zeros.
+template <typename Tin, int V, bool FULL>
+__device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg* raw, int valid, int rows, int8_t* codes,
+                                         uint8_t* exps, int64_t dim, uint32_t c, bool mine) {
+  int shift[V];
+  uint32_t fields = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < kActGroup; ++k)
+      if (FULL || k < valid) top = act8_top(top, TokVec<Tin, V>::get(raw[k], v));
+    shift[v] = act8_shift(top >> 23);
+    fields |= (top >> 23) << (8 * v);
   }
-  const float kappa = p.decay_scale * softplus_acc(p.lam[d]);
-  const float rb = p.r_bias ? p.r_bias[d] : 0.f, ib = p.i_bias ? p.i_bias[d] : 0.f;
-  const Tin* x = static_cast<const Tin*>(p.x);
-  const Tin* r = static_cast<const Tin*>(p.r);
-  const Tin* in = static_cast<const Tin*>(p.i);
-  const Tin* z = static_cast<const Tin*>(p.z);
-  Tin* y = static_cast<Tin*>(p.y);
-  const int64_t nblk = (p.L + kGlrBlock - 1) / kGlrBlock;
-  float h = p.h0 ? p.h0[id] : 0.f;
-  for (int64_t t = lo; t < hi; ++t) {
-    if (p.ckpt && (t - row0) % kGlrBlock == 0) p.ckpt[((p.offsets ? 0 : s) * nblk + (t - row0) / kGlrBlock) * p.dim + d] = h;
-    const float rho = sigmoid(to_f32(r[t * p.sr + d]) + rb);
-    const float iota = sigmoid(to_f32(in[t * p.si + d]) + ib);
-    float v;
-    const float a = decay_of(kappa * rho, v);
-    h = fmaf(a, h, hw_sqrt(v) * (iota * to_f32(x[t * p.sx + d])));
-    store_val(&y[t * p.dim + d], z ? h * silu(to_f32(z[t * p.sz + d])) : h);
-  }
-  if (p.h_last) p.h_last[id] = h;
-}
-
-// Zeros at the padding of a packed batch, and 8-bit codes of the saved activations.
-template <typename Tin>
-__global__ __launch_bounds__(256) void glr_pad_kernel(Tin* y, const int32_t* offsets, int64_t num_seqs, int64_t L,
-                                                      int64_t dim) {
-  int64_t lo = offsets[num_seqs];
-  lo = lo < 0 ? 0 : lo;
-  for (int64_t e = lo * dim + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < L * dim; e += 256ll * gridDim.x)
-    store_val(&y[e], 0.f);
-}
-
-template <typename Tin>
-__global__ __launch_bounds__(256) void glr_save_kernel(const Tin* x, int64_t stride, int8_t* codes, uint8_t* exps,
-                                                       const int32_t* offsets, int64_t num_seqs, int64_t batch,
-                                                       int64_t L, int64_t dim) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t ngrp = (L + kActGroup - 1) / kActGroup;
-  if (id >= batch * ngrp * dim) return;
-  const int64_t d = id % dim, g = id / dim % ngrp, b = id / dim / ngrp;
-  int64_t used = L;
-  if (offsets) used = offsets[num_seqs] < L ? offsets[num_seqs] : L;
-  float v[kActGroup];
-  uint32_t top = 0;
+  if (!mine) return;
+  if (V == 2) *reinterpret_cast<uint16_t*>(exps + c) = static_cast<uint16_t>(fields);
+  else exps[c] = static_cast<uint8_t>(fields);
+#pragma unroll
   for (int k = 0; k < kActGroup; ++k) {
-    const int64_t t = g * kActGroup + k;
-    v[k] = t < used ? to_f32(x[(b * L + t) * stride + d]) : 0.f;
-    top = act8_top(top, v[k]);
+    if (!FULL && k >= rows) break;
+    uint32_t both = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int q = FULL || k < valid ? act8_code(TokVec<Tin, V>::get(raw[k], v), shift[v]) : 0;
+      both |= (static_cast<uint32_t>(q) & 255u) << (8 * v);
+    }
+    int8_t* at = codes + k * dim;
+    if (V == 2) *reinterpret_cast<uint16_t*>(at + c) = static_cast<uint16_t>(both);
+    else at[c] = static_cast<int8_t>(both);
   }
-  const uint32_t field = top >> 23;
-  exps[id] = static_cast<uint8_t>(field);
-  for (int k = 0; k < kActGroup; ++k)
-    if (g * kActGroup + k < L) codes[(b * L + g * kActGroup + k) * dim + d] = static_cast<int8_t>(act8_code(v[k], act8_shift(field)));
+}
+
+template <typename Tin, int V, bool PACKED, bool GATE, bool SAVE>
+__global__ __launch_bounds__(64 * kGlrWaves) void glr_fwd_kernel(GlrFwdParams p, GlrChainWords words, int ntiles,
+                                                                 int nct) {
+  typedef TokVec<Tin, V> Tok;
+  constexpr int K = kActGroup, W = kGlrWaves;
+  __shared__ float sA[W][V][64], sB[W][V][64], sH[V][64];
+  __shared__ int sReset[W], sTile;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct;
+  const uint32_t chain = blockIdx.x % nchains;
+  int tile = 0;
+  if (ntiles > 1) {
+    if (threadIdx.x == 0) sTile = static_cast<int>(atomicAdd(&words.tickets[chain], 1u));
+    __syncthreads();
+    tile = __builtin_amdgcn_readfirstlane(sTile);
+  }
+  const int64_t b = chain / nct;
+  const int64_t c0 = static_cast<int64_t>(chain % nct) * (64 * V);
+  const int64_t D = p.dim, L = p.L;
+  // lanes past the last channel work on the last ones and store nothing
+  const int64_t cl = c0 + lane * V;
+  const bool mine = cl < D;
+  const uint32_t c = static_cast<uint32_t>(mine ? cl : D - V);
+  const int64_t t0 = static_cast<int64_t>(tile) * kGlrTile + w * K;
+  const int rows = static_cast<int>(L - t0 < 0 ? 0 : (L - t0 < K ? L - t0 : K));
+
+  // loads: 16 tokens of each input; tokens past the row's end read the last one
+  typename Tok::reg rx[K], rr[K], ri[K], rz[GATE ? K : 1];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t t = b * L + (t0 + k < L ? t0 + k : L - 1);
+    rx[k] = Tok::load(static_cast<const Tin*>(p.x) + t * p.sx + c);
+    rr[k] = Tok::load(static_cast<const Tin*>(p.r) + t * p.sr + c);
+    ri[k] = Tok::load(static_cast<const Tin*>(p.i) + t * p.si + c);
+    if (GATE) rz[k] = Tok::load(static_cast<const Tin*>(p.z) + t * p.sz + c);
+  }
+  GlrSpan sp;
+  sp.valid = rows;
+  if (PACKED) sp = glr_span(p.offsets, static_cast<int>(p.num_seqs), t0, L);
+
+  float rate[V], rb[V], ib[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    rate[v] = p.decay_scale * softplus_acc(p.lam[c + v]);
+    rb[v] = p.r_bias ? p.r_bias[c + v] : 0.f;
+    ib[v] = p.i_bias ? p.i_bias[c + v] : 0.f;
+  }
+  if (SAVE && rows > 0) {
+    const int64_t row0 = b * L + t0, group = b * ((L + K - 1) / K) + t0 / K;
+    auto save = [&](int q, const typename Tok::reg* raw) __attribute__((always_inline)) {
+      int8_t* codes = p.codes + q * p.saved_stride;
+      uint8_t* exps = reinterpret_cast<uint8_t*>(codes) + p.exps_at;
+      if (sp.valid == K) glr_save<Tin, V, true>(raw, K, K, codes + row0 * D, exps + group * D, D, c, mine);
+      else glr_save<Tin, V, false>(raw, sp.valid, rows, codes + row0 * D, exps + group * D, D, c, mine);
+    };
+    save(0, rx);
+    save(1, rr);
+    save(2, ri);
+    if (GATE) save(3, rz);
+  }
+
+  // each token's map h -> a h + u, and the wave's
+  float a[K][V], u[K][V], A[V], B[V];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float one;
+      a[k][v] = decay_of(rate[v] * sigmoid(Tok::get(rr[k], v) + rb[v]), one);
+      u[k][v] = hw_sqrt(one) * (sigmoid(Tok::get(ri[k], v) + ib[v]) * Tok::get(rx[k], v));
+    }
+  if (sp.valid < K) {   // tokens past the end leave the state alone
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k >= sp.valid)
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[k][v] = 1.f, u[k][v] = 0.f;
+  }
+  // a sequence's first token: its state depends on the sequence's initial one only.  The
+  // last states may overwrite the initial ones, so each is read once, here.
+  float first[V] = {};
+  if (PACKED && sp.starts && p.h0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (sp.starts >> k & 1) {
+        const float* from = p.h0 + static_cast<int64_t>(sp.seq_of(k)) * D + c;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float h = from[v];
+          u[k][v] = fmaf(a[k][v], h, u[k][v]);
+          if (k == 0) first[v] = h;
+        }
+      }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = a[0][v], B[v] = u[0][v];
+#pragma unroll
+    for (int k = 1; k < K; ++k) {
+      const bool start = PACKED && (sp.starts >> k & 1);
+      A[v] *= a[k][v];
+      B[v] = start ? u[k][v] : fmaf(a[k][v], B[v], u[k][v]);
+    }
+    sA[w][v][lane] = A[v];
+    sB[w][v][lane] = B[v];
+  }
+  if (PACKED && lane == 0) sReset[w] = sp.starts != 0;
+  __syncthreads();
+
+  // wave v < V joins the waves' maps of channel set v, publishes, and looks back
+  if (w < V) {
+    float TA = sA[0][w][lane], TB = sB[0][w][lane];
+    bool reset = PACKED && __builtin_amdgcn_readfirstlane(sReset[0]);
+#pragma unroll
+    for (int q = 1; q < W; ++q) {
+      const float qa = sA[q][w][lane], qb = sB[q][w][lane];
+      const bool qr = PACKED && __builtin_amdgcn_readfirstlane(sReset[q]);
+      TA *= qa;
+      TB = qr ? qb : fmaf(qa, TB, qb);
+      reset = reset || qr;
+    }
+    float h = 0.f;
+    if (tile == 0) {
+      if (!PACKED && p.h0) h = p.h0[b * D + c + w];
+    }
+    if (ntiles > 1) {
+      const GlrChain ch{words, static_cast<int64_t>(chain) * ntiles * (64 * V) + w * 64 + lane, 64 * V, tile};
+      if (tile + 1 < ntiles) {
+        if (reset) ch.publish_state(TB);
+        else if (tile == 0) ch.publish_state(fmaf(TA, h, TB));
+        else ch.publish_map(TA, TB);
+      }
+      if (tile > 0) {
+        h = ch.look_back();
+        if (tile + 1 < ntiles && !reset) ch.publish_state(fmaf(TA, h, TB));
+      }
+    }
+    sH[w][lane] = h;
+  }
+  __syncthreads();
+  if (rows == 0) return;
+
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = sH[v][lane];
+#pragma unroll
+  for (int q = 0; q < W - 1; ++q) {
+    if (q >= w) break;
+    const bool qr = PACKED && __builtin_amdgcn_readfirstlane(sReset[q]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = qr ? sB[q][v][lane] : fmaf(sA[q][v][lane], h[v], sB[q][v][lane]);
+  }
+  if (p.ckpt && w == 0 && mine) {
+    float* ck = p.ckpt + (b * ((L + kGlrBlock - 1) / kGlrBlock) + tile) * D + c;
+    const bool start = PACKED && (sp.starts & 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v) ck[v] = start ? first[v] : h[v];
+  }
+  Tin* yrow = static_cast<Tin*>(p.y) + (b * L + t0) * D;
+  auto out = [&](int k) __attribute__((always_inline)) {
+    const bool start = PACKED && (sp.starts >> k & 1);
+    float y[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = start ? u[k][v] : fmaf(a[k][v], h[v], u[k][v]);
+      y[v] = GATE ? h[v] * silu(Tok::get(rz[k], v)) : h[v];
+      if (PACKED && k >= sp.valid) y[v] = 0.f;
+    }
+    if (mine) Tok::store(yrow + k * D + c, y);
+    if (PACKED && (sp.ends >> k & 1) && p.h_last && mine) {
+      float* hl = p.h_last + static_cast<int64_t>(sp.seq_of(k)) * D + c;
+#pragma unroll
+      for (int v = 0; v < V; ++v) hl[v] = h[v];
+    }
+  };
+  if (rows == K) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) out(k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < rows) out(k);
+  }
+  if (!PACKED && p.h_last && mine && t0 + K >= L) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.h_last[b * D + c + v] = h[v];
+  }
+}
+
+// The last state of a sequence without tokens is its initial one.
+__global__ __launch_bounds__(256) void glr_empty_kernel(const int32_t* offsets, const float* from, float* to, int64_t D) {
+  const int64_t s = blockIdx.x;
+  if (offsets && offsets[s] != offsets[s + 1]) return;
+  for (int64_t d = threadIdx.x; d < D; d += 256) {
+    const float v = from ? from[s * D + d] : 0.f;
+    to[s * D + d] = v;
+  }
+}
+
+__global__ __launch_bounds__(256) void glr_clear_kernel(uint32_t* ws, size_t zeros, size_t words) {
+  const size_t n = static_cast<size_t>(gridDim.x) * 256;
+  for (size_t k = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; k < words; k += n) ws[k] = k < zeros ? 0u : kNoWord;
+}
+
+hipError_t launch_glr_clear(void* ws, const GlrChainLayout& lo, hipStream_t s) {
+  const size_t words = lo.total / 4;
+  const size_t nb = (words + 1023) / 1024;
+  hipLaunchKernelGGL(glr_clear_kernel, dim3(static_cast<unsigned>(nb < 2048 ? nb : 2048)), dim3(256), 0, s,
+                     static_cast<uint32_t*>(ws), lo.maps_at / 4, words);
+  return hipGetLastError();
+}
+
+hipError_t launch_glr_empty(const int32_t* offsets, const float* from, float* to, int64_t rows, int64_t D, hipStream_t s) {
+  if (rows > 0 && from != to)
+    hipLaunchKernelGGL(glr_empty_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, offsets, from, to, D);
+  return hipGetLastError();
 }
 
 namespace {
 
-unsigned blocks(int64_t n) { return static_cast<unsigned>((n + 255) / 256); }
+template <typename Tin, int V, bool PACKED, bool GATE>
+hipError_t launch_one(const GlrFwdParams& p, const GlrChainLayout& lo, hipStream_t s) {
+  const int nct = static_cast<int>((p.dim + 64 * V - 1) / (64 * V));
+  const dim3 grid(static_cast<unsigned>(lo.chains * lo.tiles)), wg(64 * kGlrWaves);
+  const GlrChainWords words = lo.at(p.workspace);
+  const int nt = static_cast<int>(lo.tiles);
+  if (p.codes) hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, PACKED, GATE, true>), grid, wg, 0, s, p, words, nt, nct);
+  else hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, PACKED, GATE, false>), grid, wg, 0, s, p, words, nt, nct);
+  return hipGetLastError();
+}
+
+template <typename Tin, int V>
+hipError_t launch_v(const GlrFwdParams& p, hipStream_t s) {
+  const GlrChainLayout lo(p.batch, p.L, p.dim, V);
+  if (lo.tiles > 1) {
+    const hipError_t e = launch_glr_clear(p.workspace, lo, s);
+    if (e != hipSuccess) return e;
+  }
+  if (p.offsets) return p.z ? launch_one<Tin, V, true, true>(p, lo, s) : launch_one<Tin, V, true, false>(p, lo, s);
+  return p.z ? launch_one<Tin, V, false, true>(p, lo, s) : launch_one<Tin, V, false, false>(p, lo, s);
+}
+
+// Two channels a lane where every row of every tensor holds whole aligned pairs.
+template <typename Tin>
+bool pairs(const GlrFwdParams& p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.r) |
+                       reinterpret_cast<uintptr_t>(p.i) | reinterpret_cast<uintptr_t>(p.z) |
+                       reinterpret_cast<uintptr_t>(p.y);
+  const int64_t odd = p.sx | p.sr | p.si | (p.z ? p.sz : 0) | p.dim;
+  return at % (2 * sizeof(Tin)) == 0 && odd % 2 == 0;
+}
 
 template <typename Tin>
-void launch(const GlrFwdParams& p, hipStream_t s) {
-  const int64_t nseq = p.offsets ? p.num_seqs : p.batch;
-  if (nseq > 0) hipLaunchKernelGGL((glr_fwd_kernel<Tin>), dim3(blocks(nseq * p.dim)), dim3(256), 0, s, p);
-  if (p.offsets && p.L > 0)
-    hipLaunchKernelGGL((glr_pad_kernel<Tin>), dim3(256), dim3(256), 0, s, static_cast<Tin*>(p.y), p.offsets, p.num_seqs,
-                       p.L, p.dim);
-  if (p.codes && p.L > 0) {
-    const void* src[4] = {p.x, p.r, p.i, p.z};
-    const int64_t stride[4] = {p.sx, p.sr, p.si, p.sz};
-    const int64_t n = p.batch * ((p.L + kActGroup - 1) / kActGroup) * p.dim;
-    for (int k = 0; k < (p.z ? 4 : 3); ++k) {
-      int8_t* codes = p.codes + k * p.saved_stride;
-      hipLaunchKernelGGL((glr_save_kernel<Tin>), dim3(blocks(n)), dim3(256), 0, s, static_cast<const Tin*>(src[k]),
-                         stride[k], codes, reinterpret_cast<uint8_t*>(codes) + p.exps_at, p.offsets, p.num_seqs,
-                         p.batch, p.L, p.dim);
-    }
-  }
+hipError_t launch_t(const GlrFwdParams& p, hipStream_t s) {
+  return pairs<Tin>(p) ? launch_v<Tin, 2>(p, s) : launch_v<Tin, 1>(p, s);
 }
 
 }  // namespace
 
+size_t glr_fwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim) {
+  // enough for one and for two channels a lane
+  const size_t a = GlrChainLayout(batch, L, dim, 1).bytes(), b = GlrChainLayout(batch, L, dim, 2).bytes();
+  return a > b ? a : b;
+}
+
 hipError_t launch_glr_fwd(const GlrFwdParams& p, bool bf16, hipStream_t s) {
-  if (bf16) launch<bf16_t>(p, s);
-  else launch<float>(p, s);
-  return hipGetLastError();
-}
-
-hipError_t launch_act8_pack(const void* x, int64_t stride, void* packed, int64_t batch, int64_t L, int64_t dim,
-                            bool bf16, hipStream_t s) {
-  int8_t* codes = static_cast<int8_t*>(packed);
-  uint8_t* exps = static_cast<uint8_t*>(packed) + act8_exps_at(batch, L, dim);
-  const unsigned nb = blocks(batch * ((L + kActGroup - 1) / kActGroup) * dim);
-  if (bf16)
-    hipLaunchKernelGGL((glr_save_kernel<bf16_t>), dim3(nb), dim3(256), 0, s, static_cast<const bf16_t*>(x), stride, codes,
-                       exps, nullptr, int64_t(0), batch, L, dim);
-  else
-    hipLaunchKernelGGL((glr_save_kernel<float>), dim3(nb), dim3(256), 0, s, static_cast<const float*>(x), stride, codes,
-                       exps, nullptr, int64_t(0), batch, L, dim);
-  return hipGetLastError();
-}
-
-template <typename Tin>
-__global__ __launch_bounds__(256) void act8_unpack_kernel(const int8_t* codes, const uint8_t* exps, Tin* x, int64_t batch,
-                                                          int64_t L, int64_t dim) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= batch * L * dim) return;
-  const int64_t d = id % dim, t = id / dim % L, b = id / dim / L;
-  const int64_t ngrp = (L + kActGroup - 1) / kActGroup;
-  store_val(&x[id], act8_value(codes[id], exps[(b * ngrp + t / kActGroup) * dim + d]));
-}
-
-hipError_t launch_act8_unpack(const void* packed, void* x, int64_t batch, int64_t L, int64_t dim, bool bf16,
-                              hipStream_t s) {
-  const int8_t* codes = static_cast<const int8_t*>(packed);
-  const uint8_t* exps = static_cast<const uint8_t*>(packed) + act8_exps_at(batch, L, dim);
-  const unsigned nb = blocks(batch * L * dim);
-  if (bf16)
-    hipLaunchKernelGGL((act8_unpack_kernel<bf16_t>), dim3(nb), dim3(256), 0, s, codes, exps, static_cast<bf16_t*>(x), batch,
-                       L, dim);
-  else
-    hipLaunchKernelGGL((act8_unpack_kernel<float>), dim3(nb), dim3(256), 0, s, codes, exps, static_cast<float*>(x), batch, L,
-                       dim);
-  return hipGetLastError();
+  if (p.h_last && (p.offsets || p.L == 0)) {
+    const hipError_t e = launch_glr_empty(p.offsets, p.h0, p.h_last, p.offsets ? p.num_seqs : p.batch, p.dim, s);
+    if (e != hipSuccess) return e;
+  }
+  if (p.L == 0) return hipSuccess;
+  return bf16 ? launch_t<bf16_t>(p, s) : launch_t<float>(p, s);
 }
 
 }  // namespace sscan
