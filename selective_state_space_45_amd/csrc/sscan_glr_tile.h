@@ -25,9 +25,9 @@ struct TokVec;
 
 template <>
 struct TokVec<bf16_t, 1> {
-  typedef uint16_t reg;
+  typedef uint32_t reg;
   static __device__ __forceinline__ reg load(const bf16_t* p) { return *p; }
-  static __device__ __forceinline__ float get(reg r, int) { return to_f32(r); }
+  static __device__ __forceinline__ float get(reg r, int) { return __uint_as_float(r << 16); }
   static __device__ __forceinline__ void store(bf16_t* p, const float* v) { store_val(p, v[0]); }
 };
 template <>
@@ -188,5 +188,7 @@ struct GlrChain {
 
 // Fills the words before a launch: tickets with zeros, the rest with ones.
 hipError_t launch_glr_clear(void* ws, const GlrChainLayout& lo, hipStream_t s);
+// to[s] = from[s] (zero if null), for the sequences without tokens (all, if offsets is null).
+hipError_t launch_glr_empty(const int32_t* offsets, const float* from, float* to, int64_t rows, int64_t D, hipStream_t s);
 
 }  // namespace sscan
