@@ -156,29 +156,13 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
   __syncthreads();
 
   if (w < V) {
-    float TA = sA[W - 1][w][lane], TG = sG[W - 1][w][lane];
-    bool reset = PACKED && __builtin_amdgcn_readfirstlane(sReset[W - 1]);
-#pragma unroll
-    for (int q = W - 2; q >= 0; --q) {
-      const float qa = sA[q][w][lane], qg = sG[q][w][lane];
-      const bool qr = PACKED && __builtin_amdgcn_readfirstlane(sReset[q]);
-      TA *= qa;
-      TG = qr ? qg : fmaf(qa, TG, qg);
-      reset = reset || qr;
-    }
     float e = 0.f;
-    if (pos == 0 && !PACKED && p.dlast) e = p.dlast[b * D + c + w];
+    if (!PACKED && p.dlast && pos == 0) e = p.dlast[b * D + c + w];
     if (ntiles > 1) {
-      const GlrChain ch{words, static_cast<int64_t>(chain) * ntiles * (64 * V) + w * 64 + lane, 64 * V, pos};
-      if (pos + 1 < ntiles) {
-        if (reset) ch.publish_state(TG);
-        else if (pos == 0) ch.publish_state(fmaf(TA, e, TG));
-        else ch.publish_map(TA, TG);
-      }
-      if (pos > 0) {
-        e = ch.look_back();
-        if (pos + 1 < ntiles && !reset) ch.publish_state(fmaf(TA, e, TG));
-      }
+      GlrMap all{sA[W - 1][w][lane], sG[W - 1][w][lane], PACKED && sReset[W - 1]};
+#pragma unroll
+      for (int q = W - 2; q >= 0; --q) all = GlrMap{sA[q][w][lane], sG[q][w][lane], PACKED && sReset[q]}.after(all);
+      e = glr_pass(words, chain, 64 * V, w * 64 + lane, pos, ntiles, all, e);
     }
     sE[w][lane] = e;
   }

@@ -38,7 +38,7 @@ __device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg* raw
 }
 
 template <typename Tin, int V, bool PACKED, bool GATE, bool SAVE>
-__global__ __launch_bounds__(64 * kGlrWaves) void glr_fwd_kernel(GlrFwdParams p, GlrChainWords words, int ntiles,
+__global__ __launch_bounds__(64 * kGlrWaves, V == 2 && sizeof(Tin) == 4 && GATE ? 3 : 4) void glr_fwd_kernel(GlrFwdParams p, GlrChainWords words, int ntiles,
                                                                  int nct) {
   typedef TokVec<Tin, V> Tok;
   constexpr int K = kActGroup, W = kGlrWaves;
@@ -148,31 +148,13 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_fwd_kernel(GlrFwdParams p,
 
   // wave v < V joins the waves' maps of channel set v, publishes, and looks back
   if (w < V) {
-    float TA = sA[0][w][lane], TB = sB[0][w][lane];
-    bool reset = PACKED && __builtin_amdgcn_readfirstlane(sReset[0]);
-#pragma unroll
-    for (int q = 1; q < W; ++q) {
-      const float qa = sA[q][w][lane], qb = sB[q][w][lane];
-      const bool qr = PACKED && __builtin_amdgcn_readfirstlane(sReset[q]);
-      TA *= qa;
-      TB = qr ? qb : fmaf(qa, TB, qb);
-      reset = reset || qr;
-    }
     float h = 0.f;
-    if (tile == 0) {
-      if (!PACKED && p.h0) h = p.h0[b * D + c + w];
-    }
+    if (!PACKED && p.h0 && tile == 0) h = p.h0[b * D + c + w];
     if (ntiles > 1) {
-      const GlrChain ch{words, static_cast<int64_t>(chain) * ntiles * (64 * V) + w * 64 + lane, 64 * V, tile};
-      if (tile + 1 < ntiles) {
-        if (reset) ch.publish_state(TB);
-        else if (tile == 0) ch.publish_state(fmaf(TA, h, TB));
-        else ch.publish_map(TA, TB);
-      }
-      if (tile > 0) {
-        h = ch.look_back();
-        if (tile + 1 < ntiles && !reset) ch.publish_state(fmaf(TA, h, TB));
-      }
+      GlrMap all{sA[0][w][lane], sB[0][w][lane], PACKED && sReset[0]};
+#pragma unroll
+      for (int q = 1; q < W; ++q) all = GlrMap{sA[q][w][lane], sB[q][w][lane], PACKED && sReset[q]}.after(all);
+      h = glr_pass(words, chain, 64 * V, w * 64 + lane, tile, ntiles, all, h);
     }
     sH[w][lane] = h;
   }

@@ -17,7 +17,6 @@ namespace sscan {
 
 constexpr int kGlrWaves = kGlrBlock / kActGroup;   // waves of a tile, 16 tokens each
 constexpr int kGlrTile = kGlrBlock;                // tokens of a tile: the spacing of saved states
-constexpr int kGlrWindow = 8;                      // tiles that one look back covers
 
 // V channels of one token: loaded and stored as one word per lane.
 template <typename Tin, int V>
@@ -64,12 +63,14 @@ struct GlrSpan {
   __device__ int seq_of(int k) const { return __builtin_amdgcn_readlane(seq, k); }
 };
 
-// Each of 16 lanes finds its token's sequence by bisection: the number of offsets[1 ..]
-// at or below the token.  The loads run beside those of the tokens.  Any contents of
-// offsets give indices inside [0, num_seqs).
-__device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs, int64_t t0, int64_t L) {
-  GlrSpan sp;
-  const int t = static_cast<int>(t0) + static_cast<int>(threadIdx.x & 15);
+// A token's sequence is the number of offsets[1 ..] at or below it, found by bisection.
+// The wave looks for its first token's through the scalar cache, beside the tokens' own
+// loads; only if a boundary falls among its tokens does each of 16 lanes look for its
+// own (with vector loads alone, which return after those of the tokens, a prefill of 37
+// requests, 16411 tokens of 2560 channels in bf16, took 120 us; so ... us).  Any contents
+// of offsets give indices inside [0, num_seqs).
+template <typename P>
+__device__ __forceinline__ int glr_find(P offsets, int num_seqs, int t) {
   int lo = 0, n = num_seqs;
   while (n > 0) {
     const int half = n >> 1;
@@ -77,22 +78,50 @@ __device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs
     lo = right ? lo + half + 1 : lo;
     n = right ? n - half - 1 : half;
   }
-  const bool used = lo < num_seqs && t < L;
-  sp.seq = lo < num_seqs ? lo : num_seqs - 1;
-  const int begin = offsets[sp.seq], end = offsets[sp.seq + 1];
-  const uint32_t in = static_cast<uint32_t>(__ballot(used)) & 0xffffu;
-  sp.starts = static_cast<uint32_t>(__ballot(used && begin == t)) & 0xffffu;
-  sp.ends = static_cast<uint32_t>(__ballot(used && end == t + 1)) & 0xffffu;
-  sp.valid = __builtin_popcount(in);   // padding is at the tail: the used tokens come first
+  return lo;
+}
+__device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs, int64_t t0, int64_t L) {
+  typedef const __attribute__((address_space(4))) int32_t* Scalar;
+  const Scalar so = reinterpret_cast<Scalar>(reinterpret_cast<uintptr_t>(offsets));
+  GlrSpan sp;
+  sp.valid = 0;
+  const int t = static_cast<int>(t0 < L ? t0 : L);
+  const int s = glr_find(so, num_seqs, t);
+  if (s >= num_seqs || t0 >= L) return sp;             // padding only
+  const int begin = so[s], end = so[s + 1];            // begin <= t < end
+  if (end >= t + 16) {
+    sp.seq = s;
+    sp.starts = begin == t;
+    sp.ends = end == t + 16 ? 0x8000u : 0u;
+    sp.valid = static_cast<int>(L - t0 < 16 ? L - t0 : 16);
+    return sp;
+  }
+  const int mine = t + static_cast<int>(threadIdx.x & 15);
+  const int q = glr_find(offsets, num_seqs, mine);
+  const bool used = q < num_seqs && mine < L;
+  sp.seq = q < num_seqs ? q : num_seqs - 1;
+  const int first = offsets[sp.seq], past = offsets[sp.seq + 1];
+  sp.starts = static_cast<uint32_t>(__ballot(used && first == mine)) & 0xffffu;
+  sp.ends = static_cast<uint32_t>(__ballot(used && past == mine + 1)) & 0xffffu;
+  // padding is at the tail: the used tokens come first
+  sp.valid = __builtin_popcount(static_cast<uint32_t>(__ballot(used)) & 0xffffu);
   return sp;
 }
 
 // ---------------------------------------------------------------------------
-// The chain.  Tile k publishes its map (A, B) as soon as it has it, and the state it
-// leaves once it knows the one that enters.  A later tile looks back over the window of
-// tiles before it for the nearest state, and applies the maps between, in order: the
-// same operations as going tile by tile, so results do not depend on timing.  Tiles
-// that contain a sequence's start know the state they leave at once.
+// The chain.  Its tiles form groups of 8.  Every tile publishes its map (A, B) as soon
+// as it has it; a group's last tile publishes the group's map, its tiles' maps joined in
+// order, and, once it knows the state S_g that enters the group, the one that leaves,
+// S_{g+1} = A_g S_g + B_g.  A tile waits for the maps before it in its group, which wait
+// for nothing, and looks back over up to 4 groups for the nearest state there is,
+// carried through the groups' maps after it and then the tiles'.  These are the same
+// operations wherever the state is found: results do not depend on timing.  (With
+// states per tile instead of per group, 64 tiles back, the chain itself bounded long
+// sequences: 131072 tokens of 2560 channels in bf16 took 0.79 ms, 0.56 with the wait
+// left out.)
+//
+// A map's A is at least 0; its sign bit marks a run that contains a sequence's start:
+// what it leaves is B, whatever enters.
 //
 // Each published word carries its own readiness: a word of all ones (which a fill
 // kernel writes before) is no value, and a value that would be all ones, a NaN, is
@@ -104,87 +133,138 @@ __device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs
 // tiles it may wait for were taken by workgroups that have already begun, and the
 // earliest tile waits for none.
 // ---------------------------------------------------------------------------
+constexpr int kGlrGroup = 8;   // tiles of a group
+constexpr int kGlrBack = 4;    // groups that one look back covers
+
 struct GlrChainWords {
-  uint32_t* tickets;   // [chains], zero
-  uint64_t* maps;      // [chains][tiles][64 V], all ones
-  uint32_t* states;    // [chains][tiles][64 V], all ones
+  uint32_t* tickets;    // [chains], zero
+  uint64_t* maps;       // [chains][tiles][64 V], all ones
+  uint64_t* group_maps; // [chains][groups][64 V], all ones
+  uint32_t* states;     // [chains][groups][64 V], all ones
 };
 
-// Bytes of a launch's words: tickets (to a multiple of 256), maps, states.
+// Bytes of a launch's words: tickets (to a multiple of 256), then the others.
 struct GlrChainLayout {
-  int64_t chains, tiles, lanes;
-  size_t maps_at, states_at, total;
+  int64_t chains, tiles, groups, lanes;
+  size_t maps_at, group_maps_at, states_at, total;
   GlrChainLayout(int64_t batch, int64_t L, int64_t dim, int V) {
     lanes = 64 * V;
     chains = batch * ((dim + lanes - 1) / lanes);
     tiles = (L + kGlrTile - 1) / kGlrTile;
+    groups = (tiles + kGlrGroup - 1) / kGlrGroup;
     maps_at = (static_cast<size_t>(chains) * 4 + 255) & ~size_t(255);
-    states_at = maps_at + static_cast<size_t>(chains) * tiles * lanes * 8;
-    total = states_at + static_cast<size_t>(chains) * tiles * lanes * 4;
+    group_maps_at = maps_at + static_cast<size_t>(chains) * tiles * lanes * 8;
+    states_at = group_maps_at + static_cast<size_t>(chains) * groups * lanes * 8;
+    total = states_at + static_cast<size_t>(chains) * groups * lanes * 4;
   }
   // a single tile needs no words
   size_t bytes() const { return tiles > 1 ? (total + 255) & ~size_t(255) : 0; }
   GlrChainWords at(void* ws) const {
     char* p = static_cast<char*>(ws);
     return {reinterpret_cast<uint32_t*>(p), reinterpret_cast<uint64_t*>(p + maps_at),
-            reinterpret_cast<uint32_t*>(p + states_at)};
+            reinterpret_cast<uint64_t*>(p + group_maps_at), reinterpret_cast<uint32_t*>(p + states_at)};
   }
 };
 
 constexpr uint32_t kNoWord = 0xffffffffu;
-__device__ __forceinline__ uint32_t word_of(float v) {
-  const uint32_t b = __float_as_uint(v);
-  return b == kNoWord ? 0x7fc00000u : b;
-}
 
-// One wave's view of the chain: 64 of the tile's channels, one per lane.
-struct GlrChain {
-  GlrChainWords w;
-  int64_t first;     // index of the words of tile 0 of the chain, for this lane
-  int64_t pitch;     // words from one tile to the next
-  int tile;          // position in the chain, from the end that is computed first
-
-  __device__ void publish_map(float A, float B) const {
-    __hip_atomic_store(&w.maps[first + tile * pitch], (static_cast<uint64_t>(word_of(B)) << 32) | __float_as_uint(A),
-                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+struct GlrMap {
+  float A, B;
+  bool reset;
+  // this map after `before`
+  __device__ GlrMap after(const GlrMap& before) const {
+    return reset ? *this : GlrMap{A * before.A, fmaf(A, before.B, B), before.reset};
   }
-  __device__ void publish_state(float h) const {
-    __hip_atomic_store(&w.states[first + tile * pitch], word_of(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __device__ float operator()(float h) const { return reset ? B : fmaf(A, h, B); }
+  __device__ uint64_t word() const {
+    const uint32_t a = reset ? 0x80000000u : (A != A ? 0x7fc00000u : __float_as_uint(A));
+    const uint32_t b = __float_as_uint(B);
+    return (static_cast<uint64_t>(b == kNoWord ? 0x7fc00000u : b) << 32) | a;
   }
-
-  // The state that enters this tile (tile > 0).  Called by all 64 lanes.
-  __device__ float look_back() const {
-    const int n = tile < kGlrWindow ? tile : kGlrWindow;
-    for (;;) {
-      uint32_t st[kGlrWindow];
-      uint64_t mp[kGlrWindow];
-#pragma unroll
-      for (int k = 0; k < kGlrWindow; ++k) {
-        const int64_t at = first + (tile - 1 - (k < n ? k : n - 1)) * pitch;   // past the chain's begin: a tile again, unused
-        st[k] = __hip_atomic_load(&w.states[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        mp[k] = __hip_atomic_load(&w.maps[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      // the nearest tile whose state is there for every lane, with all maps between
-      int found = -1;
-      bool maps = true;
-#pragma unroll
-      for (int k = 0; k < kGlrWindow; ++k) {
-        if (found < 0 && maps && k < n && __all(st[k] != kNoWord)) found = k;
-        maps = maps && __all(static_cast<uint32_t>(mp[k] >> 32) != kNoWord);
-      }
-      if (found >= 0) {
-        float h = 0.f;
-#pragma unroll
-        for (int k = kGlrWindow - 1; k >= 0; --k) {
-          const float A = __uint_as_float(static_cast<uint32_t>(mp[k])), B = __uint_as_float(static_cast<uint32_t>(mp[k] >> 32));
-          h = k == found ? __uint_as_float(st[k]) : (k < found ? fmaf(A, h, B) : h);
-        }
-        return h;
-      }
-      __builtin_amdgcn_s_sleep(1);
-    }
+  static __device__ GlrMap of(uint64_t w) {
+    const uint32_t a = static_cast<uint32_t>(w);
+    return {__uint_as_float(a), __uint_as_float(static_cast<uint32_t>(w >> 32)), (a >> 31) != 0};
   }
 };
+__device__ __forceinline__ bool there(uint64_t w) { return static_cast<uint32_t>(w >> 32) != kNoWord; }
+
+// One wave's part of the chain: 64 of the tile's channels, one per lane.  pos: the tile's
+// place in the chain, of ntiles > 1.  own: the tile's map; initial: the state that
+// enters the chain (read at pos 0 only).  Returns the state that enters the tile.  All 64
+// lanes call it.
+__device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain, int lanes, int at, int pos, int ntiles,
+                                          const GlrMap& own, float initial) {
+  const int g = pos / kGlrGroup, j = pos % kGlrGroup, ngroups = (ntiles + kGlrGroup - 1) / kGlrGroup;
+  // words of the tile's group, of the group before it, and of the state that enters it
+  uint64_t* maps = w.maps + (chain * ntiles + g * kGlrGroup) * lanes;
+  uint64_t* gmaps = w.group_maps + (chain * ngroups + g) * lanes;
+  uint32_t* states = w.states + (chain * ngroups + g) * lanes;
+  auto put_state = [&](int group, float h) {
+    const uint32_t b = __float_as_uint(h);
+    __hip_atomic_store(states + (group - g) * lanes + at, b == kNoWord ? 0x7fc00000u : b, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+  };
+  if (pos == 0) put_state(0, initial);
+  const bool closes = j == kGlrGroup - 1 && g + 1 < ngroups;   // the last tile of a group with another after it
+  if (j < kGlrGroup - 1 && pos + 1 < ntiles)
+    __hip_atomic_store(maps + j * lanes + at, own.word(), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (pos == 0) return initial;
+
+  uint64_t m[kGlrGroup - 1];
+  bool have = false;
+  GlrMap all = own;
+  for (;;) {
+    uint32_t s[kGlrBack];
+    uint64_t gm[kGlrBack];
+    if (!have)
+#pragma unroll
+      for (int k = 0; k < kGlrGroup - 1; ++k)
+        if (k < j) m[k] = __hip_atomic_load(maps + k * lanes + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int k = 0; k < kGlrBack; ++k) {
+      s[k] = kNoWord;
+      gm[k] = ~uint64_t(0);
+      if (k <= g) {
+        s[k] = __hip_atomic_load(states - k * lanes + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (k + 1 <= g && k + 1 < kGlrBack)
+          gm[k] = __hip_atomic_load(gmaps - (k + 1) * lanes + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    if (!have) {
+      bool ok = true;
+#pragma unroll
+      for (int k = 0; k < kGlrGroup - 1; ++k) ok = ok && (k >= j || there(m[k]));
+      have = __all(ok);
+      if (have && closes) {
+        all = GlrMap::of(m[0]);
+#pragma unroll
+        for (int k = 1; k < kGlrGroup - 1; ++k) all = GlrMap::of(m[k]).after(all);
+        all = own.after(all);
+        if (__all(all.reset)) put_state(g + 1, all.B);
+        else __hip_atomic_store(gmaps + at, all.word(), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    int found = -1;
+    bool through = true;
+#pragma unroll
+    for (int k = 0; k < kGlrBack; ++k) {
+      if (found < 0 && through && __all(s[k] != kNoWord)) found = k;
+      through = through && __all(there(gm[k]));
+    }
+    if (have && found >= 0) {
+      float h = 0.f;
+#pragma unroll
+      for (int k = kGlrBack - 1; k >= 0; --k)
+        h = k == found ? __uint_as_float(s[k]) : (k < found ? GlrMap::of(gm[k])(h) : h);
+      if (closes && !__all(all.reset)) put_state(g + 1, all(h));
+#pragma unroll
+      for (int k = 0; k < kGlrGroup - 1; ++k)
+        if (k < j) h = GlrMap::of(m[k])(h);
+      return h;
+    }
+    __builtin_amdgcn_s_sleep(1);
+  }
+}
 
 // Fills the words before a launch: tickets with zeros, the rest with ones.
 hipError_t launch_glr_clear(void* ws, const GlrChainLayout& lo, hipStream_t s);
