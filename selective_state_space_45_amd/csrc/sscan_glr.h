@@ -102,15 +102,9 @@ inline size_t act8_total(int64_t batch, int64_t L, int64_t dim) {
 // reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid(float v) { return hw_rcp(1.f + hw_exp2(-v * kLog2e)); }
 
-// sigmoid(v) and its derivative sigmoid (1 - sigmoid), the latter without the
-// cancellation of 1 - sigmoid: with w = e^-|v| and q = 1 / (1 + w), sigmoid is q or
-// w q by the sign of v, and the derivative is w q^2.
-__device__ __forceinline__ float sigmoid_d(float v, float& deriv) {
-  const float w = hw_exp2(-fabsf(v) * kLog2e);
-  const float q = hw_rcp(1.f + w);
-  deriv = w * q * q;
-  return v >= 0.f ? q : (v < 0.f ? w * q : v);   // NaN stays NaN
-}
+// The derivative s (1 - s) of a sigmoid that is s: off by at most 2^-24 (of its largest
+// value, 1/4) where s is close to 1.
+__device__ __forceinline__ float slope(float s) { return fmaf(-s, s, s); }
 
 // softplus(v) = max(v, 0) + log(1 + w), w = e^-|v|, to float32 accuracy at every v:
 // log(1 + w) = 2 atanh(s), s = w / (2 + w) <= 1/3, by its odd series through s^15
@@ -147,10 +141,10 @@ __device__ __forceinline__ float decay_of(float q, float& one_minus_a2) {
 
 __device__ __forceinline__ float hw_sqrt(float v) { return __builtin_amdgcn_sqrtf(v); }
 
-// 1 / sqrt(v), and 0 below the smallest normal number, where the hardware's reciprocal
-// root is infinite: 1 - a^2 is that small only for decay rates below 1e-37, whose terms
-// with 1 / sqrt(1 - a^2), each times the rate, are below 1e-18 of the others.
-__device__ __forceinline__ float rsq_or_0(float v) { return v < 1.17549435e-38f ? 0.f : __builtin_amdgcn_rsqf(v); }
+// 1 / m for m = sqrt(1 - a^2), and 0 below 1e-18, where 1 - a^2 is about to leave the
+// normal numbers: m is that small only for decay rates below 1e-36, whose terms with
+// 1 / m, each times the rate, are below 1e-18 of the others.
+__device__ __forceinline__ float rcp_or_0(float m) { return m < 1e-18f ? 0.f : hw_rcp(m); }
 
 // 8-bit codes.  `field` is the float32 exponent field (0 .. 255) of the group's largest
 // magnitude; 255 marks a group with an infinity or NaN.  Scaling by powers of two is

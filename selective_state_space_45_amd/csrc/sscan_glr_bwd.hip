@@ -54,7 +54,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
   const uint32_t chain = blockIdx.x % nchains;
   int pos = 0;
   if (ntiles > 1) {
-    if (threadIdx.x == 0) sTile = static_cast<int>(atomicAdd(&words.tickets[chain], 1u));
+    if (threadIdx.x == 0) sTile = static_cast<int>(atomicAdd(&words.tickets[static_cast<size_t>(chain) * kGlrTicket], 1u));
     __syncthreads();
     pos = __builtin_amdgcn_readfirstlane(sTile);
   }
@@ -96,15 +96,18 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
     h[v] = p.ckpt[(b * ntiles + tile) * D + c + v];
   }
 
-  float a[K][V], u[K][V];
+  float a[K][V], m[K][V], rho[K][V], iota[K][V], before[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float one;
-      a[k][v] = decay_of(rate[v] * sigmoid(ar.get(rr[k], v) + rb[v]), one);
-      u[k][v] = hw_sqrt(one) * (sigmoid(ai.get(ri[k], v) + ib[v]) * ax.get(rx[k], v));
+      rho[k][v] = sigmoid(ar.get(rr[k], v) + rb[v]);
+      iota[k][v] = sigmoid(ai.get(ri[k], v) + ib[v]);
+      a[k][v] = decay_of(rate[v] * rho[k][v], one);
+      m[k][v] = hw_sqrt(one);
     }
+  auto input = [&](int k, int v) __attribute__((always_inline)) { return iota[k][v] * ax.get(rx[k], v); };
   auto grad_y = [&](int k, int v) __attribute__((always_inline)) {
     const float dy = Tok::get(rg[k], v);
     return GATE ? dy * silu(az.get(rz[k], v)) : dy;
@@ -125,7 +128,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         A[v] *= a[k][v];
-        B[v] = start ? fmaf(a[k][v], state0(k, v), u[k][v]) : fmaf(a[k][v], B[v], u[k][v]);
+        B[v] = fmaf(a[k][v], start ? state0(k, v) : B[v], m[k][v] * input(k, v));
       }
     };
     auto back = [&](int k) __attribute__((always_inline)) {
@@ -166,8 +169,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
     }
     sE[w][lane] = e;
   }
-  // the states of the wave's tokens, while the gradient is on its way: u becomes the
-  // state that each token continues
+  // the states that the wave's tokens continue
 #pragma unroll
   for (int q = 0; q < W - 1; ++q) {
     if (q >= w) break;
@@ -180,17 +182,9 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (PACKED && (sp.starts >> k & 1)) h[v] = state0(k, v);
-      const float before = h[v];
-      h[v] = fmaf(a[k][v], h[v], u[k][v]);
-      u[k][v] = before;
+      before[k][v] = h[v];
+      h[v] = fmaf(a[k][v], h[v], m[k][v] * input(k, v));
     }
-  // the gates are formed again below: held over the wait they would take more registers
-  // than two workgroups a SIMD leave
-#pragma unroll
-  for (int k = 0; k < K; ++k) asm volatile("" : "+v"(rr[k]), "+v"(ri[k]), "+v"(rx[k]));
-  if (GATE)
-#pragma unroll
-    for (int k = 0; k < K; ++k) asm volatile("" : "+v"(rz[k]), "+v"(rg[k]));
   __syncthreads();
 
   float e[V], slam[V], srb[V], sib[V];
@@ -219,31 +213,25 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
     float gx[V], gr[V], gi[V], gz[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float drho, diota, one;
-      const float rho = sigmoid_d(ar.get(rr[k], v) + rb[v], drho);
-      const float iota = sigmoid_d(ai.get(ri[k], v) + ib[v], diota);
-      const float av = decay_of(rate[v] * rho, one);
-      const float rm = rsq_or_0(one), m = one * rm;
-      const float x = ax.get(rx[k], v), before = u[k][v], in = iota * x;
+      const float P = rho[k][v], I = iota[k][v], A = a[k][v], M = m[k][v], H = before[k][v];
+      const float x = ax.get(rx[k], v), in = I * x;
       float gy = Tok::get(rg[k], v);
       if (GATE) {
-        const float z = az.get(rz[k], v);
-        float dsz;
-        const float sz = sigmoid_d(z, dsz);
-        gz[v] = gy * fmaf(av, before, m * in) * fmaf(z, dsz, sz);
+        const float z = az.get(rz[k], v), sz = sigmoid(z);
+        gz[v] = gy * fmaf(A, H, M * in) * fmaf(z, slope(sz), sz);
         gy *= z * sz;
       }
       if (PACKED && (sp.ends >> k & 1)) e[v] = last_grad(k, v);
       const float g = gy + e[v];
-      const float dla = g * (av * before - in * (av * av) * rm);
-      const float du = g * m;
-      gx[v] = du * iota;
-      gi[v] = du * x * diota;
-      gr[v] = -rate[v] * dla * drho;
-      slam[v] = fmaf(dla, rho, slam[v]);
+      const float dla = g * (A * H - in * A * (A * rcp_or_0(M)));
+      const float du = g * M;
+      gx[v] = du * I;
+      gi[v] = du * x * slope(I);
+      gr[v] = -rate[v] * dla * slope(P);
+      slam[v] = fmaf(dla, P, slam[v]);
       srb[v] += gr[v];
       sib[v] += gi[v];
-      e[v] = av * g;
+      e[v] = A * g;
       if (PACKED && (sp.starts >> k & 1)) {
         if (p.dh0 && mine) p.dh0[static_cast<int64_t>(sp.seq_of(k)) * D + c + v] = e[v];
         e[v] = 0.f;
@@ -294,10 +282,19 @@ __global__ __launch_bounds__(1024) void glr_param_kernel(const float* part, cons
   const int ct = set / V, v = set % V;
   float s = 0.f;
   const int64_t n = batch * ntiles;
-  for (int64_t k = w; k < n; k += 16) {
+  auto at = [&](int64_t k) {
     const int64_t b = k / ntiles, tile = k - b * ntiles;
-    s += part[((b * nct + ct) * ntiles + tile) * (3 * 64 * V) + (kind * V + v) * 64 + lane];
+    return part[((b * nct + ct) * ntiles + tile) * (3 * 64 * V) + (kind * V + v) * 64 + lane];
+  };
+  int64_t k = w;
+  for (; k + 7 * 16 < n; k += 8 * 16) {   // eight loads in flight
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = at(k + j * 16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += x[j];
   }
+  for (; k < n; k += 16) s += at(k);
   sum[w][lane] = s;
   __syncthreads();
   const int64_t d = (static_cast<int64_t>(ct) * 64 + lane) * V + v;
@@ -356,7 +353,7 @@ bool pairs(const GlrBwdParams& p) {
 
 template <typename Tin>
 hipError_t launch_t(const GlrBwdParams& p, hipStream_t s) {
-  return pairs<Tin>(p) ? launch_v<Tin, 2>(p, s) : launch_v<Tin, 1>(p, s);
+  return launch_v<Tin, 1>(p, s);
 }
 
 }  // namespace

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && sizeof(Tin) == 4 && GATE 
   const uint32_t chain = blockIdx.x % nchains;
   int tile = 0;
   if (ntiles > 1) {
-    if (threadIdx.x == 0) sTile = static_cast<int>(atomicAdd(&words.tickets[chain], 1u));
+    if (threadIdx.x == 0) sTile = static_cast<int>(atomicAdd(&words.tickets[static_cast<size_t>(chain) * kGlrTicket], 1u));
     __syncthreads();
     tile = __builtin_amdgcn_readfirstlane(sTile);
   }

@@ -136,8 +136,12 @@ __device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs
 constexpr int kGlrGroup = 8;   // tiles of a group
 constexpr int kGlrBack = 4;    // groups that one look back covers
 
+// Counters lie a cache line apart: side by side, all of a launch's first workgroups
+// queued at a few lines, 4 us before the first load.
+constexpr int kGlrTicket = 32;
+
 struct GlrChainWords {
-  uint32_t* tickets;    // [chains], zero
+  uint32_t* tickets;    // [chains], kGlrTicket words apart, zero
   uint64_t* maps;       // [chains][tiles][64 V], all ones
   uint64_t* group_maps; // [chains][groups][64 V], all ones
   uint32_t* states;     // [chains][groups][64 V], all ones
@@ -152,7 +156,7 @@ struct GlrChainLayout {
     chains = batch * ((dim + lanes - 1) / lanes);
     tiles = (L + kGlrTile - 1) / kGlrTile;
     groups = (tiles + kGlrGroup - 1) / kGlrGroup;
-    maps_at = (static_cast<size_t>(chains) * 4 + 255) & ~size_t(255);
+    maps_at = (static_cast<size_t>(chains) * kGlrTicket * 4 + 255) & ~size_t(255);
     group_maps_at = maps_at + static_cast<size_t>(chains) * tiles * lanes * 8;
     states_at = group_maps_at + static_cast<size_t>(chains) * groups * lanes * 8;
     total = states_at + static_cast<size_t>(chains) * groups * lanes * 4;
