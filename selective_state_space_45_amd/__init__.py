@@ -393,33 +393,79 @@ for _name, _args, _res in (
     getattr(_lib, _name).restype = _res
 
 
-def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
-    """Checks a token tensor whose rows may be columns of a wider one (last index dense,
-    tokens evenly spaced); returns its token stride in elements."""
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return shape[-1]
-    st = t.stride()
-    step = st[-2]
-    even = t.dim() == 2 or shape[0] == 1 or st[0] == shape[1] * step
-    if t.dim() == 3 and shape[1] == 1:
-        step, even = st[0], True
-    if (st[-1] != 1 and shape[-1] != 1) or not even or step < shape[-1]:
+# The calls below are made once a token in a decode loop, where the host's time counts:
+# a good argument costs one helper call, and the messages are made only for a bad one.
+
+def _rows(t: torch.Tensor, name: str, dtype, shape):
+    """(address, token stride in elements) of a token tensor, whose rows may be columns of a
+    wider one (last index dense, tokens evenly spaced)."""
+    if t.is_cuda and t.dtype is dtype and t.shape == shape:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[-1]
+        st = t.stride()
+        step, even = st[-2], len(shape) == 2 or shape[0] == 1 or st[0] == shape[1] * st[-2]
+        if len(shape) == 3 and shape[1] == 1:
+            step, even = st[0], True
+        if (st[-1] == 1 or shape[-1] == 1) and even and step >= shape[-1]:
+            return t.data_ptr(), step
         raise ValueError(f"{name} must have a dense last dimension and evenly spaced tokens, got strides {st}")
-    return step
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _at(t: Optional[torch.Tensor], name: str, dtype, shape):
+    """The address of a dense tensor (None for None)."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _dev(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _bytes_at(t: Optional[torch.Tensor], name: str):
+    """(address, bytes) of a dense buffer of any type ((None, 0) for None)."""
+    if t is None:
+        return None, 0
+    if not (t.is_cuda and t.is_contiguous()):
+        _dev(t, name)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_at(t: torch.Tensor):
+    """The handle of the current stream of t's device."""
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _strides(values, dim: int):
-    return None if all(v == dim for v in values) else (ctypes.c_int64 * 4)(*values)
+    for v in values:
+        if v != dim:
+            return (ctypes.c_int64 * 4)(*values)
+    return None
 
 
-def _nbytes(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+def _nseq(offsets, batch):
+    """(address of offsets, number of sequences)."""
+    if offsets is None:
+        return None, batch
+    _dev(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be [sequences + 1]")
+    return offsets.data_ptr(), offsets.numel() - 1
+
+
+def _scratch(workspace, need, device):
+    """A workspace of `need` bytes unless one was given, with its address and size."""
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return (workspace,) + _bytes_at(workspace, "workspace")
 
 
 def act8_bytes(batch: int, seqlen: int, dim: int) -> int:
@@ -436,12 +482,11 @@ def sscan_act8_pack(x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torc
     if x.dtype not in _DTYPES:
         raise ValueError("x must be float32 or bfloat16")
     batch, seqlen, dim = x.shape
-    stride = _rows(x, "x", x.dtype, x.shape)
+    at, stride = _rows(x, "x", x.dtype, x.shape)
     if out is None:
         out = torch.empty(act8_bytes(batch, seqlen, dim), dtype=torch.uint8, device=x.device)
-    _dev(out, "out")
-    _check(_lib.sscan_act8_pack(batch, seqlen, dim, _DTYPES[x.dtype], _ptr(x), stride, _ptr(out), _nbytes(out),
-                                _stream(x.device)))
+    to, size = _bytes_at(out, "out")
+    _check(_lib.sscan_act8_pack(batch, seqlen, dim, _DTYPES[x.dtype], at, stride, to, size, _stream_at(x)))
     return out
 
 
@@ -453,12 +498,11 @@ def sscan_act8_unpack(packed: torch.Tensor, shape, dtype=torch.bfloat16, out: Op
         raise ValueError("shape must be [batch, seqlen, dim]")
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
-    _dev(packed, "packed")
+    at, size = _bytes_at(packed, "packed")
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=packed.device)
-    _dev(out, "out", dtype, shape)
-    _check(_lib.sscan_act8_unpack(shape[0], shape[1], shape[2], _DTYPES[dtype], _ptr(packed), _nbytes(packed), _ptr(out),
-                                  _stream(packed.device)))
+    _check(_lib.sscan_act8_unpack(shape[0], shape[1], shape[2], _DTYPES[dtype], at, size,
+                                  _at(out, "out", dtype, torch.Size(shape)), _stream_at(packed)))
     return out
 
 
@@ -476,27 +520,6 @@ def glr_saved_bytes(batch: int, seqlen: int, dim: int, gated: bool = False) -> i
 def glr_workspace_size(batch: int, seqlen: int, dim: int, backward: bool = False) -> int:
     fn = _lib.sscan_glr_bwd_workspace_size if backward else _lib.sscan_glr_fwd_workspace_size
     return int(fn(batch, seqlen, dim))
-
-
-def _glr_params(dim, device, lam, r_bias, i_bias, offsets, batch):
-    """Checks the per-channel parameters and offsets; returns the number of sequences."""
-    _dev(lam, "lam", torch.float32, (dim,))
-    if r_bias is not None:
-        _dev(r_bias, "r_bias", torch.float32, (dim,))
-    if i_bias is not None:
-        _dev(i_bias, "i_bias", torch.float32, (dim,))
-    if offsets is None:
-        return batch
-    _dev(offsets, "offsets", torch.int32)
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must be [sequences + 1]")
-    return offsets.numel() - 1
-
-
-def _glr_workspace(workspace, need, device):
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace
 
 
 def sscan_glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor,
@@ -520,27 +543,25 @@ def sscan_glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.
     if x.dtype not in _DTYPES:
         raise ValueError("x must be float32 or bfloat16")
     batch, seqlen, dim = shape = x.shape
-    dev = x.device
-    strides = [_rows(x, "x", x.dtype, shape), _rows(r, "r", x.dtype, shape), _rows(i, "i", x.dtype, shape),
-               dim if z is None else _rows(z, "z", x.dtype, shape)]
-    nseq = _glr_params(dim, dev, lam, r_bias, i_bias, offsets, batch)
-    if initial_state is not None:
-        _dev(initial_state, "initial_state", torch.float32, (nseq, dim))
-    y = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else _dev(out, "out", x.dtype, shape)
+    dtype = x.dtype
+    px, sx = _rows(x, "x", dtype, shape)
+    pr, sr = _rows(r, "r", dtype, shape)
+    pi, si = _rows(i, "i", dtype, shape)
+    pz, sz = (None, dim) if z is None else _rows(z, "z", dtype, shape)
+    poff, nseq = _nseq(offsets, batch)
+    y = torch.empty(shape, dtype=dtype, device=x.device) if out is None else out
     if last_state is None and return_last_state:
-        last_state = torch.empty((nseq, dim), dtype=torch.float32, device=dev)
-    elif last_state is not None:
-        _dev(last_state, "last_state", torch.float32, (nseq, dim))
-    if checkpoints is not None:
-        _dev(checkpoints, "checkpoints")
-    if saved is not None:
-        _dev(saved, "saved")
-    workspace = _glr_workspace(workspace, _lib.sscan_glr_fwd_workspace_size(batch, seqlen, dim), dev)
-    _check(_lib.sscan_glr_fwd(batch, seqlen, dim, _DTYPES[x.dtype], _ptr(x), _ptr(r), _ptr(i), _ptr(z),
-                              _strides(strides, dim), _ptr(lam), _ptr(r_bias), _ptr(i_bias), decay_scale,
-                              _ptr(initial_state), _ptr(offsets), nseq, _ptr(y), _ptr(last_state), _ptr(checkpoints),
-                              _nbytes(checkpoints), _ptr(saved), _nbytes(saved), _ptr(workspace), _nbytes(workspace),
-                              _stream(dev)))
+        last_state = torch.empty((nseq, dim), dtype=torch.float32, device=x.device)
+    workspace, pw, nw = _scratch(workspace, _lib.sscan_glr_fwd_workspace_size(batch, seqlen, dim), x.device)
+    f32, per_channel, per_seq = torch.float32, (dim,), (nseq, dim)
+    rc = _lib.sscan_glr_fwd(
+        batch, seqlen, dim, _DTYPES[dtype], px, pr, pi, pz, _strides((sx, sr, si, sz), dim),
+        _at(lam, "lam", f32, per_channel), _at(r_bias, "r_bias", f32, per_channel),
+        _at(i_bias, "i_bias", f32, per_channel), decay_scale, _at(initial_state, "initial_state", f32, per_seq), poff, nseq,
+        _at(y, "out", dtype, shape), _at(last_state, "last_state", f32, per_seq), *_bytes_at(checkpoints, "checkpoints"),
+        *_bytes_at(saved, "saved"), pw, nw, _stream_at(x))
+    if rc:
+        _check(rc)
     return (y, last_state) if return_last_state else y
 
 
@@ -565,49 +586,47 @@ def sscan_glr_bwd(lam: torch.Tensor, dy: torch.Tensor, checkpoints: torch.Tensor
         raise ValueError("dy must be float32 or bfloat16")
     batch, seqlen, dim = shape = dy.shape
     dtype, dev = dy.dtype, dy.device
-    _dev(dy, "dy")
+    px = pr = pi = pz = None
+    sx = sr = si = sz = dim
     if saved is not None:
         if x is not None or r is not None or i is not None or z is not None:
             raise ValueError("give either saved or x, r, i and z")
-        _dev(saved, "saved")
-        strides = [dim] * 4
     else:
         if x is None or r is None or i is None:
             raise ValueError("x, r and i are required without saved")
         gated = z is not None
-        strides = [_rows(x, "x", dtype, shape), _rows(r, "r", dtype, shape), _rows(i, "i", dtype, shape),
-                   dim if z is None else _rows(z, "z", dtype, shape)]
-    nseq = _glr_params(dim, dev, lam, r_bias, i_bias, offsets, batch)
-    for t, name in ((initial_state, "initial_state"), (dlast_state, "dlast_state")):
-        if t is not None:
-            _dev(t, name, torch.float32, (nseq, dim))
-    _dev(checkpoints, "checkpoints")
+        px, sx = _rows(x, "x", dtype, shape)
+        pr, sr = _rows(r, "r", dtype, shape)
+        pi, si = _rows(i, "i", dtype, shape)
+        if gated:
+            pz, sz = _rows(z, "z", dtype, shape)
+    poff, nseq = _nseq(offsets, batch)
     out = dict(out or {})
-    grad_strides = []
-    for name in ("dx", "dr", "di", "dz"):
-        if name == "dz" and not gated:
-            grad_strides.append(dim)
-            continue
-        t = out.get(name)
-        if t is None:
-            out[name] = torch.empty(shape, dtype=dtype, device=dev)
-            grad_strides.append(dim)
-        else:
-            grad_strides.append(_rows(t, name, dtype, shape))
-    for name, want, size in (("dlam", True, (dim,)), ("dr_bias", want_dbias, (dim,)), ("di_bias", want_dbias, (dim,)),
-                             ("dinitial_state", want_dinitial_state, (nseq, dim))):
-        if name in out:
-            _dev(out[name], name, torch.float32, size)
-        elif want:
-            out[name] = torch.empty(size, dtype=torch.float32, device=dev)
-    workspace = _glr_workspace(workspace, _lib.sscan_glr_bwd_workspace_size(batch, seqlen, dim), dev)
-    _check(_lib.sscan_glr_bwd(batch, seqlen, dim, _DTYPES[dtype], _ptr(x), _ptr(r), _ptr(i), _ptr(z),
-                              _strides(strides, dim), _ptr(saved), _nbytes(saved), _ptr(lam), _ptr(r_bias),
-                              _ptr(i_bias), decay_scale, _ptr(initial_state), _ptr(offsets), nseq, _ptr(checkpoints),
-                              _nbytes(checkpoints), _ptr(dy), _ptr(dlast_state), _ptr(out["dx"]), _ptr(out["dr"]),
-                              _ptr(out["di"]), _ptr(out.get("dz")), _strides(grad_strides, dim), _ptr(out["dlam"]),
-                              _ptr(out.get("dr_bias")), _ptr(out.get("di_bias")), _ptr(out.get("dinitial_state")),
-                              _ptr(workspace), _nbytes(workspace), _stream(dev)))
+    grads = []
+    for name in ("dx", "dr", "di", "dz") if gated else ("dx", "dr", "di"):
+        g = out.get(name)
+        if g is None:
+            g = out[name] = torch.empty(shape, dtype=dtype, device=dev)
+        grads.append(_rows(g, name, dtype, shape))
+    if not gated:
+        grads.append((None, dim))
+    f32, per_channel, per_seq = torch.float32, (dim,), (nseq, dim)
+    for name, want, size in (("dlam", True, per_channel), ("dr_bias", want_dbias, per_channel),
+                             ("di_bias", want_dbias, per_channel), ("dinitial_state", want_dinitial_state, per_seq)):
+        if want and name not in out:
+            out[name] = torch.empty(size, dtype=f32, device=dev)
+    workspace, pw, nw = _scratch(workspace, _lib.sscan_glr_bwd_workspace_size(batch, seqlen, dim), dev)
+    rc = _lib.sscan_glr_bwd(
+        batch, seqlen, dim, _DTYPES[dtype], px, pr, pi, pz, _strides((sx, sr, si, sz), dim), *_bytes_at(saved, "saved"),
+        _at(lam, "lam", f32, per_channel), _at(r_bias, "r_bias", f32, per_channel),
+        _at(i_bias, "i_bias", f32, per_channel), decay_scale, _at(initial_state, "initial_state", f32, per_seq), poff, nseq,
+        *_bytes_at(checkpoints, "checkpoints"), _at(dy, "dy", dtype, shape),
+        _at(dlast_state, "dlast_state", f32, per_seq), grads[0][0], grads[1][0], grads[2][0], grads[3][0],
+        _strides([g[1] for g in grads], dim), _at(out["dlam"], "dlam", f32, per_channel),
+        _at(out.get("dr_bias"), "dr_bias", f32, per_channel), _at(out.get("di_bias"), "di_bias", f32, per_channel),
+        _at(out.get("dinitial_state"), "dinitial_state", f32, per_seq), pw, nw, _stream_at(dy))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -625,17 +644,21 @@ def sscan_glr_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: tor
     if x.dtype not in _DTYPES:
         raise ValueError("x must be float32 or bfloat16")
     batch, dim = shape = x.shape
-    strides = [_rows(x, "x", x.dtype, shape), _rows(r, "r", x.dtype, shape), _rows(i, "i", x.dtype, shape),
-               dim if z is None else _rows(z, "z", x.dtype, shape)]
-    _glr_params(dim, x.device, lam, r_bias, i_bias, None, batch)
+    dtype = x.dtype
+    px, sx = _rows(x, "x", dtype, shape)
+    pr, sr = _rows(r, "r", dtype, shape)
+    pi, si = _rows(i, "i", dtype, shape)
+    pz, sz = (None, dim) if z is None else _rows(z, "z", dtype, shape)
     if state.dim() != 2:
         raise ValueError("state must be [slots, dim]")
-    _dev(state, "state", torch.float32, (state.shape[0], dim))
-    for t, name in ((slots, "slots"), (slots_out, "slots_out")):
-        if t is not None:
-            _dev(t, name, torch.int32, (batch,))
-    y = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else _dev(out, "out", x.dtype, shape)
-    _check(_lib.sscan_glr_step(batch, dim, _DTYPES[x.dtype], _ptr(state), state.shape[0], _ptr(slots), _ptr(slots_out),
-                               _ptr(x), _ptr(r), _ptr(i), _ptr(z), _strides(strides, dim), _ptr(lam), _ptr(r_bias),
-                               _ptr(i_bias), decay_scale, _ptr(y), _stream(x.device)))
+    pool = state.shape[0]
+    y = torch.empty(shape, dtype=dtype, device=x.device) if out is None else out
+    f32, per_channel, per_row = torch.float32, (dim,), (batch,)
+    rc = _lib.sscan_glr_step(
+        batch, dim, _DTYPES[dtype], _at(state, "state", f32, (pool, dim)), pool, _at(slots, "slots", torch.int32, per_row),
+        _at(slots_out, "slots_out", torch.int32, per_row), px, pr, pi, pz, _strides((sx, sr, si, sz), dim),
+        _at(lam, "lam", f32, per_channel), _at(r_bias, "r_bias", f32, per_channel),
+        _at(i_bias, "i_bias", f32, per_channel), decay_scale, _at(y, "out", dtype, shape), _stream_at(x))
+    if rc:
+        _check(rc)
     return y

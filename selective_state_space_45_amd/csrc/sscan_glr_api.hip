@@ -52,6 +52,11 @@ int check_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
   return SSCAN_OK;
 }
 
+// One lane each for `n` items, 256 a workgroup, counts its workgroups in 31 bits.
+int check_lanes(int64_t n) {
+  return n / 256 < INT32_MAX ? int(SSCAN_OK) : fail(SSCAN_ERR_INVALID_ARG, "batch*seqlen*dim too large");
+}
+
 // A token tensor: rows of dim elements, `stride` elements apart.
 struct Tok {
   const char* name;
@@ -276,6 +281,7 @@ int glr_step(int64_t batch, int64_t dim, int dtype, float* state, int64_t num_sl
              const int64_t* strides, const float* lam, const float* r_bias, const float* i_bias, float decay_scale,
              void* y, void* stream) {
   SSCAN_TRY(check_sizes(batch, 1, dim, dtype));
+  SSCAN_TRY(check_lanes(batch * dim));
   if (num_slots < 0 || !fits(num_slots, dim, 1))
     return fail(SSCAN_ERR_INVALID_ARG, "num_slots %lld negative or too large", (long long)num_slots);
   if (!slots && batch > num_slots)
@@ -321,6 +327,7 @@ int act8_check(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const Tok&
   SSCAN_TRY(check_sizes(batch, seqlen, dim, dtype));
   const int64_t rows = batch * seqlen;
   if (rows == 0 || dim == 0) return SSCAN_OK;
+  SSCAN_TRY(check_lanes(batch * ((seqlen + SSCAN_ACT8_GROUP - 1) / SSCAN_ACT8_GROUP) * dim));
   const size_t es = dtype == SSCAN_BF16 ? 2 : 4;
   if (!x.p) return fail(SSCAN_ERR_INVALID_ARG, "null required pointer (x)");
   SSCAN_TRY(check_tok(x, rows, dim, es));
