@@ -45,7 +45,9 @@ int check_sizes(int64_t batch, int64_t seqlen, int64_t dim, int dtype) {
 }
 
 // The recurrence's launches count their tiles (64 tokens, at least 64 channels) in 31 bits.
+// A channel's byte offset in a row is held in 32.
 int check_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
+  if (dim > (1 << 28)) return fail(SSCAN_ERR_INVALID_ARG, "dim too large");
   const int64_t blocks = (seqlen + SSCAN_GLR_BLOCK - 1) / SSCAN_GLR_BLOCK, sets = (dim + 63) / 64;
   if (batch > 0 && blocks > 0 && sets > 0 && (blocks > INT32_MAX / sets || batch > INT32_MAX / (blocks * sets)))
     return fail(SSCAN_ERR_INVALID_ARG, "batch*seqlen*dim too large");

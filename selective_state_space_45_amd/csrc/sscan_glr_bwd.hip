@@ -12,7 +12,7 @@ struct GlrAct {
   int64_t stride;
   __device__ GlrAct(const void* from, int64_t s, const GlrBwdParams&, int, int64_t, uint32_t)
       : p(static_cast<const Tin*>(from)), stride(s) {}
-  __device__ __forceinline__ reg load(int64_t t, uint32_t c) const { return TokVec<Tin, V>::load(p + t * stride + c); }
+  __device__ __forceinline__ reg load(int64_t t, uint32_t c) const { return TokVec<Tin, V>::load(p + t * stride, c * sizeof(Tin)); }
   __device__ __forceinline__ float get(reg r, int v) const { return TokVec<Tin, V>::get(r, v); }
 };
 template <typename Tin, int V>
@@ -30,7 +30,7 @@ struct GlrAct<Tin, V, true> {
     for (int v = 0; v < V; ++v) scale[v] = act8_value(1, f >> (8 * v) & 255u);
   }
   __device__ __forceinline__ reg load(int64_t t, uint32_t c) const {
-    return *reinterpret_cast<const word*>(p + t * stride + c);
+    return row_load<word>(p + t * stride, c);
   }
   __device__ __forceinline__ float get(reg r, int v) const {
     return static_cast<float>(static_cast<int8_t>(r >> (8 * v))) * scale[v];
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
   const int64_t D = p.dim, L = p.L;
   const int64_t cl = c0 + lane * V;
   const bool mine = cl < D;
-  const uint32_t c = static_cast<uint32_t>(mine ? cl : D - V);
+  const uint32_t c = static_cast<uint32_t>(mine ? cl : D - V), cb = c * sizeof(Tin);
   const int64_t t0 = static_cast<int64_t>(tile) * kGlrTile + w * K;
   const int rows = static_cast<int>(L - t0 < 0 ? 0 : (L - t0 < K ? L - t0 : K));
 
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
     rr[k] = ar.load(t, c);
     ri[k] = ai.load(t, c);
     rx[k] = ax.load(t, c);
-    rg[k] = Tok::load(static_cast<const Tin*>(p.dy) + t * D + c);
+    rg[k] = Tok::load(static_cast<const Tin*>(p.dy) + t * D, cb);
     if (GATE) rz[k] = az.load(t, c);
   }
   GlrSpan sp;
@@ -204,10 +204,10 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_bwd_kernel(GlrBwdParams p,
   Tin* dzp = GATE ? static_cast<Tin*>(p.dz) + row0 * p.gz : nullptr;
   auto put = [&](int k, const float* gx, const float* gr, const float* gi, const float* gz) __attribute__((always_inline)) {
     if (!mine) return;
-    Tok::store(dxp + k * p.gx + c, gx);
-    Tok::store(drp + k * p.gr + c, gr);
-    Tok::store(dip + k * p.gi + c, gi);
-    if (GATE) Tok::store(dzp + k * p.gz + c, gz);
+    Tok::store(dxp + k * p.gx, cb, gx);
+    Tok::store(drp + k * p.gr, cb, gr);
+    Tok::store(dip + k * p.gi, cb, gi);
+    if (GATE) Tok::store(dzp + k * p.gz, cb, gz);
   };
   auto token = [&](int k) __attribute__((always_inline)) {
     float gx[V], gr[V], gi[V], gz[V];

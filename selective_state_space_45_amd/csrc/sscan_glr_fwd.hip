@@ -20,25 +20,25 @@ __device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg* raw
     fields |= (top >> 23) << (8 * v);
   }
   if (!mine) return;
-  if (V == 2) *reinterpret_cast<uint16_t*>(exps + c) = static_cast<uint16_t>(fields);
-  else exps[c] = static_cast<uint8_t>(fields);
+  if (V == 2) row_store<uint16_t>(exps, c, static_cast<uint16_t>(fields));
+  else row_store<uint8_t>(exps, c, static_cast<uint8_t>(fields));
 #pragma unroll
   for (int k = 0; k < kActGroup; ++k) {
-    if (!FULL && k >= rows) break;
     uint32_t both = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int q = FULL || k < valid ? act8_code(TokVec<Tin, V>::get(raw[k], v), shift[v]) : 0;
       both |= (static_cast<uint32_t>(q) & 255u) << (8 * v);
     }
-    int8_t* at = codes + k * dim;
-    if (V == 2) *reinterpret_cast<uint16_t*>(at + c) = static_cast<uint16_t>(both);
-    else at[c] = static_cast<int8_t>(both);
+    if (FULL || k < rows) {
+      if (V == 2) row_store<uint16_t>(codes + k * dim, c, static_cast<uint16_t>(both));
+      else row_store<uint8_t>(codes + k * dim, c, static_cast<uint8_t>(both));
+    }
   }
 }
 
 template <typename Tin, int V, bool PACKED, bool GATE, bool SAVE>
-__global__ __launch_bounds__(64 * kGlrWaves, V == 2 && sizeof(Tin) == 4 && GATE ? 3 : 4) void glr_fwd_kernel(GlrFwdParams p, GlrChainWords words, int ntiles,
+__global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4) ? 3 : 4) void glr_fwd_kernel(GlrFwdParams p, GlrChainWords words, int ntiles,
                                                                  int nct) {
   typedef TokVec<Tin, V> Tok;
   constexpr int K = kActGroup, W = kGlrWaves;
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && sizeof(Tin) == 4 && GATE 
   // lanes past the last channel work on the last ones and store nothing
   const int64_t cl = c0 + lane * V;
   const bool mine = cl < D;
-  const uint32_t c = static_cast<uint32_t>(mine ? cl : D - V);
+  const uint32_t c = static_cast<uint32_t>(mine ? cl : D - V), cb = c * sizeof(Tin);
   const int64_t t0 = static_cast<int64_t>(tile) * kGlrTile + w * K;
   const int rows = static_cast<int>(L - t0 < 0 ? 0 : (L - t0 < K ? L - t0 : K));
 
@@ -68,10 +68,10 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && sizeof(Tin) == 4 && GATE 
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int64_t t = b * L + (t0 + k < L ? t0 + k : L - 1);
-    rx[k] = Tok::load(static_cast<const Tin*>(p.x) + t * p.sx + c);
-    rr[k] = Tok::load(static_cast<const Tin*>(p.r) + t * p.sr + c);
-    ri[k] = Tok::load(static_cast<const Tin*>(p.i) + t * p.si + c);
-    if (GATE) rz[k] = Tok::load(static_cast<const Tin*>(p.z) + t * p.sz + c);
+    rx[k] = Tok::load(static_cast<const Tin*>(p.x) + t * p.sx, cb);
+    rr[k] = Tok::load(static_cast<const Tin*>(p.r) + t * p.sr, cb);
+    ri[k] = Tok::load(static_cast<const Tin*>(p.i) + t * p.si, cb);
+    if (GATE) rz[k] = Tok::load(static_cast<const Tin*>(p.z) + t * p.sz, cb);
   }
   GlrSpan sp;
   sp.valid = rows;
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && sizeof(Tin) == 4 && GATE 
       y[v] = GATE ? h[v] * silu(Tok::get(rz[k], v)) : h[v];
       if (PACKED && k >= sp.valid) y[v] = 0.f;
     }
-    if (mine) Tok::store(yrow + k * D + c, y);
+    if (mine) Tok::store(yrow + k * D, cb, y);
     if (PACKED && (sp.ends >> k & 1) && p.h_last && mine) {
       float* hl = p.h_last + static_cast<int64_t>(sp.seq_of(k)) * D + c;
 #pragma unroll

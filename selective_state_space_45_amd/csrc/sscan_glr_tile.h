@@ -18,41 +18,64 @@ namespace sscan {
 constexpr int kGlrWaves = kGlrBlock / kActGroup;   // waves of a tile, 16 tokens each
 constexpr int kGlrTile = kGlrBlock;                // tokens of a tile: the spacing of saved states
 
-// V channels of one token: loaded and stored as one word per lane.
+// An element `at` bytes into a row that is the same for the whole wave: the
+// row's address in scalar registers and the lane's 32-bit offset are added in the load
+// itself.  The empty asm keeps the compiler from adding the offset to a common base
+// first, which leaves a 64-bit vector addition to every load.
+template <typename T>
+using GlobalPtr = __attribute__((address_space(1))) T*;
+template <typename T>
+__device__ __forceinline__ T row_load(const void* row, uint32_t at) {
+  uintptr_t r = reinterpret_cast<uintptr_t>(row);
+  asm("" : "+s"(r));
+  return __builtin_nontemporal_load(reinterpret_cast<GlobalPtr<const T>>(r + at));
+}
+template <typename T>
+__device__ __forceinline__ void row_store(void* row, uint32_t at, T v) {
+  uintptr_t r = reinterpret_cast<uintptr_t>(row);
+  asm("" : "+s"(r));
+  __builtin_nontemporal_store(v, reinterpret_cast<GlobalPtr<T>>(r + at));
+}
+
+// V channels of one token: loaded and stored as one word per lane, `at` bytes into a row.
 template <typename Tin, int V>
 struct TokVec;
 
 template <>
 struct TokVec<bf16_t, 1> {
   typedef uint32_t reg;
-  static __device__ __forceinline__ reg load(const bf16_t* p) { return *p; }
+  static __device__ __forceinline__ reg load(const bf16_t* row, uint32_t at) { return row_load<bf16_t>(row, at); }
   static __device__ __forceinline__ float get(reg r, int) { return __uint_as_float(r << 16); }
-  static __device__ __forceinline__ void store(bf16_t* p, const float* v) { store_val(p, v[0]); }
+  static __device__ __forceinline__ void store(bf16_t* row, uint32_t at, const float* v) {
+    row_store<bf16_t>(row, at, __builtin_bit_cast(bf16_t, static_cast<__bf16>(v[0])));
+  }
 };
 template <>
 struct TokVec<bf16_t, 2> {
   typedef uint32_t reg;
-  static __device__ __forceinline__ reg load(const bf16_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+  static __device__ __forceinline__ reg load(const bf16_t* row, uint32_t at) { return row_load<uint32_t>(row, at); }
   static __device__ __forceinline__ float get(reg r, int v) { return __uint_as_float(v ? r & 0xffff0000u : r << 16); }
-  static __device__ __forceinline__ void store(bf16_t* p, const float* v) {
+  static __device__ __forceinline__ void store(bf16_t* row, uint32_t at, const float* v) {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
     typedef float f2 __attribute__((ext_vector_type(2)));
-    *reinterpret_cast<b2*>(p) = __builtin_convertvector((f2{v[0], v[1]}), b2);
+    row_store<uint32_t>(row, at, __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[0], v[1]}), b2)));
   }
 };
 template <>
 struct TokVec<float, 1> {
   typedef float reg;
-  static __device__ __forceinline__ reg load(const float* p) { return *p; }
+  static __device__ __forceinline__ reg load(const float* row, uint32_t at) { return row_load<float>(row, at); }
   static __device__ __forceinline__ float get(reg r, int) { return r; }
-  static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
+  static __device__ __forceinline__ void store(float* row, uint32_t at, const float* v) { row_store<float>(row, at, v[0]); }
 };
 template <>
 struct TokVec<float, 2> {
   typedef float reg __attribute__((ext_vector_type(2)));
-  static __device__ __forceinline__ reg load(const float* p) { return *reinterpret_cast<const reg*>(p); }
+  static __device__ __forceinline__ reg load(const float* row, uint32_t at) { return row_load<reg>(row, at); }
   static __device__ __forceinline__ float get(reg r, int v) { return v ? r.y : r.x; }
-  static __device__ __forceinline__ void store(float* p, const float* v) { *reinterpret_cast<reg*>(p) = reg{v[0], v[1]}; }
+  static __device__ __forceinline__ void store(float* row, uint32_t at, const float* v) {
+    row_store<reg>(row, at, reg{v[0], v[1]});
+  }
 };
 
 // The sequences that a wave's 16 tokens t0 .. t0 + 15 belong to (packed requests).
