@@ -101,6 +101,8 @@ inline size_t act8_total(int64_t batch, int64_t L, int64_t dim) {
 // sigmoid(v) = 1 / (1 + e^-v).  e^-v overflows to infinity for v below -88, whose
 // reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid(float v) { return hw_rcp(1.f + hw_exp2(-v * kLog2e)); }
+// sigmoid(v + bias) given nb = -bias log2(e).
+__device__ __forceinline__ float gate(float v, float nb) { return hw_rcp(1.f + hw_exp2(fmaf(v, -kLog2e, nb))); }
 
 // The derivative s (1 - s) of a sigmoid that is s: off by at most 2^-24 (of its largest
 // value, 1/4) where s is close to 1.
@@ -123,37 +125,31 @@ __device__ __forceinline__ float softplus_acc(float v) {
   return (v > 0.f ? v : (v <= 0.f ? 0.f : v)) + 2.f * s * p;
 }
 
-// a = e^-q and v = 1 - a^2 for q = decay rate x gate >= 0.  1 - a^2 loses its leading
-// digits for a near 1, so for q < 1/2 it is 2 a sinh(q) with sinh by its series through
-// q^7 (the next term is below 1.1e-8 of it there); elsewhere a^2 <= e^-1 and the
-// difference is exact enough.
-__device__ __forceinline__ float decay_of(float q, float& one_minus_a2) {
-  const float a = hw_exp2(-q * kLog2e);
-  const float q2 = q * q;
-  float p = fmaf(q2, 1.f / 5040.f, 1.f / 120.f);
-  p = fmaf(q2, p, 1.f / 6.f);
-  p = fmaf(q2, p, 1.f);
-  const float near1 = (2.f * a) * (q * p);
+// a = e^-q and 1 - a^2 for q >= 0, given q log2(e).  1 - a^2 loses its leading digits for
+// a near 1, so for q < 1/4 it is 2 a sinh(q) with sinh by its series through q^5 (the next
+// term is below 5e-8 of it there); elsewhere a^2 < 0.61 and the difference is exact enough.
+__device__ __forceinline__ float decay_of(float q2, float& one_minus_a2) {
+  constexpr float c1 = 2.f * kLn2, c3 = c1 * kLn2 * kLn2 / 6.f, c5 = c3 * kLn2 * kLn2 / 20.f;
+  const float a = hw_exp2(-q2);
+  const float s = q2 * q2;
+  const float near1 = a * (q2 * fmaf(s, fmaf(s, c5, c3), c1));
   const float far = fmaf(-a, a, 1.f);
-  one_minus_a2 = q < 0.5f ? near1 : far;
+  one_minus_a2 = q2 < 0.25f * kLog2e ? near1 : far;
   return a;
 }
 
 __device__ __forceinline__ float hw_sqrt(float v) { return __builtin_amdgcn_sqrtf(v); }
-
-// 1 / m for m = sqrt(1 - a^2), and 0 below 1e-18, where 1 - a^2 is about to leave the
-// normal numbers: m is that small only for decay rates below 1e-36, whose terms with
-// 1 / m, each times the rate, are below 1e-18 of the others.
-__device__ __forceinline__ float rcp_or_0(float m) { return m < 1e-18f ? 0.f : hw_rcp(m); }
 
 // 8-bit codes.  `field` is the float32 exponent field (0 .. 255) of the group's largest
 // magnitude; 255 marks a group with an infinity or NaN.  Scaling by powers of two is
 // exact (ldexp reaches every exponent a field asks for), so the only rounding is to the
 // whole number.
 __device__ __forceinline__ int act8_shift(uint32_t field) { return (field < 1u ? 1 : static_cast<int>(field)) - 133; }
-__device__ __forceinline__ int act8_code(float v, int shift) {
-  const float c = rintf(__builtin_amdgcn_ldexpf(v, -shift));
-  return static_cast<int>(fminf(fmaxf(c, -127.f), 127.f));
+// A code, in the low byte.  Adding 1.5 x 2^23 rounds to the whole number (ties to even)
+// and leaves it in the low bits.
+__device__ __forceinline__ uint32_t act8_code(float v, int shift) {
+  constexpr float k = 12582912.f;
+  return __float_as_uint(__builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(v, -shift) + k, k - 127.f, k + 127.f));
 }
 __device__ __forceinline__ float act8_value(int code, uint32_t field) {
   const float v = __builtin_amdgcn_ldexpf(static_cast<float>(code), act8_shift(field));

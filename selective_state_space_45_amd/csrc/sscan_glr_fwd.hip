@@ -3,43 +3,44 @@
 
 namespace sscan {
 
-// Exponent field and codes of a wave's 16 tokens of one tensor, for V channels of a lane.
+// Exponent fields and codes of a wave's 16 tokens of one tensor, for V channels of a lane.
 // FULL: 16 tokens; otherwise the first `valid` of `rows` count, the others as zeros.
-template <typename Tin, int V, bool FULL>
-__device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg* raw, int valid, int rows, int8_t* codes,
-                                         uint8_t* exps, int64_t dim, uint32_t c, bool mine) {
+template <typename Tin, int V, bool LINES, bool FULL>
+__device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg (&raw)[kActGroup], int valid, int rows,
+                                         int8_t* codes, uint8_t* exps, int64_t dim, uint32_t c, bool mine) {
+  typedef TokVec<Tin, V> Tok;
+  typedef typename std::conditional<V == 2, uint16_t, uint8_t>::type word;
+  typename Tok::reg top = {};
+#pragma unroll
+  for (int k = 0; k < kActGroup; ++k)
+    if (FULL || k < valid) top = Tok::top(top, raw[k]);
   int shift[V];
   uint32_t fields = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < kActGroup; ++k)
-      if (FULL || k < valid) top = act8_top(top, TokVec<Tin, V>::get(raw[k], v));
-    shift[v] = act8_shift(top >> 23);
-    fields |= (top >> 23) << (8 * v);
+    const uint32_t f = Tok::field(top, v);
+    shift[v] = act8_shift(f);
+    fields |= f << (8 * v);
   }
   if (!mine) return;
-  if (V == 2) row_store<uint16_t>(exps, c, static_cast<uint16_t>(fields));
-  else row_store<uint8_t>(exps, c, static_cast<uint8_t>(fields));
+  row_store<word, LINES>(exps, c, static_cast<word>(fields));
 #pragma unroll
   for (int k = 0; k < kActGroup; ++k) {
-    uint32_t both = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int q = FULL || k < valid ? act8_code(TokVec<Tin, V>::get(raw[k], v), shift[v]) : 0;
-      both |= (static_cast<uint32_t>(q) & 255u) << (8 * v);
-    }
-    if (FULL || k < rows) {
-      if (V == 2) row_store<uint16_t>(codes + k * dim, c, static_cast<uint16_t>(both));
-      else row_store<uint8_t>(codes + k * dim, c, static_cast<uint8_t>(both));
-    }
+    uint32_t q = act8_code(Tok::get(raw[k], 0), shift[0]);
+    if (V == 2) q = __builtin_amdgcn_perm(act8_code(Tok::get(raw[k], V - 1), shift[V - 1]), q, 0x0c0c0400u);
+    if (!FULL && k >= valid) q = 0;
+    if (FULL || k < rows) row_store<word, LINES>(codes, c, static_cast<word>(q));
+    codes += dim;
   }
 }
 
-template <typename Tin, int V, bool PACKED, bool GATE, bool SAVE>
-__global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4) ? 3 : 4) void glr_fwd_kernel(GlrFwdParams p, GlrChainWords words, int ntiles,
-                                                                 int nct) {
+// One tile.  Bound by memory: 8 bytes an element in bf16 (10 with a gate) against about 25
+// vector operations and 6 of the quarter-rate ones.  The map of a wave's 16 tokens needs
+// each of them once, and so does the output, so a and u stay in registers between the two
+// while the state is on its way; four waves a SIMD cover that wait.
+template <typename Tin, int V, bool LINES, bool PACKED, bool GATE, bool SAVE>
+__global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4) ? 3 : 4) void glr_fwd_kernel(
+    GlrFwdParams p, GlrChainWords words, int ntiles, int nct) {
   typedef TokVec<Tin, V> Tok;
   constexpr int K = kActGroup, W = kGlrWaves;
   __shared__ float sA[W][V][64], sB[W][V][64], sH[V][64];
@@ -49,7 +50,8 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
   const uint32_t chain = blockIdx.x % nchains;
   int tile = 0;
   if (ntiles > 1) {
-    if (threadIdx.x == 0) sTile = static_cast<int>(atomicAdd(&words.tickets[static_cast<size_t>(chain) * kGlrTicket], 1u));
+    if (threadIdx.x == 0)
+      sTile = static_cast<int>(atomicAdd(&words.tickets[static_cast<size_t>(chain) * kGlrTicket], 1u));
     __syncthreads();
     tile = __builtin_amdgcn_readfirstlane(sTile);
   }
@@ -63,34 +65,48 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
   const int64_t t0 = static_cast<int64_t>(tile) * kGlrTile + w * K;
   const int rows = static_cast<int>(L - t0 < 0 ? 0 : (L - t0 < K ? L - t0 : K));
 
-  // loads: 16 tokens of each input; tokens past the row's end read the last one
-  typename Tok::reg rx[K], rr[K], ri[K], rz[GATE ? K : 1];
+  // 16 tokens of each input; tokens past the row's end read its last one
+  typename Tok::reg rx[K], rr[K], ri[K], rz[K];
+  {
+    const int64_t t = b * L + (rows ? t0 : L - 1);
+    const Tin* px = static_cast<const Tin*>(p.x) + t * p.sx;
+    const Tin* pr = static_cast<const Tin*>(p.r) + t * p.sr;
+    const Tin* pi = static_cast<const Tin*>(p.i) + t * p.si;
+    const Tin* pz = GATE ? static_cast<const Tin*>(p.z) + t * p.sz : nullptr;
+    auto load = [&](auto full) __attribute__((always_inline)) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int64_t t = b * L + (t0 + k < L ? t0 + k : L - 1);
-    rx[k] = Tok::load(static_cast<const Tin*>(p.x) + t * p.sx, cb);
-    rr[k] = Tok::load(static_cast<const Tin*>(p.r) + t * p.sr, cb);
-    ri[k] = Tok::load(static_cast<const Tin*>(p.i) + t * p.si, cb);
-    if (GATE) rz[k] = Tok::load(static_cast<const Tin*>(p.z) + t * p.sz, cb);
+      for (int k = 0; k < K; ++k) {
+        rx[k] = row_load<typename Tok::word, LINES>(px, cb);
+        rr[k] = row_load<typename Tok::word, LINES>(pr, cb);
+        ri[k] = row_load<typename Tok::word, LINES>(pi, cb);
+        if (GATE) rz[k] = row_load<typename Tok::word, LINES>(pz, cb);
+        if (decltype(full)::value || k + 1 < rows) {
+          px += p.sx, pr += p.sr, pi += p.si;
+          if (GATE) pz += p.sz;
+        }
+      }
+    };
+    if (rows == K) load(std::true_type{});
+    else load(std::false_type{});
   }
   GlrSpan sp;
   sp.valid = rows;
   if (PACKED) sp = glr_span(p.offsets, static_cast<int>(p.num_seqs), t0, L);
 
-  float rate[V], rb[V], ib[V];
+  float rate[V], nrb[V], nib[V];   // times log2(e); the biases negated
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    rate[v] = p.decay_scale * softplus_acc(p.lam[c + v]);
-    rb[v] = p.r_bias ? p.r_bias[c + v] : 0.f;
-    ib[v] = p.i_bias ? p.i_bias[c + v] : 0.f;
+    rate[v] = p.decay_scale * softplus_acc(p.lam[c + v]) * kLog2e;
+    nrb[v] = p.r_bias ? -kLog2e * p.r_bias[c + v] : 0.f;
+    nib[v] = p.i_bias ? -kLog2e * p.i_bias[c + v] : 0.f;
   }
   if (SAVE && rows > 0) {
     const int64_t row0 = b * L + t0, group = b * ((L + K - 1) / K) + t0 / K;
-    auto save = [&](int q, const typename Tok::reg* raw) __attribute__((always_inline)) {
+    auto save = [&](int q, const typename Tok::reg(&raw)[K]) __attribute__((always_inline)) {
       int8_t* codes = p.codes + q * p.saved_stride;
       uint8_t* exps = reinterpret_cast<uint8_t*>(codes) + p.exps_at;
-      if (sp.valid == K) glr_save<Tin, V, true>(raw, K, K, codes + row0 * D, exps + group * D, D, c, mine);
-      else glr_save<Tin, V, false>(raw, sp.valid, rows, codes + row0 * D, exps + group * D, D, c, mine);
+      if (sp.valid == K) glr_save<Tin, V, LINES, true>(raw, K, K, codes + row0 * D, exps + group * D, D, c, mine);
+      else glr_save<Tin, V, LINES, false>(raw, sp.valid, rows, codes + row0 * D, exps + group * D, D, c, mine);
     };
     save(0, rx);
     save(1, rr);
@@ -105,8 +121,8 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float one;
-      a[k][v] = decay_of(rate[v] * sigmoid(Tok::get(rr[k], v) + rb[v]), one);
-      u[k][v] = hw_sqrt(one) * (sigmoid(Tok::get(ri[k], v) + ib[v]) * Tok::get(rx[k], v));
+      a[k][v] = decay_of(rate[v] * gate(Tok::get(rr[k], v), nrb[v]), one);
+      u[k][v] = hw_sqrt(one) * (gate(Tok::get(ri[k], v), nib[v]) * Tok::get(rx[k], v));
     }
   if (sp.valid < K) {   // tokens past the end leave the state alone
 #pragma unroll
@@ -187,7 +203,8 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
       y[v] = GATE ? h[v] * silu(Tok::get(rz[k], v)) : h[v];
       if (PACKED && k >= sp.valid) y[v] = 0.f;
     }
-    if (mine) Tok::store(yrow + k * D, cb, y);
+    if (mine) row_store<typename Tok::word, LINES>(yrow, cb, Tok::put(y));
+    yrow += D;
     if (PACKED && (sp.ends >> k & 1) && p.h_last && mine) {
       float* hl = p.h_last + static_cast<int64_t>(sp.seq_of(k)) * D + c;
 #pragma unroll
@@ -239,41 +256,36 @@ hipError_t launch_glr_empty(const int32_t* offsets, const float* from, float* to
 
 namespace {
 
-template <typename Tin, int V, bool PACKED, bool GATE>
-hipError_t launch_one(const GlrFwdParams& p, const GlrChainLayout& lo, hipStream_t s) {
-  const int nct = static_cast<int>((p.dim + 64 * V - 1) / (64 * V));
+template <typename Tin, int V, bool LINES, bool PACKED, bool GATE>
+void launch_save(const GlrFwdParams& p, const GlrChainLayout& lo, hipStream_t s) {
+  const int nct = static_cast<int>((p.dim + 64 * V - 1) / (64 * V)), nt = static_cast<int>(lo.tiles);
   const dim3 grid(static_cast<unsigned>(lo.chains * lo.tiles)), wg(64 * kGlrWaves);
-  const GlrChainWords words = lo.at(p.workspace);
-  const int nt = static_cast<int>(lo.tiles);
-  if (p.codes) hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, PACKED, GATE, true>), grid, wg, 0, s, p, words, nt, nct);
-  else hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, PACKED, GATE, false>), grid, wg, 0, s, p, words, nt, nct);
-  return hipGetLastError();
+  const GlrChainWords w = lo.at(p.workspace);
+  if (p.codes) hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, LINES, PACKED, GATE, true>), grid, wg, 0, s, p, w, nt, nct);
+  else hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, LINES, PACKED, GATE, false>), grid, wg, 0, s, p, w, nt, nct);
 }
 
-template <typename Tin, int V>
+template <typename Tin, int V, bool LINES>
 hipError_t launch_v(const GlrFwdParams& p, hipStream_t s) {
   const GlrChainLayout lo(p.batch, p.L, p.dim, V);
   if (lo.tiles > 1) {
     const hipError_t e = launch_glr_clear(p.workspace, lo, s);
     if (e != hipSuccess) return e;
   }
-  if (p.offsets) return p.z ? launch_one<Tin, V, true, true>(p, lo, s) : launch_one<Tin, V, true, false>(p, lo, s);
-  return p.z ? launch_one<Tin, V, false, true>(p, lo, s) : launch_one<Tin, V, false, false>(p, lo, s);
+  if (p.offsets) p.z ? launch_save<Tin, V, LINES, true, true>(p, lo, s) : launch_save<Tin, V, LINES, true, false>(p, lo, s);
+  else p.z ? launch_save<Tin, V, LINES, false, true>(p, lo, s) : launch_save<Tin, V, LINES, false, false>(p, lo, s);
+  return hipGetLastError();
 }
 
-// Two channels a lane where every row of every tensor holds whole aligned pairs.
-template <typename Tin>
-bool pairs(const GlrFwdParams& p) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.r) |
-                       reinterpret_cast<uintptr_t>(p.i) | reinterpret_cast<uintptr_t>(p.z) |
-                       reinterpret_cast<uintptr_t>(p.y);
-  const int64_t odd = p.sx | p.sr | p.si | (p.z ? p.sz : 0) | p.dim;
-  return at % (2 * sizeof(Tin)) == 0 && odd % 2 == 0;
-}
-
+// Two channels a lane where every row of every tensor holds whole aligned pairs, and rows
+// past the caches where each starts on a cache line.
 template <typename Tin>
 hipError_t launch_t(const GlrFwdParams& p, hipStream_t s) {
-  return pairs<Tin>(p) ? launch_v<Tin, 2>(p, s) : launch_v<Tin, 1>(p, s);
+  uintptr_t bits = static_cast<uintptr_t>(p.sx | p.sr | p.si | (p.z ? p.sz : 0) | p.dim) * sizeof(Tin);
+  for (const void* q : {p.x, p.r, p.i, p.z, static_cast<const void*>(p.y)}) bits |= reinterpret_cast<uintptr_t>(q);
+  if (p.codes) bits |= static_cast<uintptr_t>(p.dim);   // the codes' rows
+  if (bits % kCacheLine == 0) return launch_v<Tin, 2, true>(p, s);
+  return bits % (2 * sizeof(Tin)) == 0 ? launch_v<Tin, 2, false>(p, s) : launch_v<Tin, 1, false>(p, s);
 }
 
 }  // namespace

@@ -18,11 +18,11 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrStepParams p) {
     return;
   }
   const int64_t to = p.slots_out ? p.slots_out[b] : slot;
-  const float kappa = p.decay_scale * softplus_acc(p.lam[d]);
-  const float rho = sigmoid(to_f32(static_cast<const Tin*>(p.r)[b * p.sr + d]) + (p.r_bias ? p.r_bias[d] : 0.f));
-  const float iota = sigmoid(to_f32(static_cast<const Tin*>(p.i)[b * p.si + d]) + (p.i_bias ? p.i_bias[d] : 0.f));
+  const float rate = p.decay_scale * softplus_acc(p.lam[d]) * kLog2e;
+  const float rho = gate(to_f32(static_cast<const Tin*>(p.r)[b * p.sr + d]), p.r_bias ? -kLog2e * p.r_bias[d] : 0.f);
+  const float iota = gate(to_f32(static_cast<const Tin*>(p.i)[b * p.si + d]), p.i_bias ? -kLog2e * p.i_bias[d] : 0.f);
   float v;
-  const float a = decay_of(kappa * rho, v);
+  const float a = decay_of(rate * rho, v);
   const float h = fmaf(a, p.state[slot * p.dim + d], hw_sqrt(v) * (iota * to_f32(static_cast<const Tin*>(p.x)[b * p.sx + d])));
   if (to >= 0 && to < p.num_slots) p.state[to * p.dim + d] = h;
   store_val(&y[id], p.z ? h * silu(to_f32(static_cast<const Tin*>(p.z)[b * p.sz + d])) : h);

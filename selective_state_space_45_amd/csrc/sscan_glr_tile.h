@@ -16,66 +16,84 @@
 namespace sscan {
 
 constexpr int kGlrWaves = kGlrBlock / kActGroup;   // waves of a tile, 16 tokens each
+constexpr uintptr_t kCacheLine = 128;
 constexpr int kGlrTile = kGlrBlock;                // tokens of a tile: the spacing of saved states
 
-// An element `at` bytes into a row that is the same for the whole wave: the
-// row's address in scalar registers and the lane's 32-bit offset are added in the load
-// itself.  The empty asm keeps the compiler from adding the offset to a common base
-// first, which leaves a 64-bit vector addition to every load.
+// An element `at` bytes into a row that is the same for the whole wave: the row's address
+// in scalar registers and the lane's 32-bit offset are added in the load itself.  The
+// empty asm keeps the compiler from adding the offset to a common base first, which
+// leaves a 64-bit vector addition to every load.  LINES: the wave's rows are whole cache
+// lines; then they pass by the caches, since nothing here reads them again.  Lines that
+// two waves share gain from staying (2 x 2047 x 1535 float32, forward and backward: 0.135
+// ms streamed, 0.120 not; 8 x 4096 x 2048 bf16: 0.376 and 0.397).
 template <typename T>
 using GlobalPtr = __attribute__((address_space(1))) T*;
-template <typename T>
+template <typename T, bool LINES>
 __device__ __forceinline__ T row_load(const void* row, uint32_t at) {
   uintptr_t r = reinterpret_cast<uintptr_t>(row);
   asm("" : "+s"(r));
-  return __builtin_nontemporal_load(reinterpret_cast<GlobalPtr<const T>>(r + at));
+  const GlobalPtr<const T> p = reinterpret_cast<GlobalPtr<const T>>(r + at);
+  return LINES ? __builtin_nontemporal_load(p) : *p;
 }
-template <typename T>
+template <typename T, bool LINES>
 __device__ __forceinline__ void row_store(void* row, uint32_t at, T v) {
   uintptr_t r = reinterpret_cast<uintptr_t>(row);
   asm("" : "+s"(r));
-  __builtin_nontemporal_store(v, reinterpret_cast<GlobalPtr<T>>(r + at));
+  const GlobalPtr<T> p = reinterpret_cast<GlobalPtr<T>>(r + at);
+  if (LINES) __builtin_nontemporal_store(v, p);
+  else *p = v;
 }
 
-// V channels of one token: loaded and stored as one word per lane, `at` bytes into a row.
+// V channels of one token: one word per lane.  top: the word's magnitudes, whose maxima
+// over words give the largest exponents.
 template <typename Tin, int V>
 struct TokVec;
 
 template <>
 struct TokVec<bf16_t, 1> {
   typedef uint32_t reg;
-  static __device__ __forceinline__ reg load(const bf16_t* row, uint32_t at) { return row_load<bf16_t>(row, at); }
+  typedef bf16_t word;
   static __device__ __forceinline__ float get(reg r, int) { return __uint_as_float(r << 16); }
-  static __device__ __forceinline__ void store(bf16_t* row, uint32_t at, const float* v) {
-    row_store<bf16_t>(row, at, __builtin_bit_cast(bf16_t, static_cast<__bf16>(v[0])));
-  }
+  static __device__ __forceinline__ word put(const float* v) { return __builtin_bit_cast(bf16_t, static_cast<__bf16>(v[0])); }
+  static __device__ __forceinline__ reg top(reg t, reg r) { return (r & 0x7fffu) > t ? r & 0x7fffu : t; }
+  static __device__ __forceinline__ uint32_t field(reg t, int) { return t >> 7; }
 };
 template <>
 struct TokVec<bf16_t, 2> {
   typedef uint32_t reg;
-  static __device__ __forceinline__ reg load(const bf16_t* row, uint32_t at) { return row_load<uint32_t>(row, at); }
+  typedef uint32_t word;
   static __device__ __forceinline__ float get(reg r, int v) { return __uint_as_float(v ? r & 0xffff0000u : r << 16); }
-  static __device__ __forceinline__ void store(bf16_t* row, uint32_t at, const float* v) {
+  static __device__ __forceinline__ word put(const float* v) {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
     typedef float f2 __attribute__((ext_vector_type(2)));
-    row_store<uint32_t>(row, at, __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[0], v[1]}), b2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{v[0], v[1]}), b2));
   }
+  static __device__ __forceinline__ reg top(reg t, reg r) {
+    typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u2, t),
+                                                                  __builtin_bit_cast(u2, r & 0x7fff7fffu)));
+  }
+  static __device__ __forceinline__ uint32_t field(reg t, int v) { return v ? t >> 23 : (t >> 7) & 255u; }
 };
 template <>
 struct TokVec<float, 1> {
   typedef float reg;
-  static __device__ __forceinline__ reg load(const float* row, uint32_t at) { return row_load<float>(row, at); }
+  typedef float word;
   static __device__ __forceinline__ float get(reg r, int) { return r; }
-  static __device__ __forceinline__ void store(float* row, uint32_t at, const float* v) { row_store<float>(row, at, v[0]); }
+  static __device__ __forceinline__ word put(const float* v) { return v[0]; }
+  static __device__ __forceinline__ reg top(reg t, reg r) { return __uint_as_float(act8_top(__float_as_uint(t), r)); }
+  static __device__ __forceinline__ uint32_t field(reg t, int) { return __float_as_uint(t) >> 23; }
 };
 template <>
 struct TokVec<float, 2> {
   typedef float reg __attribute__((ext_vector_type(2)));
-  static __device__ __forceinline__ reg load(const float* row, uint32_t at) { return row_load<reg>(row, at); }
+  typedef reg word;
   static __device__ __forceinline__ float get(reg r, int v) { return v ? r.y : r.x; }
-  static __device__ __forceinline__ void store(float* row, uint32_t at, const float* v) {
-    row_store<reg>(row, at, reg{v[0], v[1]});
+  static __device__ __forceinline__ word put(const float* v) { return reg{v[0], v[1]}; }
+  static __device__ __forceinline__ reg top(reg t, reg r) {
+    return reg{TokVec<float, 1>::top(t.x, r.x), TokVec<float, 1>::top(t.y, r.y)};
   }
+  static __device__ __forceinline__ uint32_t field(reg t, int v) { return __float_as_uint(v ? t.y : t.x) >> 23; }
 };
 
 // The sequences that a wave's 16 tokens t0 .. t0 + 15 belong to (packed requests).
