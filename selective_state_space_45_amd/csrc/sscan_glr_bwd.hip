@@ -13,7 +13,7 @@ struct GlrAct {
   int64_t stride;
   __device__ GlrAct(const void* from, int64_t s, const GlrBwdParams&, int, int64_t t, int64_t, uint32_t)
       : row(static_cast<const Tin*>(from) + t * s), stride(s) {}
-  __device__ __forceinline__ reg load(uint32_t c) const { return row_load<typename Tok::word, LINES>(row, c * sizeof(Tin)); }
+  __device__ __forceinline__ reg load(uint32_t at) const { return row_load<typename Tok::word, LINES>(row, at); }
   __device__ __forceinline__ float get(reg r) const { return Tok::get(r, 0); }
 };
 template <typename Tin, bool LINES>
@@ -28,8 +28,30 @@ struct GlrAct<Tin, LINES, true> {
     stride = q.dim;
     scale = act8_value(1, row_load<uint8_t, false>(reinterpret_cast<const uint8_t*>(codes) + q.exps_at + group * q.dim, c));
   }
-  __device__ __forceinline__ reg load(uint32_t c) const { return row_load<int8_t, LINES>(row, c); }
+  __device__ __forceinline__ reg load(uint32_t at) const { return row_load<int8_t, LINES>(row, at); }
   __device__ __forceinline__ float get(reg r) const { return static_cast<float>(r) * scale; }
+};
+
+// x and dy of a token, held over the wait for the gradient: in bf16 they share a word.
+template <typename Tin, typename Act>
+struct GlrPair {
+  typename Act::reg x;
+  typename TokVec<Tin, 1>::reg dy;
+  __device__ __forceinline__ void set(typename Act::reg rx, typename TokVec<Tin, 1>::reg rg) { x = rx, dy = rg; }
+  __device__ __forceinline__ void forget() { asm("" : "+v"(x)); }
+  __device__ __forceinline__ float get_x(const Act& act) const { return act.get(x); }
+  __device__ __forceinline__ float get_dy() const { return dy; }
+};
+template <typename Act>
+struct GlrPair<bf16_t, Act> {
+  uint32_t both;
+  __device__ __forceinline__ void set(typename Act::reg rx, uint32_t rg) {
+    both = __builtin_amdgcn_perm(rg, static_cast<uint32_t>(rx), 0x05040100u);
+    forget();   // that it was two registers
+  }
+  __device__ __forceinline__ void forget() { asm("" : "+v"(both)); }
+  __device__ __forceinline__ float get_x(const Act& act) const { return act.get(static_cast<int16_t>(both)); }
+  __device__ __forceinline__ float get_dy() const { return __uint_as_float(both & 0xffff0000u); }
 };
 
 // One tile, the chain running from the last tokens to the first.  The states inside the
@@ -38,13 +60,13 @@ struct GlrAct<Tin, LINES, true> {
 // map with the same factor a, so one exchange through shared memory serves both.
 //
 // 14 bytes an element in bf16 against about 50 vector operations and 7 of the
-// quarter-rate ones: both near the time of the other.  One channel a lane: the two gates,
-// a, sqrt(1 - a^2) and the state before each of 16 tokens stay in registers over the wait
-// for the gradient.  With two channels a lane they do not fit three waves a SIMD, and
+// quarter-rate ones: both near the time of the other.  One channel a lane: what the
+// gradients need of each of 16 tokens but the gradient that arrives is formed before the
+// wait for it and stays in registers.  With two channels a lane they do not fit three waves a SIMD, and
 // formed again after the wait they cost more than the second channel saves (8 x 4096 x
 // 2048 bf16, forward and backward: 0.442 ms, and 0.397 in this form).
 template <typename Tin, bool LINES, bool PACKED, bool GATE, bool SAVED>
-__global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
+__global__ __launch_bounds__(64 * kGlrWaves, GATE || sizeof(Tin) == 4 ? 3 : 4) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
                                                                  int ntiles, int nct) {
   typedef TokVec<Tin, 1> Tok;
   typedef GlrAct<Tin, LINES, SAVED> Act;
@@ -68,8 +90,8 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   const int64_t cl = static_cast<int64_t>(chain % nct) * 64 + lane;
   const bool mine = cl < D;
   const uint32_t c = static_cast<uint32_t>(mine ? cl : D - 1), cb = c * sizeof(Tin);
-  const int64_t t0 = static_cast<int64_t>(tile) * kGlrTile + w * K;
-  const int rows = static_cast<int>(L - t0 < 0 ? 0 : (L - t0 < K ? L - t0 : K));
+  const int L32 = static_cast<int>(L), t0 = tile * kGlrTile + w * K;
+  const int rows = L32 - t0 < 0 ? 0 : (L32 - t0 < K ? L32 - t0 : K);
 
   // 16 tokens of each input; tokens past the row's end read its last one
   const int64_t ngrp = (L + K - 1) / K;
@@ -81,25 +103,26 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   {
     const Tin* pg = static_cast<const Tin*>(p.dy) + tl * D;
     auto load = [&](auto full) __attribute__((always_inline)) {
+      const uint32_t at = here(cb), act_at = here(SAVED ? c : cb);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        rr[k] = ar.load(c);
-        ri[k] = ai.load(c);
-        rx[k] = ax.load(c);
-        rg[k] = row_load<typename Tok::word, LINES>(pg, cb);
-        if (GATE) rz[k] = az.load(c);
-        if (decltype(full)::value || k + 1 < rows) {
-          ar.row += ar.stride, ai.row += ai.stride, ax.row += ax.stride, pg += D;
-          if (GATE) az.row += az.stride;
-        }
+        rr[k] = ar.load(act_at);
+        ri[k] = ai.load(act_at);
+        rx[k] = ax.load(act_at);
+        rg[k] = row_load<typename Tok::word, LINES>(pg, at);
+        if (GATE) rz[k] = az.load(act_at);
+        const int64_t more = decltype(full)::value || k + 1 < rows ? 1 : 0;
+        ar.row += more * ar.stride, ai.row += more * ai.stride, ax.row += more * ax.stride, pg += more * D;
+        if (GATE) az.row += more * az.stride;
       }
+      apart<decltype(full)::value>();
     };
     if (rows == K) load(std::true_type{});
     else load(std::false_type{});
   }
   GlrSpan sp;
   sp.valid = rows;
-  if (PACKED) sp = glr_span(p.offsets, static_cast<int>(p.num_seqs), t0, L);
+  if (PACKED) sp = glr_span(p.offsets, static_cast<int>(p.num_seqs), t0, L32);
 
   const float rate = p.decay_scale * softplus_acc(p.lam[c]), rate2 = rate * kLog2e;
   const float nrb = p.r_bias ? -kLog2e * p.r_bias[c] : 0.f, nib = p.i_bias ? -kLog2e * p.i_bias[c] : 0.f;
@@ -108,7 +131,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   // m = sqrt(1 - a^2) stays above 1e-18, for its reciprocal: it is smaller only at decay
   // rates below 1e-36, whose terms with 1 / m, each times the rate, are below 1e-18 of
   // the others.
-  float a[K], m[K], rho[K], iota[K], before[K];
+  float a[K], m[K], rho[K], iota[K], part_a[K], state[GATE ? K : 1];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     float one;
@@ -116,8 +139,12 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
     iota[k] = gate(ai.get(ri[k]), nib);
     a[k] = decay_of(rate2 * rho[k], one);
     m[k] = hw_sqrt(fmaxf(one, 1e-36f));
+    if (k % 4 == 3) __builtin_amdgcn_sched_barrier(0);
   }
-  auto input = [&](int k) __attribute__((always_inline)) { return iota[k] * ax.get(rx[k]); };
+  GlrPair<Tin, Act> xg[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) xg[k].set(rx[k], rg[k]);
+  auto input = [&](int k) __attribute__((always_inline)) { return iota[k] * xg[k].get_x(ax); };
   auto state0 = [&](int k) __attribute__((always_inline)) {
     return p.h0 ? p.h0[static_cast<int64_t>(sp.seq_of(k)) * D + c] : 0.f;
   };
@@ -133,7 +160,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
     };
     auto back = [&](int k) __attribute__((always_inline)) {
       if (PACKED && (sp.ends >> k & 1)) G = last_grad(k);
-      const float dy = Tok::get(rg[k], 0);
+      const float dy = xg[k].get_dy();
       G = a[k] * (G + (GATE ? dy * silu(az.get(rz[k])) : dy));
       if (PACKED && (sp.starts >> k & 1)) G = 0.f;
     };
@@ -142,6 +169,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
       for (int k = 0; k < K; ++k) ahead(k);
 #pragma unroll
       for (int k = K - 1; k >= 0; --k) back(k);
+      apart<true>();
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -149,10 +177,17 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
 #pragma unroll
       for (int k = K - 1; k >= 0; --k)
         if (k < sp.valid) back(k);
+      apart<false>();
     }
     sA[w][lane] = A, sB[w][lane] = B, sG[w][lane] = G;
   }
   if (PACKED && lane == 0) sReset[w] = sp.starts != 0;
+  // products of these are formed again below: kept, they would take 32 registers more
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    asm("" : "+v"(m[k]));
+    xg[k].forget();
+  }
   __syncthreads();
 
   if (w == 0) {
@@ -166,15 +201,20 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
     }
     sE[lane] = e;
   }
-  // the states that the wave's tokens continue
+  // the states that the wave's tokens continue, and with them dlog_a / e' of each token,
+  // h_{t-1} - iota x a / m (part_a); m becomes dx / g
 #pragma unroll
   for (int q = 0; q < W - 1; ++q)
     if (q < w) h = GlrMap{sA[q][lane], sB[q][lane], PACKED && sReset[q]}(h);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (PACKED && (sp.starts >> k & 1)) h = state0(k);
-    before[k] = h;
-    h = fmaf(a[k], h, m[k] * input(k));
+    const float in = input(k);
+    part_a[k] = fmaf(-in, a[k] * hw_rcp(m[k]), h);
+    h = fmaf(a[k], h, m[k] * in);
+    if (GATE) state[k] = h;
+    m[k] *= iota[k];
+    if (k % 4 == 3) __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
 
@@ -187,48 +227,51 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   Tin* pr = static_cast<Tin*>(p.dr) + end * p.gr;
   Tin* pi = static_cast<Tin*>(p.di) + end * p.gi;
   Tin* pz = GATE ? static_cast<Tin*>(p.dz) + end * p.gz : nullptr;
+  uint32_t at = cb;
   auto put = [&](float gx, float gr, float gi, float gz) __attribute__((always_inline)) {
-    if (mine) {
-      row_store<typename Tok::word, LINES>(px, cb, Tok::put(&gx));
-      row_store<typename Tok::word, LINES>(pr, cb, Tok::put(&gr));
-      row_store<typename Tok::word, LINES>(pi, cb, Tok::put(&gi));
-      if (GATE) row_store<typename Tok::word, LINES>(pz, cb, Tok::put(&gz));
-    }
+    row_store<typename Tok::word, LINES>(px, at, Tok::put(&gx));
+    row_store<typename Tok::word, LINES>(pr, at, Tok::put(&gr));
+    row_store<typename Tok::word, LINES>(pi, at, Tok::put(&gi));
+    if (GATE) row_store<typename Tok::word, LINES>(pz, at, Tok::put(&gz));
     px -= p.gx, pr -= p.gr, pi -= p.gi;
     if (GATE) pz -= p.gz;
   };
   auto token = [&](int k) __attribute__((always_inline)) {
-    const float x = ax.get(rx[k]), in = input(k);
-    float gy = Tok::get(rg[k], 0), gz = 0.f;
+    float gy = xg[k].get_dy(), gz = 0.f;
     if (GATE) {
       const float z = az.get(rz[k]), sz = sigmoid(z);
-      gz = gy * fmaf(a[k], before[k], m[k] * in) * fmaf(z, slope(sz), sz);
+      gz = gy * state[k] * fmaf(z, slope(sz), sz);
       gy *= z * sz;
     }
     if (PACKED && (sp.ends >> k & 1)) e = last_grad(k);
     const float g = gy + e;
     e = a[k] * g;
-    const float dla = e * fmaf(-in, a[k] * hw_rcp(m[k]), before[k]);
-    const float gx = g * m[k] * iota[k];
-    const float gxx = gx * x, gi = fmaf(-iota[k], gxx, gxx);
+    const float dla = e * part_a[k], gx = g * m[k];
+    const float gxx = gx * xg[k].get_x(ax), gi = fmaf(-iota[k], gxx, gxx);
     const float dlp = dla * rho[k], rdl = -rate * dlp, gr = fmaf(-rho[k], rdl, rdl);
     slam += dlp;
     srb += gr;
     sib += gi;
     if (PACKED && (sp.starts >> k & 1)) {
-      if (p.dh0 && mine) p.dh0[static_cast<int64_t>(sp.seq_of(k)) * D + c] = e;
+      if (p.dh0) p.dh0[static_cast<int64_t>(sp.seq_of(k)) * D + c] = e;
       e = 0.f;
     }
     put(gx, gr, gi, gz);
+    if (k % 4 == 0) __builtin_amdgcn_sched_barrier(0);
   };
-  if (sp.valid == K) {
+  if (mine) {
+    if (sp.valid == K) {
+      at = here(cb);
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k) token(k);
-  } else {
+      for (int k = K - 1; k >= 0; --k) token(k);
+      apart<true>();
+    } else {
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-      if (k < sp.valid) token(k);
-      else if (k < rows) put(0.f, 0.f, 0.f, 0.f);
+      for (int k = K - 1; k >= 0; --k) {
+        if (k < sp.valid) token(k);
+        else if (k < rows) put(0.f, 0.f, 0.f, 0.f);
+      }
+      apart<false>();
     }
   }
   if (!PACKED && p.dh0 && mine && tile == 0 && w == 0) p.dh0[b * D + c] = e;

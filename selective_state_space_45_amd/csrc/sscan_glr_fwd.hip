@@ -23,6 +23,7 @@ __device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg (&ra
     fields |= f << (8 * v);
   }
   if (!mine) return;
+  c = here(c);
   row_store<word, LINES>(exps, c, static_cast<word>(fields));
 #pragma unroll
   for (int k = 0; k < kActGroup; ++k) {
@@ -62,8 +63,8 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
   const int64_t cl = c0 + lane * V;
   const bool mine = cl < D;
   const uint32_t c = static_cast<uint32_t>(mine ? cl : D - V), cb = c * sizeof(Tin);
-  const int64_t t0 = static_cast<int64_t>(tile) * kGlrTile + w * K;
-  const int rows = static_cast<int>(L - t0 < 0 ? 0 : (L - t0 < K ? L - t0 : K));
+  const int L32 = static_cast<int>(L), t0 = tile * kGlrTile + w * K;
+  const int rows = L32 - t0 < 0 ? 0 : (L32 - t0 < K ? L32 - t0 : K);
 
   // 16 tokens of each input; tokens past the row's end read its last one
   typename Tok::reg rx[K], rr[K], ri[K], rz[K];
@@ -74,24 +75,25 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
     const Tin* pi = static_cast<const Tin*>(p.i) + t * p.si;
     const Tin* pz = GATE ? static_cast<const Tin*>(p.z) + t * p.sz : nullptr;
     auto load = [&](auto full) __attribute__((always_inline)) {
+      const uint32_t at = here(cb);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        rx[k] = row_load<typename Tok::word, LINES>(px, cb);
-        rr[k] = row_load<typename Tok::word, LINES>(pr, cb);
-        ri[k] = row_load<typename Tok::word, LINES>(pi, cb);
-        if (GATE) rz[k] = row_load<typename Tok::word, LINES>(pz, cb);
-        if (decltype(full)::value || k + 1 < rows) {
-          px += p.sx, pr += p.sr, pi += p.si;
-          if (GATE) pz += p.sz;
-        }
+        rx[k] = row_load<typename Tok::word, LINES>(px, at);
+        rr[k] = row_load<typename Tok::word, LINES>(pr, at);
+        ri[k] = row_load<typename Tok::word, LINES>(pi, at);
+        if (GATE) rz[k] = row_load<typename Tok::word, LINES>(pz, at);
+        const int64_t more = decltype(full)::value || k + 1 < rows ? 1 : 0;
+        px += more * p.sx, pr += more * p.sr, pi += more * p.si;
+        if (GATE) pz += more * p.sz;
       }
+      apart<decltype(full)::value>();
     };
     if (rows == K) load(std::true_type{});
     else load(std::false_type{});
   }
   GlrSpan sp;
   sp.valid = rows;
-  if (PACKED) sp = glr_span(p.offsets, static_cast<int>(p.num_seqs), t0, L);
+  if (PACKED) sp = glr_span(p.offsets, static_cast<int>(p.num_seqs), t0, L32);
 
   float rate[V], nrb[V], nib[V];   // times log2(e); the biases negated
 #pragma unroll
@@ -193,7 +195,9 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
 #pragma unroll
     for (int v = 0; v < V; ++v) ck[v] = start ? first[v] : h[v];
   }
+  if (!mine) return;
   Tin* yrow = static_cast<Tin*>(p.y) + (b * L + t0) * D;
+  const uint32_t at = here(cb);
   auto out = [&](int k) __attribute__((always_inline)) {
     const bool start = PACKED && (sp.starts >> k & 1);
     float y[V];
@@ -203,9 +207,9 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
       y[v] = GATE ? h[v] * silu(Tok::get(rz[k], v)) : h[v];
       if (PACKED && k >= sp.valid) y[v] = 0.f;
     }
-    if (mine) row_store<typename Tok::word, LINES>(yrow, cb, Tok::put(y));
+    row_store<typename Tok::word, LINES>(yrow, at, Tok::put(y));
     yrow += D;
-    if (PACKED && (sp.ends >> k & 1) && p.h_last && mine) {
+    if (PACKED && (sp.ends >> k & 1) && p.h_last) {
       float* hl = p.h_last + static_cast<int64_t>(sp.seq_of(k)) * D + c;
 #pragma unroll
       for (int v = 0; v < V; ++v) hl[v] = h[v];
@@ -214,12 +218,14 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
   if (rows == K) {
 #pragma unroll
     for (int k = 0; k < K; ++k) out(k);
+    apart<true>();
   } else {
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (k < rows) out(k);
+    apart<false>();
   }
-  if (!PACKED && p.h_last && mine && t0 + K >= L) {
+  if (!PACKED && p.h_last && t0 + K >= L32) {
 #pragma unroll
     for (int v = 0; v < V; ++v) p.h_last[b * D + c + v] = h[v];
   }

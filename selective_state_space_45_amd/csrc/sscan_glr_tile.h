@@ -44,6 +44,22 @@ __device__ __forceinline__ void row_store(void* row, uint32_t at, T v) {
   else *p = v;
 }
 
+// A lane's offset, to be used in one block of code: the compiler then sees there that it
+// has 32 bits, which the load's form needs.
+__device__ __forceinline__ uint32_t here(uint32_t at) {
+  asm("" : "+v"(at));
+  return at;
+}
+
+// Ends the code for a whole wave of 16 tokens and for a short one, each with a mark of
+// its own: alike at their ends, the compiler joins them there, with every address of
+// either in vector registers.
+template <bool FULL>
+__device__ __forceinline__ void apart() {
+  if (FULL) asm volatile("; 16 tokens");
+  else asm volatile("; fewer");
+}
+
 // V channels of one token: one word per lane.  top: the word's magnitudes, whose maxima
 // over words give the largest exponents.
 template <typename Tin, int V>
@@ -121,12 +137,12 @@ __device__ __forceinline__ int glr_find(P offsets, int num_seqs, int t) {
   }
   return lo;
 }
-__device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs, int64_t t0, int64_t L) {
+__device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs, int t0, int L) {
   typedef const __attribute__((address_space(4))) int32_t* Scalar;
   const Scalar so = reinterpret_cast<Scalar>(reinterpret_cast<uintptr_t>(offsets));
   GlrSpan sp;
   sp.valid = 0;
-  const int t = static_cast<int>(t0 < L ? t0 : L);
+  const int t = t0 < L ? t0 : L;
   const int s = glr_find(so, num_seqs, t);
   if (s >= num_seqs || t0 >= L) return sp;             // padding only
   const int begin = so[s], end = so[s + 1];            // begin <= t < end
@@ -134,7 +150,7 @@ __device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs
     sp.seq = s;
     sp.starts = begin == t;
     sp.ends = end == t + 16 ? 0x8000u : 0u;
-    sp.valid = static_cast<int>(L - t0 < 16 ? L - t0 : 16);
+    sp.valid = L - t0 < 16 ? L - t0 : 16;
     return sp;
   }
   const int mine = t + static_cast<int>(threadIdx.x & 15);
@@ -213,6 +229,22 @@ struct GlrChainLayout {
 
 constexpr uint32_t kNoWord = 0xffffffffu;
 
+// One lane's word of a row of them, in one access that is coherent across the chip.
+template <typename T>
+__device__ __forceinline__ T word_load(const T* row, uint32_t lane) {
+  uintptr_t r = reinterpret_cast<uintptr_t>(row);
+  asm("" : "+s"(r));
+  return __hip_atomic_load(reinterpret_cast<GlobalPtr<T>>(r + static_cast<uint32_t>(lane * sizeof(T))), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ void word_store(T* row, uint32_t lane, T v) {
+  uintptr_t r = reinterpret_cast<uintptr_t>(row);
+  asm("" : "+s"(r));
+  __hip_atomic_store(reinterpret_cast<GlobalPtr<T>>(r + static_cast<uint32_t>(lane * sizeof(T))), v, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+
 struct GlrMap {
   float A, B;
   bool reset;
@@ -237,8 +269,9 @@ __device__ __forceinline__ bool there(uint64_t w) { return static_cast<uint32_t>
 // place in the chain, of ntiles > 1.  own: the tile's map; initial: the state that
 // enters the chain (read at pos 0 only).  Returns the state that enters the tile.  All 64
 // lanes call it.
-__device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain, int lanes, int at, int pos, int ntiles,
-                                          const GlrMap& own, float initial) {
+__device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain, int lanes, uint32_t lane, int pos,
+                                          int ntiles, const GlrMap& own, float initial) {
+  lane = here(lane);
   const int g = pos / kGlrGroup, j = pos % kGlrGroup, ngroups = (ntiles + kGlrGroup - 1) / kGlrGroup;
   // words of the tile's group, of the group before it, and of the state that enters it
   uint64_t* maps = w.maps + (chain * ntiles + g * kGlrGroup) * lanes;
@@ -246,13 +279,12 @@ __device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain,
   uint32_t* states = w.states + (chain * ngroups + g) * lanes;
   auto put_state = [&](int group, float h) {
     const uint32_t b = __float_as_uint(h);
-    __hip_atomic_store(states + (group - g) * lanes + at, b == kNoWord ? 0x7fc00000u : b, __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
+    word_store(states + (group - g) * lanes, lane, b == kNoWord ? 0x7fc00000u : b);
   };
   if (pos == 0) put_state(0, initial);
   const bool closes = j == kGlrGroup - 1 && g + 1 < ngroups;   // the last tile of a group with another after it
   if (j < kGlrGroup - 1 && pos + 1 < ntiles)
-    __hip_atomic_store(maps + j * lanes + at, own.word(), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    word_store(maps + j * lanes, lane, own.word());
   if (pos == 0) return initial;
 
   uint64_t m[kGlrGroup - 1];
@@ -264,15 +296,15 @@ __device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain,
     if (!have)
 #pragma unroll
       for (int k = 0; k < kGlrGroup - 1; ++k)
-        if (k < j) m[k] = __hip_atomic_load(maps + k * lanes + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (k < j) m[k] = word_load(maps + k * lanes, lane);
 #pragma unroll
     for (int k = 0; k < kGlrBack; ++k) {
       s[k] = kNoWord;
       gm[k] = ~uint64_t(0);
       if (k <= g) {
-        s[k] = __hip_atomic_load(states - k * lanes + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s[k] = word_load(states - k * lanes, lane);
         if (k + 1 <= g && k + 1 < kGlrBack)
-          gm[k] = __hip_atomic_load(gmaps - (k + 1) * lanes + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          gm[k] = word_load(gmaps - (k + 1) * lanes, lane);
       }
     }
     if (!have) {
@@ -286,7 +318,7 @@ __device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain,
         for (int k = 1; k < kGlrGroup - 1; ++k) all = GlrMap::of(m[k]).after(all);
         all = own.after(all);
         if (__all(all.reset)) put_state(g + 1, all.B);
-        else __hip_atomic_store(gmaps + at, all.word(), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else word_store(gmaps, lane, all.word());
       }
     }
     int found = -1;
