@@ -66,7 +66,7 @@ struct GlrPair<bf16_t, Act> {
 // formed again after the wait they cost more than the second channel saves (8 x 4096 x
 // 2048 bf16, forward and backward: 0.442 ms, and 0.397 in this form).
 template <typename Tin, bool LINES, bool PACKED, bool GATE, bool SAVED>
-__global__ __launch_bounds__(64 * kGlrWaves, GATE || sizeof(Tin) == 4 ? 3 : 4) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
+__global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
                                                                  int ntiles, int nct) {
   typedef TokVec<Tin, 1> Tok;
   typedef GlrAct<Tin, LINES, SAVED> Act;
@@ -139,7 +139,6 @@ __global__ __launch_bounds__(64 * kGlrWaves, GATE || sizeof(Tin) == 4 ? 3 : 4) v
     iota[k] = gate(ai.get(ri[k]), nib);
     a[k] = decay_of(rate2 * rho[k], one);
     m[k] = hw_sqrt(fmaxf(one, 1e-36f));
-    if (k % 4 == 3) __builtin_amdgcn_sched_barrier(0);
   }
   GlrPair<Tin, Act> xg[K];
 #pragma unroll
@@ -214,7 +213,6 @@ __global__ __launch_bounds__(64 * kGlrWaves, GATE || sizeof(Tin) == 4 ? 3 : 4) v
     h = fmaf(a[k], h, m[k] * in);
     if (GATE) state[k] = h;
     m[k] *= iota[k];
-    if (k % 4 == 3) __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
 
@@ -257,7 +255,6 @@ __global__ __launch_bounds__(64 * kGlrWaves, GATE || sizeof(Tin) == 4 ? 3 : 4) v
       e = 0.f;
     }
     put(gx, gr, gi, gz);
-    if (k % 4 == 0) __builtin_amdgcn_sched_barrier(0);
   };
   if (mine) {
     if (sp.valid == K) {
