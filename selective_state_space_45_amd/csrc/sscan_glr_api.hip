@@ -283,7 +283,7 @@ int glr_step(int64_t batch, int64_t dim, int dtype, float* state, int64_t num_sl
              const int64_t* strides, const float* lam, const float* r_bias, const float* i_bias, float decay_scale,
              void* y, void* stream) {
   SSCAN_TRY(check_sizes(batch, 1, dim, dtype));
-  SSCAN_TRY(check_lanes(batch * dim));
+  SSCAN_TRY(check_tiles(batch, 1, dim));
   if (num_slots < 0 || !fits(num_slots, dim, 1))
     return fail(SSCAN_ERR_INVALID_ARG, "num_slots %lld negative or too large", (long long)num_slots);
   if (!slots && batch > num_slots)

@@ -196,7 +196,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
       GlrMap all{sA[W - 1][lane], sG[W - 1][lane], PACKED && sReset[W - 1]};
 #pragma unroll
       for (int q = W - 2; q >= 0; --q) all = GlrMap{sA[q][lane], sG[q][lane], PACKED && sReset[q]}.after(all);
-      e = glr_pass(words, chain, 64, lane, pos, ntiles, all, e);
+      e = glr_pass<64>(words, chain, lane, pos, ntiles, all, e);
     }
     sE[lane] = e;
   }
@@ -301,12 +301,12 @@ __global__ __launch_bounds__(1024) void glr_param_kernel(const float* part, cons
     return part[(((b * nct + ct) * ntiles + tile) * 3 + kind) * 64 + lane];
   };
   int64_t k = w;
-  for (; k + 7 * 16 < n; k += 8 * 16) {   // eight loads in flight
-    float x[8];
+  for (; k + 15 * 16 < n; k += 16 * 16) {   // sixteen loads in flight
+    float x[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = at(k + j * 16);
+    for (int j = 0; j < 16; ++j) x[j] = at(k + j * 16);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += x[j];
+    for (int j = 0; j < 16; ++j) s += x[j];
   }
   for (; k < n; k += 16) s += at(k);
   sum[w][lane] = s;
@@ -333,10 +333,6 @@ void launch_saved(const GlrBwdParams& p, const GlrChainLayout& lo, float* part, 
 
 template <typename Tin, bool LINES>
 hipError_t launch_lines(const GlrBwdParams& p, const GlrChainLayout& lo, float* part, int nct, hipStream_t s) {
-  if (lo.tiles > 1) {
-    const hipError_t e = launch_glr_clear(p.workspace, lo, s);
-    if (e != hipSuccess) return e;
-  }
   if (p.offsets)
     p.dz ? launch_saved<Tin, LINES, true, true>(p, lo, part, nct, s) : launch_saved<Tin, LINES, true, false>(p, lo, part, nct, s);
   else
@@ -349,6 +345,11 @@ hipError_t launch_t(const GlrBwdParams& p, hipStream_t s) {
   const GlrChainLayout lo(p.batch, p.L, p.dim, 1);
   const int nct = static_cast<int>((p.dim + 63) / 64);
   float* part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + lo.bytes());
+  // without tokens (or for the requests that have none) the gradient passes through
+  const bool some = p.offsets || p.L == 0;
+  const hipError_t e = launch_glr_begin(p.workspace, lo, p.offsets, p.offsets ? p.num_seqs : p.batch, p.dlast,
+                                        some ? p.dh0 : nullptr, p.dim, s);
+  if (e != hipSuccess) return e;
   if (p.batch > 0 && p.L > 0) {
     // past the caches where every row of every tensor starts on a cache line
     uintptr_t bits = static_cast<uintptr_t>(p.dim | p.gx | p.gr | p.gi | (p.dz ? p.gz : 0)) * sizeof(Tin);
@@ -373,10 +374,6 @@ size_t glr_bwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim) {
 }
 
 hipError_t launch_glr_bwd(const GlrBwdParams& p, bool bf16, hipStream_t s) {
-  if (p.dh0 && (p.offsets || p.L == 0)) {
-    const hipError_t e = launch_glr_empty(p.offsets, p.dlast, p.dh0, p.offsets ? p.num_seqs : p.batch, p.dim, s);
-    if (e != hipSuccess) return e;
-  }
   return bf16 ? launch_t<bf16_t>(p, s) : launch_t<float>(p, s);
 }
 

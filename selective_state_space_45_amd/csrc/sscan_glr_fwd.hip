@@ -40,7 +40,7 @@ __device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg (&ra
 // each of them once, and so does the output, so a and u stay in registers between the two
 // while the state is on its way; four waves a SIMD cover that wait.
 template <typename Tin, int V, bool LINES, bool PACKED, bool GATE, bool SAVE>
-__global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4) ? 3 : 4) void glr_fwd_kernel(
+__global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE && sizeof(Tin) == 4) ? 3 : 4) void glr_fwd_kernel(
     GlrFwdParams p, GlrChainWords words, int ntiles, int nct) {
   typedef TokVec<Tin, V> Tok;
   constexpr int K = kActGroup, W = kGlrWaves;
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
       GlrMap all{sA[0][w][lane], sB[0][w][lane], PACKED && sReset[0]};
 #pragma unroll
       for (int q = 1; q < W; ++q) all = GlrMap{sA[q][w][lane], sB[q][w][lane], PACKED && sReset[q]}.after(all);
-      h = glr_pass(words, chain, 64 * V, w * 64 + lane, tile, ntiles, all, h);
+      h = glr_pass<64 * V>(words, chain, w * 64 + lane, tile, ntiles, all, h);
     }
     sH[w][lane] = h;
   }
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
   }
   if (!mine) return;
   Tin* yrow = static_cast<Tin*>(p.y) + (b * L + t0) * D;
-  const uint32_t at = here(cb);
+  uint32_t at = cb;
   auto out = [&](int k) __attribute__((always_inline)) {
     const bool start = PACKED && (sp.starts >> k & 1);
     float y[V];
@@ -216,6 +216,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
     }
   };
   if (rows == K) {
+    at = here(cb);
 #pragma unroll
     for (int k = 0; k < K; ++k) out(k);
     apart<true>();
@@ -231,32 +232,34 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE || sizeof(Tin) == 4
   }
 }
 
-// The last state of a sequence without tokens is its initial one.
-__global__ __launch_bounds__(256) void glr_empty_kernel(const int32_t* offsets, const float* from, float* to, int64_t D) {
-  const int64_t s = blockIdx.x;
-  if (offsets && offsets[s] != offsets[s + 1]) return;
-  for (int64_t d = threadIdx.x; d < D; d += 256) {
-    const float v = from ? from[s * D + d] : 0.f;
-    to[s * D + d] = v;
+// What comes before a launch over tiles: the chain's words (16 bytes a lane; the first
+// `zeros` of them zero, the rest all ones), and in workgroups of their own the sequences
+// without tokens, to[s] = from[s] (zero if from is null).
+__global__ __launch_bounds__(256) void glr_begin_kernel(uint4* words, size_t zeros, size_t count, unsigned clearing,
+                                                        const int32_t* offsets, int64_t rows, const float* from, float* to,
+                                                        int64_t D) {
+  if (blockIdx.x < clearing) {
+    const size_t n = static_cast<size_t>(clearing) * 256;
+    for (size_t k = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; k < count; k += n) {
+      const uint32_t v = k < zeros ? 0u : kNoWord;
+      words[k] = make_uint4(v, v, v, v);
+    }
+    return;
+  }
+  for (int64_t s = blockIdx.x - clearing; s < rows; s += gridDim.x - clearing) {
+    if (offsets && offsets[s] != offsets[s + 1]) continue;
+    for (int64_t d = threadIdx.x; d < D; d += 256) to[s * D + d] = from ? from[s * D + d] : 0.f;
   }
 }
 
-__global__ __launch_bounds__(256) void glr_clear_kernel(uint32_t* ws, size_t zeros, size_t words) {
-  const size_t n = static_cast<size_t>(gridDim.x) * 256;
-  for (size_t k = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; k < words; k += n) ws[k] = k < zeros ? 0u : kNoWord;
-}
-
-hipError_t launch_glr_clear(void* ws, const GlrChainLayout& lo, hipStream_t s) {
-  const size_t words = lo.total / 4;
-  const size_t nb = (words + 1023) / 1024;
-  hipLaunchKernelGGL(glr_clear_kernel, dim3(static_cast<unsigned>(nb < 2048 ? nb : 2048)), dim3(256), 0, s,
-                     static_cast<uint32_t*>(ws), lo.maps_at / 4, words);
-  return hipGetLastError();
-}
-
-hipError_t launch_glr_empty(const int32_t* offsets, const float* from, float* to, int64_t rows, int64_t D, hipStream_t s) {
-  if (rows > 0 && from != to)
-    hipLaunchKernelGGL(glr_empty_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, offsets, from, to, D);
+hipError_t launch_glr_begin(void* ws, const GlrChainLayout& lo, const int32_t* offsets, int64_t rows, const float* from,
+                            float* to, int64_t D, hipStream_t s) {
+  const size_t count = lo.bytes() / 16;
+  const unsigned clearing = static_cast<unsigned>((count + 1023) / 1024 < 2048 ? (count + 1023) / 1024 : 2048);
+  const unsigned rest = to && to != from ? static_cast<unsigned>(rows < 256 ? rows : 256) : 0;
+  if (clearing + rest == 0) return hipSuccess;
+  hipLaunchKernelGGL(glr_begin_kernel, dim3(clearing + rest), dim3(256), 0, s, static_cast<uint4*>(ws), lo.maps_at / 16,
+                     count, clearing, offsets, rows, from, to, D);
   return hipGetLastError();
 }
 
@@ -274,10 +277,11 @@ void launch_save(const GlrFwdParams& p, const GlrChainLayout& lo, hipStream_t s)
 template <typename Tin, int V, bool LINES>
 hipError_t launch_v(const GlrFwdParams& p, hipStream_t s) {
   const GlrChainLayout lo(p.batch, p.L, p.dim, V);
-  if (lo.tiles > 1) {
-    const hipError_t e = launch_glr_clear(p.workspace, lo, s);
-    if (e != hipSuccess) return e;
-  }
+  // without tokens (or for the requests that have none) the last state is the initial one
+  const bool some = p.offsets || p.L == 0;
+  const hipError_t e = launch_glr_begin(p.workspace, lo, p.offsets, p.offsets ? p.num_seqs : p.batch, p.h0,
+                                        some ? p.h_last : nullptr, p.dim, s);
+  if (e != hipSuccess || p.L == 0) return e;
   if (p.offsets) p.z ? launch_save<Tin, V, LINES, true, true>(p, lo, s) : launch_save<Tin, V, LINES, true, false>(p, lo, s);
   else p.z ? launch_save<Tin, V, LINES, false, true>(p, lo, s) : launch_save<Tin, V, LINES, false, false>(p, lo, s);
   return hipGetLastError();
@@ -303,11 +307,6 @@ size_t glr_fwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim) {
 }
 
 hipError_t launch_glr_fwd(const GlrFwdParams& p, bool bf16, hipStream_t s) {
-  if (p.h_last && (p.offsets || p.L == 0)) {
-    const hipError_t e = launch_glr_empty(p.offsets, p.h0, p.h_last, p.offsets ? p.num_seqs : p.batch, p.dim, s);
-    if (e != hipSuccess) return e;
-  }
-  if (p.L == 0) return hipSuccess;
   return bf16 ? launch_t<bf16_t>(p, s) : launch_t<float>(p, s);
 }
 

@@ -229,20 +229,17 @@ struct GlrChainLayout {
 
 constexpr uint32_t kNoWord = 0xffffffffu;
 
-// One lane's word of a row of them, in one access that is coherent across the chip.
-template <typename T>
-__device__ __forceinline__ T word_load(const T* row, uint32_t lane) {
-  uintptr_t r = reinterpret_cast<uintptr_t>(row);
-  asm("" : "+s"(r));
-  return __hip_atomic_load(reinterpret_cast<GlobalPtr<T>>(r + static_cast<uint32_t>(lane * sizeof(T))), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+// One lane's word of row `k` from a row of LANES words each, in one access that is coherent
+// across the chip: the row's distance is part of the instruction (within its 4096 bytes).
+template <int LANES, typename T>
+__device__ __forceinline__ T word_load(const T* row, uint32_t lane, int k) {
+  const GlobalPtr<T> at = reinterpret_cast<GlobalPtr<T>>(reinterpret_cast<uintptr_t>(row) + static_cast<uint32_t>(lane * sizeof(T)));
+  return __hip_atomic_load(at + k * LANES, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 template <typename T>
 __device__ __forceinline__ void word_store(T* row, uint32_t lane, T v) {
-  uintptr_t r = reinterpret_cast<uintptr_t>(row);
-  asm("" : "+s"(r));
-  __hip_atomic_store(reinterpret_cast<GlobalPtr<T>>(r + static_cast<uint32_t>(lane * sizeof(T))), v, __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
+  const GlobalPtr<T> at = reinterpret_cast<GlobalPtr<T>>(reinterpret_cast<uintptr_t>(row) + static_cast<uint32_t>(lane * sizeof(T)));
+  __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 struct GlrMap {
@@ -269,22 +266,22 @@ __device__ __forceinline__ bool there(uint64_t w) { return static_cast<uint32_t>
 // place in the chain, of ntiles > 1.  own: the tile's map; initial: the state that
 // enters the chain (read at pos 0 only).  Returns the state that enters the tile.  All 64
 // lanes call it.
-__device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain, int lanes, uint32_t lane, int pos,
-                                          int ntiles, const GlrMap& own, float initial) {
-  lane = here(lane);
+template <int LANES>
+__device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain, uint32_t lane, int pos, int ntiles,
+                                          const GlrMap& own, float initial) {
   const int g = pos / kGlrGroup, j = pos % kGlrGroup, ngroups = (ntiles + kGlrGroup - 1) / kGlrGroup;
   // words of the tile's group, of the group before it, and of the state that enters it
-  uint64_t* maps = w.maps + (chain * ntiles + g * kGlrGroup) * lanes;
-  uint64_t* gmaps = w.group_maps + (chain * ngroups + g) * lanes;
-  uint32_t* states = w.states + (chain * ngroups + g) * lanes;
+  uint64_t* maps = w.maps + (chain * ntiles + g * kGlrGroup) * LANES;
+  uint64_t* gmaps = w.group_maps + (chain * ngroups + g) * LANES;
+  uint32_t* states = w.states + (chain * ngroups + g) * LANES;
   auto put_state = [&](int group, float h) {
     const uint32_t b = __float_as_uint(h);
-    word_store(states + (group - g) * lanes, lane, b == kNoWord ? 0x7fc00000u : b);
+    word_store(states + (group - g) * LANES, lane, b == kNoWord ? 0x7fc00000u : b);
   };
   if (pos == 0) put_state(0, initial);
   const bool closes = j == kGlrGroup - 1 && g + 1 < ngroups;   // the last tile of a group with another after it
   if (j < kGlrGroup - 1 && pos + 1 < ntiles)
-    word_store(maps + j * lanes, lane, own.word());
+    word_store(maps + j * LANES, lane, own.word());
   if (pos == 0) return initial;
 
   uint64_t m[kGlrGroup - 1];
@@ -296,15 +293,15 @@ __device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain,
     if (!have)
 #pragma unroll
       for (int k = 0; k < kGlrGroup - 1; ++k)
-        if (k < j) m[k] = word_load(maps + k * lanes, lane);
+        if (k < j) m[k] = k < 4 ? word_load<LANES>(maps, lane, k) : word_load<LANES>(maps + 4 * LANES, lane, k - 4);
 #pragma unroll
     for (int k = 0; k < kGlrBack; ++k) {
       s[k] = kNoWord;
       gm[k] = ~uint64_t(0);
       if (k <= g) {
-        s[k] = word_load(states - k * lanes, lane);
+        s[k] = word_load<LANES>(states, lane, -k);
         if (k + 1 <= g && k + 1 < kGlrBack)
-          gm[k] = word_load(gmaps - (k + 1) * lanes, lane);
+          gm[k] = word_load<LANES>(gmaps, lane, -(k + 1));
       }
     }
     if (!have) {
@@ -343,9 +340,10 @@ __device__ __forceinline__ float glr_pass(const GlrChainWords& w, int64_t chain,
   }
 }
 
-// Fills the words before a launch: tickets with zeros, the rest with ones.
-hipError_t launch_glr_clear(void* ws, const GlrChainLayout& lo, hipStream_t s);
-// to[s] = from[s] (zero if null), for the sequences without tokens (all, if offsets is null).
-hipError_t launch_glr_empty(const int32_t* offsets, const float* from, float* to, int64_t rows, int64_t D, hipStream_t s);
+// Fills the chain's words before a launch (tickets with zeros, the rest with ones), and
+// sets to[s] = from[s] (zero if null) for the sequences without tokens: those of equal
+// offsets, or all if offsets is null.
+hipError_t launch_glr_begin(void* ws, const GlrChainLayout& lo, const int32_t* offsets, int64_t rows, const float* from,
+                            float* to, int64_t D, hipStream_t s);
 
 }  // namespace sscan
