@@ -164,12 +164,14 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
       if (PACKED && (sp.starts >> k & 1)) G = 0.f;
     };
     if (sp.valid == K) {
+      apart<true>();
 #pragma unroll
       for (int k = 0; k < K; ++k) ahead(k);
 #pragma unroll
       for (int k = K - 1; k >= 0; --k) back(k);
       apart<true>();
     } else {
+      apart<false>();
 #pragma unroll
       for (int k = 0; k < K; ++k)
         if (k < sp.valid) ahead(k);
@@ -258,11 +260,13 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   };
   if (mine) {
     if (sp.valid == K) {
+      apart<true>();
       at = here(cb);
 #pragma unroll
       for (int k = K - 1; k >= 0; --k) token(k);
       apart<true>();
     } else {
+      apart<false>();
 #pragma unroll
       for (int k = K - 1; k >= 0; --k) {
         if (k < sp.valid) token(k);
@@ -287,34 +291,38 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
 }
 
 // Parameter gradients: the tiles' sums, over batch rows and tiles in a fixed order.  One
-// workgroup per 64 channels and parameter, 16 waves taking every 16th tile.
+// workgroup per 16 channels and parameter, 64 sets of 16 lanes taking every 64th tile (16
+// channels rather than 64: four times the workgroups, for loads that wait on memory).
 __global__ __launch_bounds__(1024) void glr_param_kernel(const float* part, const float* lam, float decay_scale, float* dlam,
                                                          float* drb, float* dib, int64_t batch, int64_t ntiles, int64_t D,
                                                          int nct) {
-  __shared__ float sum[16][64];
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int kind = blockIdx.x % 3, ct = blockIdx.x / 3;
-  float s = 0.f;
+  __shared__ float sum[64][16];
+  const int set = threadIdx.x >> 4, lane = threadIdx.x & 15;
+  const int kind = blockIdx.x % 3, quarter = blockIdx.x / 3 % 4, ct = blockIdx.x / 12;
   const int64_t n = batch * ntiles;
   auto at = [&](int64_t k) {
     const int64_t b = k / ntiles, tile = k - b * ntiles;
-    return part[(((b * nct + ct) * ntiles + tile) * 3 + kind) * 64 + lane];
+    return part[(((b * nct + ct) * ntiles + tile) * 3 + kind) * 64 + quarter * 16 + lane];
   };
-  int64_t k = w;
-  for (; k + 15 * 16 < n; k += 16 * 16) {   // sixteen loads in flight
-    float x[16];
+  float s = 0.f;
+  int64_t k = set;
+  for (; k + 7 * 64 < n; k += 8 * 64) {   // eight loads in flight
+    float x[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = at(k + j * 16);
+    for (int j = 0; j < 8; ++j) x[j] = at(k + j * 64);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) s += x[j];
+    for (int j = 0; j < 8; ++j) s += x[j];
   }
-  for (; k < n; k += 16) s += at(k);
-  sum[w][lane] = s;
+  for (; k < n; k += 64) s += at(k);
+  sum[set][lane] = s;
   __syncthreads();
-  const int64_t d = static_cast<int64_t>(ct) * 64 + lane;
-  if (w > 0 || d >= D) return;
+  if (set >= 4) return;                   // one wave is left
 #pragma unroll
-  for (int q = 1; q < 16; ++q) s += sum[q][lane];
+  for (int q = 1; q < 16; ++q) s += sum[set + 4 * q][lane];
+  sum[set][lane] = s;
+  const int64_t d = static_cast<int64_t>(ct) * 64 + quarter * 16 + lane;
+  if (set > 0 || d >= D) return;
+  s = ((s + sum[1][lane]) + sum[2][lane]) + sum[3][lane];
   if (kind == 0) dlam[d] = -decay_scale * sigmoid(lam[d]) * s;
   else if (kind == 1 && drb) drb[d] = s;
   else if (kind == 2 && dib) dib[d] = s;
@@ -361,7 +369,7 @@ hipError_t launch_t(const GlrBwdParams& p, hipStream_t s) {
                                                 : launch_lines<Tin, false>(p, lo, part, nct, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(glr_param_kernel, dim3(static_cast<unsigned>(3 * nct)), dim3(1024), 0, s, part, p.lam, p.decay_scale,
+  hipLaunchKernelGGL(glr_param_kernel, dim3(static_cast<unsigned>(12 * nct)), dim3(1024), 0, s, part, p.lam, p.decay_scale,
                      p.dlam, p.dr_bias, p.di_bias, p.batch, lo.tiles, p.dim, nct);
   return hipGetLastError();
 }

@@ -51,9 +51,9 @@ __device__ __forceinline__ uint32_t here(uint32_t at) {
   return at;
 }
 
-// Ends the code for a whole wave of 16 tokens and for a short one, each with a mark of
-// its own: alike at their ends, the compiler joins them there, with every address of
-// either in vector registers.
+// Marks the begin and the end of the code for a whole wave of 16 tokens and of that for a
+// short one: where they are alike the compiler takes them together before or after the
+// branch, with every address and product of either in vector registers.
 template <bool FULL>
 __device__ __forceinline__ void apart() {
   if (FULL) asm volatile("; 16 tokens");
