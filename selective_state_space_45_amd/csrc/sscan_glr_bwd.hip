@@ -59,12 +59,15 @@ struct GlrPair<bf16_t, Act> {
 // gradient that leaves a token towards the one before is e' = a (gy + e), again an affine
 // map with the same factor a, so one exchange through shared memory serves both.
 //
-// 14 bytes an element in bf16 against about 50 vector operations and 7 of the
-// quarter-rate ones: both near the time of the other.  One channel a lane: what the
-// gradients need of each of 16 tokens but the gradient that arrives is formed before the
-// wait for it and stays in registers.  With two channels a lane they do not fit three waves a SIMD, and
-// formed again after the wait they cost more than the second channel saves (8 x 4096 x
-// 2048 bf16, forward and backward: 0.442 ms, and 0.397 in this form).
+// 14 bytes an element in bf16 against about 50 vector operations and 7 of the quarter-rate
+// ones, each about half of the time it takes: bound by the latency of its phases (a ticket,
+// loads, maps, the wait, stores: 10 us a workgroup) at three waves a SIMD.  One channel a
+// lane: what the gradients need of each of 16 tokens but the gradient that arrives is
+// formed before the wait for it and stays in registers.  With two channels a lane that
+// does not fit, and formed again after the wait it costs more than the second channel
+// saves (8 x 4096 x 2048 bf16, forward and backward: 0.442 ms, and 0.397 with one); four
+// waves a SIMD spill (0.417 against 0.376).  8 x 4096 x 2048 bf16: 0.235 ms, 4.0 TB/s; from
+// 8 bits 0.240 ms.
 template <typename Tin, bool LINES, bool PACKED, bool GATE, bool SAVED>
 __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
                                                                  int ntiles, int nct) {

@@ -6,9 +6,12 @@
 // registers.  The tiles of one batch row and channel range form a chain.  A run of
 // tokens is an affine map of the state that enters it, h -> A h + B, so each wave first
 // forms its own (A, B), the workgroup joins them, and the state entering the tile comes
-// from the tile before by a single pass over memory (GlrChain below): every input is
+// from the tile before by a single pass over memory (glr_pass below): every input is
 // read once whatever the length, and a long sequence of few channels still fills the
-// chip, since all its tiles are workgroups of their own.
+// chip, since all its tiles are workgroups of their own.  (Workgroups of 8 waves and 128
+// tokens: 8 x 4096 x 2048 bf16 gated 0.192 ms against 0.164, with the chain as it then
+// was.  Workgroups that stay and take tile after tile, with or without the next one's
+// tokens already in registers: 0.18 and 0.29 against 0.154, for the registers they take.)
 #pragma once
 
 #include "sscan_glr.h"
@@ -23,9 +26,9 @@ constexpr int kGlrTile = kGlrBlock;                // tokens of a tile: the spac
 // in scalar registers and the lane's 32-bit offset are added in the load itself.  The
 // empty asm keeps the compiler from adding the offset to a common base first, which
 // leaves a 64-bit vector addition to every load.  LINES: the wave's rows are whole cache
-// lines; then they pass by the caches, since nothing here reads them again.  Lines that
-// two waves share gain from staying (2 x 2047 x 1535 float32, forward and backward: 0.135
-// ms streamed, 0.120 not; 8 x 4096 x 2048 bf16: 0.376 and 0.397).
+// lines; then they are streamed, since nothing here reads them again (forward and
+// backward at 8 x 4096 x 2048 bf16: 0.372 ms, 0.396 without).  Lines that two waves share
+// gain from staying (2 x 2047 x 1535 float32: 0.135 ms streamed, 0.120 not).
 template <typename T>
 using GlobalPtr = __attribute__((address_space(1))) T*;
 template <typename T, bool LINES>
@@ -123,9 +126,9 @@ struct GlrSpan {
 // A token's sequence is the number of offsets[1 ..] at or below it, found by bisection.
 // The wave looks for its first token's through the scalar cache, beside the tokens' own
 // loads; only if a boundary falls among its tokens does each of 16 lanes look for its
-// own (with vector loads alone, which return after those of the tokens, a prefill of 37
-// requests, 16411 tokens of 2560 channels in bf16, took 120 us; so ... us).  Any contents
-// of offsets give indices inside [0, num_seqs).
+// own.  (By vector loads alone, which return after those of the tokens, a prefill of 37
+// requests, 16411 tokens of 2560 channels in bf16, takes 0.107 ms, so 0.102.)  Any
+// contents of offsets give indices inside [0, num_seqs).
 template <typename P>
 __device__ __forceinline__ int glr_find(P offsets, int num_seqs, int t) {
   int lo = 0, n = num_seqs;
@@ -170,18 +173,18 @@ __device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs
 // as it has it; a group's last tile publishes the group's map, its tiles' maps joined in
 // order, and, once it knows the state S_g that enters the group, the one that leaves,
 // S_{g+1} = A_g S_g + B_g.  A tile waits for the maps before it in its group, which wait
-// for nothing, and looks back over up to 4 groups for the nearest state there is,
-// carried through the groups' maps after it and then the tiles'.  These are the same
-// operations wherever the state is found: results do not depend on timing.  (With
-// states per tile instead of per group, 64 tiles back, the chain itself bounded long
-// sequences: 131072 tokens of 2560 channels in bf16 took 0.79 ms, 0.56 with the wait
-// left out.)
+// for nothing, and looks back over two groups for the nearest state there is, carried
+// through the groups' maps after it and then the tiles'.  These are the same operations
+// wherever the state is found: results do not depend on timing.  (131072 tokens of 2560
+// channels in bf16, 20 chains: 0.79 ms with a state for every tile and 64 tiles looked
+// back over, 0.71 with groups; after other steps 0.637 with groups of 4, 0.621 with 8 and
+// four groups back, 0.607 with two back.  The same tiles without the wait: 0.56.)
 //
 // A map's A is at least 0; its sign bit marks a run that contains a sequence's start:
 // what it leaves is B, whatever enters.
 //
-// Each published word carries its own readiness: a word of all ones (which a fill
-// kernel writes before) is no value, and a value that would be all ones, a NaN, is
+// Each published word carries its own readiness: a word of all ones (which a kernel
+// writes before) is no value, and a value that would be all ones, a NaN, is
 // stored as another NaN.  So one relaxed atomic access, coherent across the XCDs, both
 // tests and reads; no other memory passes between tiles, and no order beyond that of
 // the word itself is needed.
@@ -191,10 +194,10 @@ __device__ __forceinline__ GlrSpan glr_span(const int32_t* offsets, int num_seqs
 // earliest tile waits for none.
 // ---------------------------------------------------------------------------
 constexpr int kGlrGroup = 8;   // tiles of a group
-constexpr int kGlrBack = 4;    // groups that one look back covers
+constexpr int kGlrBack = 2;    // groups that one look back covers
 
-// Counters lie a cache line apart: side by side, all of a launch's first workgroups
-// queued at a few lines, 4 us before the first load.
+// Counters lie a cache line apart: side by side, all of a launch's first workgroups queue
+// at a few lines, 4 us before the first load (2 x 2048 x 1536 float32: 28.7 us, apart 23.3).
 constexpr int kGlrTicket = 32;
 
 struct GlrChainWords {
