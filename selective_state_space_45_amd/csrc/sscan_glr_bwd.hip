@@ -59,17 +59,18 @@ struct GlrPair<bf16_t, Act> {
 // gradient that leaves a token towards the one before is e' = a (gy + e), again an affine
 // map with the same factor a, so one exchange through shared memory serves both.
 //
-// 14 bytes an element in bf16 against about 50 vector operations and 7 of the quarter-rate
-// ones, each about half of the time it takes: bound by the latency of its phases (a ticket,
-// loads, maps, the wait, stores: 10 us a workgroup) at three waves a SIMD.  One channel a
-// lane: what the gradients need of each of 16 tokens but the gradient that arrives is
-// formed before the wait for it and stays in registers.  With two channels a lane that
-// does not fit, and formed again after the wait it costs more than the second channel
-// saves (8 x 4096 x 2048 bf16, forward and backward: 0.442 ms, and 0.397 with one); four
-// waves a SIMD spill (0.417 against 0.376).  8 x 4096 x 2048 bf16: 0.235 ms, 4.0 TB/s; from
-// 8 bits 0.240 ms.
+// 14 bytes an element in bf16 against about 60 vector operations, 7 of them at half rate:
+// counters show the vector units busy half of the time and the memory at 4.2 TB/s; bound
+// by the latency of its phases (a ticket, loads, maps, the wait, stores: 10 us a
+// workgroup) at the waves that the registers allow.  One channel a lane: what the
+// gradients need of each of 16 tokens but the gradient that arrives is formed before the
+// wait for it and stays in registers.  With two channels a lane that does not fit, and
+// formed again after the wait it costs more than the second channel saves (8 x 4096 x 2048
+// bf16, forward and backward: 0.442 ms, and 0.397 with one).  Four waves a SIMD for bf16
+// without a gate (0.361 ms, with three 0.381); the other forms spill at four (with a gate,
+// 2 x 2047 x 1535 float32: 0.163 ms, with three 0.108).  8 x 4096 x 2048 bf16: 0.22 ms.
 template <typename Tin, bool LINES, bool PACKED, bool GATE, bool SAVED>
-__global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
+__global__ __launch_bounds__(64 * kGlrWaves, PACKED || GATE || sizeof(Tin) == 4 ? 3 : 4) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
                                                                  int ntiles, int nct) {
   typedef TokVec<Tin, 1> Tok;
   typedef GlrAct<Tin, LINES, SAVED> Act;
@@ -78,7 +79,12 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   __shared__ int sReset[W], sTile;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct;
-  const uint32_t chain = blockIdx.x % nchains;
+  // Workgroups go round-robin over the 8 XCDs.  Two neighbouring chains share the cache
+  // lines of the 8-bit codes (64 bytes of 128 each), so they go to one XCD: a 16-set of
+  // chains takes them in the order 0, 2, .., 14, 1, 3, .. (from 8 bits, 8 x 4096 x 2048,
+  // forward and backward: 0.408 ms, in order 0.418; from bf16 0.360 and 0.364).
+  uint32_t chain = blockIdx.x % nchains;
+  if (chain < nchains / 16 * 16) chain = (chain & ~15u) | (chain & 7u) << 1 | (chain >> 3 & 1u);
   int pos = 0;
   if (ntiles > 1) {
     if (threadIdx.x == 0)
@@ -146,6 +152,17 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   GlrPair<Tin, Act> xg[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) xg[k].set(rx[k], rg[k]);
+  // Tokens past the end, whatever they hold, pass the state and the gradient on (a = 1,
+  // x = dy = 0) and have zero gradients themselves (iota, rho, and part_a below).
+  if (sp.valid < K) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k >= sp.valid) {
+        a[k] = m[k] = 1.f, rho[k] = iota[k] = 0.f;
+        xg[k].set({}, {});
+        if (GATE) rz[k] = {};
+      }
+  }
   auto input = [&](int k) __attribute__((always_inline)) { return iota[k] * xg[k].get_x(ax); };
   auto state0 = [&](int k) __attribute__((always_inline)) {
     return p.h0 ? p.h0[static_cast<int64_t>(sp.seq_of(k)) * D + c] : 0.f;
@@ -166,23 +183,10 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
       G = a[k] * (G + (GATE ? dy * silu(az.get(rz[k])) : dy));
       if (PACKED && (sp.starts >> k & 1)) G = 0.f;
     };
-    if (sp.valid == K) {
-      apart<true>();
 #pragma unroll
-      for (int k = 0; k < K; ++k) ahead(k);
+    for (int k = 0; k < K; ++k) ahead(k);
 #pragma unroll
-      for (int k = K - 1; k >= 0; --k) back(k);
-      apart<true>();
-    } else {
-      apart<false>();
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (k < sp.valid) ahead(k);
-#pragma unroll
-      for (int k = K - 1; k >= 0; --k)
-        if (k < sp.valid) back(k);
-      apart<false>();
-    }
+    for (int k = K - 1; k >= 0; --k) back(k);
     sA[w][lane] = A, sB[w][lane] = B, sG[w][lane] = G;
   }
   if (PACKED && lane == 0) sReset[w] = sp.starts != 0;
@@ -191,6 +195,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
   for (int k = 0; k < K; ++k) {
     asm("" : "+v"(m[k]));
     xg[k].forget();
+    if (GATE) asm("" : "+v"(rz[k]));
   }
   __syncthreads();
 
@@ -219,26 +224,29 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
     if (GATE) state[k] = h;
     m[k] *= iota[k];
   }
+  if (sp.valid < K) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k >= sp.valid) {
+        part_a[k] = 0.f;
+        if (GATE) state[k] = 0.f;
+      }
+  }
   __syncthreads();
 
   float e = sE[lane], slam = 0.f, srb = 0.f, sib = 0.f;
 #pragma unroll
   for (int q = W - 1; q > 0; --q)
     if (q > w) e = GlrMap{sA[q][lane], sG[q][lane], PACKED && sReset[q]}(e);
-  const int64_t end = b * L + t0 + (rows ? rows - 1 : 0);   // the wave's last token
-  Tin* px = static_cast<Tin*>(p.dx) + end * p.gx;
-  Tin* pr = static_cast<Tin*>(p.dr) + end * p.gr;
-  Tin* pi = static_cast<Tin*>(p.di) + end * p.gi;
-  Tin* pz = GATE ? static_cast<Tin*>(p.dz) + end * p.gz : nullptr;
-  uint32_t at = cb;
-  auto put = [&](float gx, float gr, float gi, float gz) __attribute__((always_inline)) {
-    row_store<typename Tok::word, LINES>(px, at, Tok::put(&gx));
-    row_store<typename Tok::word, LINES>(pr, at, Tok::put(&gr));
-    row_store<typename Tok::word, LINES>(pi, at, Tok::put(&gi));
-    if (GATE) row_store<typename Tok::word, LINES>(pz, at, Tok::put(&gz));
-    px -= p.gx, pr -= p.gr, pi -= p.gi;
-    if (GATE) pz -= p.gz;
-  };
+  // rows from the wave's last token to its first; a token past the row's end writes its
+  // zeros to the last row, which its own token then overwrites
+  const int64_t end = b * L + t0 + rows - 1;
+  const int64_t sx = step(p.gx), sr = step(p.gr), si = step(p.gi), sz = step(p.gz);
+  Tin* px = static_cast<Tin*>(p.dx) + end * sx;
+  Tin* pr = static_cast<Tin*>(p.dr) + end * sr;
+  Tin* pi = static_cast<Tin*>(p.di) + end * si;
+  Tin* pz = GATE ? static_cast<Tin*>(p.dz) + end * sz : nullptr;
+  const uint32_t at = here(cb);
   auto token = [&](int k) __attribute__((always_inline)) {
     float gy = xg[k].get_dy(), gz = 0.f;
     if (GATE) {
@@ -259,24 +267,16 @@ __global__ __launch_bounds__(64 * kGlrWaves, 3) void glr_bwd_kernel(GlrBwdParams
       if (p.dh0) p.dh0[static_cast<int64_t>(sp.seq_of(k)) * D + c] = e;
       e = 0.f;
     }
-    put(gx, gr, gi, gz);
+    row_store<typename Tok::word, LINES>(px, at, Tok::put(&gx));
+    row_store<typename Tok::word, LINES>(pr, at, Tok::put(&gr));
+    row_store<typename Tok::word, LINES>(pi, at, Tok::put(&gi));
+    if (GATE) row_store<typename Tok::word, LINES>(pz, at, Tok::put(&gz));
+    px -= k < rows ? sx : 0, pr -= k < rows ? sr : 0, pi -= k < rows ? si : 0;
+    if (GATE) pz -= k < rows ? sz : 0;
   };
-  if (mine) {
-    if (sp.valid == K) {
-      apart<true>();
-      at = here(cb);
+  if (mine && rows > 0) {
 #pragma unroll
-      for (int k = K - 1; k >= 0; --k) token(k);
-      apart<true>();
-    } else {
-      apart<false>();
-#pragma unroll
-      for (int k = K - 1; k >= 0; --k) {
-        if (k < sp.valid) token(k);
-        else if (k < rows) put(0.f, 0.f, 0.f, 0.f);
-      }
-      apart<false>();
-    }
+    for (int k = K - 1; k >= 0; --k) token(k);
   }
   if (!PACKED && p.dh0 && mine && tile == 0 && w == 0) p.dh0[b * D + c] = e;
 

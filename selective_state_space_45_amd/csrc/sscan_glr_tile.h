@@ -54,6 +54,13 @@ __device__ __forceinline__ uint32_t here(uint32_t at) {
   return at;
 }
 
+// A row's stride, to be added from row to row: known to the compiler it becomes all its
+// multiples, for which there are not the scalar registers.
+__device__ __forceinline__ int64_t step(int64_t stride) {
+  asm volatile("" : "+s"(stride));
+  return stride;
+}
+
 // Marks the begin and the end of the code for a whole wave of 16 tokens and of that for a
 // short one: where they are alike the compiler takes them together before or after the
 // branch, with every address and product of either in vector registers.
