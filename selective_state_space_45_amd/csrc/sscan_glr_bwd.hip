@@ -79,12 +79,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACKED || GATE || sizeof(Tin) == 4 
   __shared__ int sReset[W], sTile;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct;
-  // Workgroups go round-robin over the 8 XCDs.  Two neighbouring chains share the cache
-  // lines of the 8-bit codes (64 bytes of 128 each), so they go to one XCD: a 16-set of
-  // chains takes them in the order 0, 2, .., 14, 1, 3, .. (from 8 bits, 8 x 4096 x 2048,
-  // forward and backward: 0.408 ms, in order 0.418; from bf16 0.360 and 0.364).
-  uint32_t chain = blockIdx.x % nchains;
-  if (chain < nchains / 16 * 16) chain = (chain & ~15u) | (chain & 7u) << 1 | (chain >> 3 & 1u);
+  const uint32_t chain = glr_chain(blockIdx.x, nchains);
   int pos = 0;
   if (ntiles > 1) {
     if (threadIdx.x == 0)

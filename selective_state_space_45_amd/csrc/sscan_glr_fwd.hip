@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE && sizeof(Tin) == 4
   __shared__ int sReset[W], sTile;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct;
-  const uint32_t chain = blockIdx.x % nchains;
+  const uint32_t chain = glr_chain(blockIdx.x, nchains);
   int tile = 0;
   if (ntiles > 1) {
     if (threadIdx.x == 0)
