@@ -67,8 +67,9 @@ struct GlrPair<bf16_t, Act> {
 // wait for it and stays in registers.  With two channels a lane that does not fit, and
 // formed again after the wait it costs more than the second channel saves (8 x 4096 x 2048
 // bf16, forward and backward: 0.442 ms, and 0.397 with one).  Four waves a SIMD for bf16
-// without a gate (0.361 ms, with three 0.381); the other forms spill at four (with a gate,
-// 2 x 2047 x 1535 float32: 0.163 ms, with three 0.108).  8 x 4096 x 2048 bf16: 0.22 ms.
+// without a gate (0.361 ms, with three 0.381); the other forms spill at four (2 x 2047 x
+// 1535 float32, gated, in an earlier form: 0.163 ms, with three 0.118).  8 x 4096 x 2048
+// bf16: 0.22 ms.
 template <typename Tin, bool LINES, bool PACKED, bool GATE, bool SAVED>
 __global__ __launch_bounds__(64 * kGlrWaves, PACKED || GATE || sizeof(Tin) == 4 ? 3 : 4) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
                                                                  int ntiles, int nct) {
