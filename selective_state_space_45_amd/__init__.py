@@ -444,6 +444,11 @@ def _stream_at(t: torch.Tensor):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+def _dense_like(x: torch.Tensor) -> torch.Tensor:
+    """A dense tensor of x's shape (empty_like is the cheaper call, where it gives that)."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _strides(values, dim: int):
     for v in values:
         if v != dim:
@@ -549,7 +554,7 @@ def sscan_glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.
     pi, si = _rows(i, "i", dtype, shape)
     pz, sz = (None, dim) if z is None else _rows(z, "z", dtype, shape)
     poff, nseq = _nseq(offsets, batch)
-    y = torch.empty(shape, dtype=dtype, device=x.device) if out is None else out
+    y = _dense_like(x) if out is None else out
     if last_state is None and return_last_state:
         last_state = torch.empty((nseq, dim), dtype=torch.float32, device=x.device)
     workspace, pw, nw = _scratch(workspace, _lib.sscan_glr_fwd_workspace_size(batch, seqlen, dim), x.device)
@@ -586,6 +591,7 @@ def sscan_glr_bwd(lam: torch.Tensor, dy: torch.Tensor, checkpoints: torch.Tensor
         raise ValueError("dy must be float32 or bfloat16")
     batch, seqlen, dim = shape = dy.shape
     dtype, dev = dy.dtype, dy.device
+    pdy = _at(dy, "dy", dtype, shape)
     px = pr = pi = pz = None
     sx = sr = si = sz = dim
     if saved is not None:
@@ -606,7 +612,7 @@ def sscan_glr_bwd(lam: torch.Tensor, dy: torch.Tensor, checkpoints: torch.Tensor
     for name in ("dx", "dr", "di", "dz") if gated else ("dx", "dr", "di"):
         g = out.get(name)
         if g is None:
-            g = out[name] = torch.empty(shape, dtype=dtype, device=dev)
+            g = out[name] = torch.empty_like(dy)
         grads.append(_rows(g, name, dtype, shape))
     if not gated:
         grads.append((None, dim))
@@ -620,7 +626,7 @@ def sscan_glr_bwd(lam: torch.Tensor, dy: torch.Tensor, checkpoints: torch.Tensor
         batch, seqlen, dim, _DTYPES[dtype], px, pr, pi, pz, _strides((sx, sr, si, sz), dim), *_bytes_at(saved, "saved"),
         _at(lam, "lam", f32, per_channel), _at(r_bias, "r_bias", f32, per_channel),
         _at(i_bias, "i_bias", f32, per_channel), decay_scale, _at(initial_state, "initial_state", f32, per_seq), poff, nseq,
-        *_bytes_at(checkpoints, "checkpoints"), _at(dy, "dy", dtype, shape),
+        *_bytes_at(checkpoints, "checkpoints"), pdy,
         _at(dlast_state, "dlast_state", f32, per_seq), grads[0][0], grads[1][0], grads[2][0], grads[3][0],
         _strides([g[1] for g in grads], dim), _at(out["dlam"], "dlam", f32, per_channel),
         _at(out.get("dr_bias"), "dr_bias", f32, per_channel), _at(out.get("di_bias"), "di_bias", f32, per_channel),
@@ -652,7 +658,7 @@ def sscan_glr_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: tor
     if state.dim() != 2:
         raise ValueError("state must be [slots, dim]")
     pool = state.shape[0]
-    y = torch.empty(shape, dtype=dtype, device=x.device) if out is None else out
+    y = _dense_like(x) if out is None else out
     f32, per_channel, per_row = torch.float32, (dim,), (batch,)
     rc = _lib.sscan_glr_step(
         batch, dim, _DTYPES[dtype], _at(state, "state", f32, (pool, dim)), pool, _at(slots, "slots", torch.int32, per_row),
