@@ -137,3 +137,50 @@ def test_many_requests(ss):
     y, last = ss.sscan_glr_fwd(**dev, offsets=torch.from_numpy(off).cuda(), return_last_state=True)
     ry, rl, _ = glr.fwd(**w, offsets=off)
     assert np.abs(y.double().cpu().numpy() - ry).max() <= 1e-4 and np.abs(last.double().cpu().numpy() - rl).max() <= 1e-4
+
+
+@pytest.mark.parametrize("offsets", [None, [0, 0, 70, 71, 400, 400, 1500]])
+def test_states_in_place(ss, offsets):
+    """The last states over the initial ones: the same values as in a buffer of their own, with
+    sequences over many tiles, inside one, and empty."""
+    g = torch.Generator("cuda").manual_seed(4)
+    B, L, D = (3 if offsets is None else 1), 1500, 260
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    w = dict(x=n(B, L, D), r=n(B, L, D), i=n(B, L, D), lam=n(D) - 3)
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    h0 = n(B if off is None else len(offsets) - 1, D)
+    ck = torch.empty(ss.glr_checkpoint_bytes(B, L, D) // 4, device="cuda")
+    y, last = ss.sscan_glr_fwd(**w, offsets=off, initial_state=h0, checkpoints=ck, return_last_state=True)
+    for _ in range(5):
+        state, ck2 = h0.clone(), torch.empty_like(ck)
+        y2 = ss.sscan_glr_fwd(**w, offsets=off, initial_state=state, last_state=state, checkpoints=ck2)
+        assert torch.equal(y, y2) and torch.equal(state, last) and torch.equal(ck, ck2)
+
+
+def test_two_streams_at_once(ss):
+    """Two long sequences, forward and backward, each on a stream of its own: calls that share
+    the chip share nothing else."""
+    def inputs(seed):
+        g = torch.Generator("cuda").manual_seed(seed)
+        n = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+        L, D = 20000, 192
+        return dict(x=n(1, L, D), r=n(1, L, D), i=n(1, L, D)), n(1, L, D), torch.zeros(D, device="cuda") - 3
+
+    def both(w, dy, lam):
+        ck = torch.empty(ss.glr_checkpoint_bytes(*dy.shape) // 4, device="cuda")
+        y = ss.sscan_glr_fwd(**w, lam=lam, checkpoints=ck)
+        return [y] + list(ss.sscan_glr_bwd(lam, dy, ck, **w).values())
+
+    sets = [inputs(1), inputs(2)]
+    alone = [both(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    together = [[], []]
+    for _ in range(4):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                together[k].append(both(*sets[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for got in together[k]:
+            assert all(torch.equal(a, b) for a, b in zip(got, alone[k]))
