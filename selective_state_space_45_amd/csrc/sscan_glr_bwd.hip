@@ -319,6 +319,10 @@ __global__ __launch_bounds__(1024) void glr_param_kernel(const float* part, cons
 #pragma unroll
   for (int q = 1; q < 16; ++q) s += sum[set + 4 * q][lane];
   sum[set][lane] = s;
+  // the wave's writes before its reads of them below: without it the compiler may put them
+  // the other way round, since a lane of set 0 reads none that it wrote
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
   const int64_t d = static_cast<int64_t>(ct) * 64 + quarter * 16 + lane;
   if (set > 0 || d >= D) return;
   s = ((s + sum[1][lane]) + sum[2][lane]) + sum[3][lane];

@@ -1,0 +1,37 @@
+"""GPU: the gated linear recurrence and the 8-bit activations where they can go wrong, against
+the plain float64 form.  `close` and its bounds are those of the recurrence's
+other tests."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import glr
+from test_gpu_glr import BF, F32, Work, close, run_fwd, ss  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,L", [(149, 130), (150, 130), (300, 130), (1, 33000)])
+def test_parameter_sums_over_many_tiles(ss, dtype, B, L):  # noqa: F811
+    """447 and 450 tiles (around the 448 from which the sums are taken eight tiles at a time),
+    900 in short rows, and 516 of one sequence.  Per channel: the sum's terms carry a relative
+    error below 3e-6 each, so their sum one below 3e-6 of the sum of their magnitudes; adding
+    n of them in partial sums of at most n / 64 adds (n / 64 + 8) 2^-24 of it."""
+    w = Work(B, L, 5, dtype, seed=B + L, gate=False)
+    _, _, ck = run_fwd(ss, w)
+    before = glr.fwd(**w.refs(), **w.par)[2]
+    close(ck.view(B, -1, 5), before[:, ::64], F32, "checkpoints")
+    dl = torch.from_numpy(w.dl).cuda()
+    g = ss.sscan_glr_bwd(dy=w.dy, checkpoints=ck, dlast_state=dl, **w.inputs(), **w.dpar)
+    ref = glr.bwd(**w.refs(), dy=w.ref["dy"], dlast_state=w.dl, before=before, **w.par)
+    lam = w.par["lam"].astype(np.float64)
+    rho = 1 / (1 + np.exp(-(w.ref["r"] + w.par["r_bias"])))
+    each = {"dr_bias": ref["dr"], "di_bias": ref["di"],
+            "dlam": ref["dr"] / (np.log1p(np.exp(lam)) * (1 + np.exp(-lam)) * (1 - rho))}
+    tiles = B * -(-L // 64)
+    for k, terms in each.items():
+        np.testing.assert_allclose(terms.sum((0, 1)), ref[k], rtol=1e-9, atol=1e-12 * np.abs(terms).sum())
+        size = np.abs(terms).sum((0, 1))
+        err = np.abs(g[k].double().cpu().numpy() - ref[k])
+        assert (err <= (3e-6 + (tiles / 64 + 8) * 2.0 ** -24) * size).all(), (k, err / size)
