@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACKED || GATE || sizeof(Tin) == 4 
     rho[k] = gate(ar.get(rr[k]), nrb);
     iota[k] = gate(ai.get(ri[k]), nib);
     a[k] = decay_of(rate2 * rho[k], one);
-    m[k] = hw_sqrt(fmaxf(one, 1e-36f));
+    m[k] = hw_sqrt(__builtin_elementwise_maximum(one, 1e-36f));   // (a NaN stays one)
   }
   GlrPair<Tin, Act> xg[K];
 #pragma unroll

@@ -35,3 +35,22 @@ def test_parameter_sums_over_many_tiles(ss, dtype, B, L):  # noqa: F811
         size = np.abs(terms).sum((0, 1))
         err = np.abs(g[k].double().cpu().numpy() - ref[k])
         assert (err <= (3e-6 + (tiles / 64 + 8) * 2.0 ** -24) * size).all(), (k, err / size)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("name", ["r", "i", "x", "lam", "r_bias"])
+@pytest.mark.parametrize("offsets", [None, [0, 20, 120, 150]])
+def test_nan_reaches_every_gradient_that_depends_on_it(ss, name, dtype, offsets):  # noqa: F811
+    """A NaN in one channel: the gradients are not finite exactly where the formula's are not."""
+    w = Work(1 if offsets else 2, 150, 8, dtype, seed=9, gate=False, offsets=offsets)
+    if name in w.dev:
+        w.dev[name][0, 70, 3] = float("nan")
+        w.ref[name][0, 70, 3] = np.nan
+    else:
+        w.dpar[name][3] = float("nan")
+        w.par[name][3] = np.nan
+    _, _, ck = run_fwd(ss, w)
+    g = ss.sscan_glr_bwd(dy=w.dy, checkpoints=ck, dlast_state=torch.from_numpy(w.dl).cuda(), **w.inputs(), **w.dpar)
+    ref = glr.bwd(**w.refs(), dy=w.ref["dy"], dlast_state=w.dl, **w.par)
+    for k in ("dx", "dr", "di", "dlam", "dr_bias", "di_bias", "dinitial_state"):
+        assert np.array_equal(torch.isfinite(g[k]).cpu().numpy(), np.isfinite(ref[k])), k
