@@ -273,6 +273,17 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACKED || GATE || sizeof(Tin) == 4 
   if (mine && rows > 0) {
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) token(k);
+    // padding has no gradient, though a factor of its zeros may be infinite or NaN (lam, or the
+    // power of two that 8-bit codes share with a request's last tokens)
+    if (PACKED) {
+      for (int64_t t = b * L + t0 + sp.valid; t <= end; ++t) {
+        const typename Tok::word none = {};
+        row_store<typename Tok::word, LINES>(static_cast<Tin*>(p.dx) + t * sx, at, none);
+        row_store<typename Tok::word, LINES>(static_cast<Tin*>(p.dr) + t * sr, at, none);
+        row_store<typename Tok::word, LINES>(static_cast<Tin*>(p.di) + t * si, at, none);
+        if (GATE) row_store<typename Tok::word, LINES>(static_cast<Tin*>(p.dz) + t * sz, at, none);
+      }
+    }
   }
   if (!PACKED && p.dh0 && mine && tile == 0 && w == 0) p.dh0[b * D + c] = e;
 

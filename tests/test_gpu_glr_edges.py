@@ -54,3 +54,34 @@ def test_nan_reaches_every_gradient_that_depends_on_it(ss, name, dtype, offsets)
     ref = glr.bwd(**w.refs(), dy=w.ref["dy"], dlast_state=w.dl, **w.par)
     for k in ("dx", "dr", "di", "dlam", "dr_bias", "di_bias", "dinitial_state"):
         assert np.array_equal(torch.isfinite(g[k]).cpu().numpy(), np.isfinite(ref[k])), k
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("name", ["x", "r", "i", "z", "dy", "lam"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kept", [False, True])
+def test_padding_has_no_gradient_beside_nonfinite_tokens(ss, name, dtype, bad, kept):  # noqa: F811
+    """An infinity or NaN in the last request's last tokens, of whose group of 16 the rest is
+    padding (or in a parameter): zeros at the padding all the same, and the requests before it,
+    whose groups are others, as without it."""
+    w = Work(1, 200, 40, dtype, seed=7, offsets=[0, 32, 101])
+
+    def both():
+        saved = torch.empty(ss.glr_saved_bytes(1, 200, 40, True), dtype=torch.uint8, device="cuda") if kept else None
+        y, _, ck = run_fwd(ss, w, saved=saved)
+        given = dict(saved=saved, gated=True) if kept else w.inputs()
+        return y, ss.sscan_glr_bwd(dy=w.dy, checkpoints=ck, **given, **w.dpar)
+
+    y0, g0 = both()
+    if name == "lam":
+        w.dpar["lam"][::3] = bad
+    else:
+        (w.dy if name == "dy" else w.dev[name])[:, 99, ::3] = bad
+    y, g = both()
+    assert not y[:, 101:].any()
+    for k in ("dx", "dr", "di", "dz"):
+        assert not g[k][:, 101:].any(), k              # true of NaN too
+        if name != "lam":
+            assert torch.equal(g[k][:, :32], g0[k][:, :32]), k
+    if name in ("x", "lam", "dy"):                     # it was met (an infinite gate is an open one)
+        assert not all(torch.isfinite(g[k][:, 32:101]).all() for k in ("dx", "dr", "di"))
