@@ -386,6 +386,9 @@ sscan_status sscan_bwd_checkpointed(int64_t batch, int64_t seqlen, int64_t dim, 
  * strides: host array of 4 token strides of x, r, i, z in elements (each at least
  * dim), so that the inputs can be columns of one projection's output: token t of
  * batch row b is at (b seqlen + t) stride.  NULL: all dense.  y and dy are dense.
+ *
+ * Limits: seqlen at most SSCAN_MAX_SEQLEN, dim at most 2^28, and batch ceil(seqlen / 64)
+ * ceil(dim / 64) below 2^31 (for one token: seqlen 1).
  */
 
 /* Tokens between the saved states of sscan_glr_fwd's checkpoints. */
@@ -414,6 +417,7 @@ size_t sscan_act8_bytes(int64_t batch, int64_t seqlen, int64_t dim);
  * 0 for dense) into `packed`, and back into a dense x.  The values that come back are
  * rounded to dtype (bfloat16 holds every packed value exactly).  packed must be
  * 256-byte aligned, of packed_bytes >= sscan_act8_bytes, and overlap no tensor.
+ * batch ceil(seqlen / 16) dim is at most 2^39 - 257.
  */
 sscan_status sscan_act8_pack(int64_t batch, int64_t seqlen, int64_t dim, int dtype, const void* x,
                              int64_t x_stride, void* packed, size_t packed_bytes, void* stream);

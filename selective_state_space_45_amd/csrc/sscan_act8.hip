@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void act8_pack_kernel(const Tin* x, int64_t st
                                                         int64_t lanes, int64_t words, int64_t ngrp, int64_t L, int64_t dim) {
   typedef typename ActWords<Tin, VEC>::elems Elems;
   typedef typename ActWords<Tin, VEC>::bytes Bytes;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t id = static_cast<int64_t>(workgroup<256>()) * 256 + threadIdx.x;
   if (id >= lanes) return;
   const ActPlace at(id, words, ngrp, VEC);
   const int64_t t0 = at.g * kActGroup, row0 = at.b * L + t0;
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void act8_unpack_kernel(const int8_t* codes, c
                                                           int64_t words, int64_t ngrp, int64_t L, int64_t dim) {
   typedef typename ActWords<Tin, VEC>::elems Elems;
   typedef typename ActWords<Tin, VEC>::bytes Bytes;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t id = static_cast<int64_t>(workgroup<256>()) * 256 + threadIdx.x;
   if (id >= lanes) return;
   const ActPlace at(id, words, ngrp, VEC);
   const int64_t t0 = at.g * kActGroup, row0 = at.b * L + t0;
@@ -115,7 +115,7 @@ int act_vec(const void* x, size_t elem, int64_t stride, int64_t dim, int most) {
 template <typename Tin, int VEC>
 hipError_t pack(const void* x, int64_t stride, void* packed, int64_t batch, int64_t L, int64_t dim, hipStream_t s) {
   const int64_t ngrp = (L + kActGroup - 1) / kActGroup, words = dim / VEC, lanes = batch * ngrp * words;
-  hipLaunchKernelGGL((act8_pack_kernel<Tin, VEC>), dim3(static_cast<unsigned>((lanes + 255) / 256)), dim3(256), 0, s,
+  hipLaunchKernelGGL((act8_pack_kernel<Tin, VEC>), grid_of<256>((lanes + 255) / 256), dim3(256), 0, s,
                      static_cast<const Tin*>(x), stride, static_cast<int8_t*>(packed),
                      static_cast<uint8_t*>(packed) + act8_exps_at(batch, L, dim), lanes, words, ngrp, L, dim);
   return hipGetLastError();
@@ -124,7 +124,7 @@ hipError_t pack(const void* x, int64_t stride, void* packed, int64_t batch, int6
 template <typename Tin, int VEC>
 hipError_t unpack(const void* packed, void* x, int64_t batch, int64_t L, int64_t dim, hipStream_t s) {
   const int64_t ngrp = (L + kActGroup - 1) / kActGroup, words = dim / VEC, lanes = batch * ngrp * words;
-  hipLaunchKernelGGL((act8_unpack_kernel<Tin, VEC>), dim3(static_cast<unsigned>((lanes + 255) / 256)), dim3(256), 0, s,
+  hipLaunchKernelGGL((act8_unpack_kernel<Tin, VEC>), grid_of<256>((lanes + 255) / 256), dim3(256), 0, s,
                      static_cast<const int8_t*>(packed), static_cast<const uint8_t*>(packed) + act8_exps_at(batch, L, dim),
                      static_cast<Tin*>(x), lanes, words, ngrp, L, dim);
   return hipGetLastError();

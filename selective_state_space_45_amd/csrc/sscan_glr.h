@@ -98,6 +98,19 @@ inline size_t act8_total(int64_t batch, int64_t L, int64_t dim) {
   return act8_exps_at(batch, L, dim) + ((exps + 255) & ~size_t(255));
 }
 
+// Grids.  HIP counts a launch's threads along an axis in 32 bits, so workgroups of THREADS
+// beyond 2^31 threads go on in further rows of the grid; the last row is filled up with
+// workgroups past the number asked for, which end at once.
+template <int THREADS>
+constexpr uint32_t kGridRow = (uint32_t(1) << 31) / THREADS;
+template <int THREADS>
+inline dim3 grid_of(int64_t n) {
+  constexpr int64_t row = kGridRow<THREADS>;
+  return n <= row ? dim3(static_cast<unsigned>(n)) : dim3(static_cast<unsigned>(row), static_cast<unsigned>((n + row - 1) / row));
+}
+template <int THREADS>
+__device__ __forceinline__ uint32_t workgroup() { return blockIdx.y * kGridRow<THREADS> + blockIdx.x; }
+
 // sigmoid(v) = 1 / (1 + e^-v).  e^-v overflows to infinity for v below -88, whose
 // reciprocal is the right 0.
 __device__ __forceinline__ float sigmoid(float v) { return hw_rcp(1.f + hw_exp2(-v * kLog2e)); }

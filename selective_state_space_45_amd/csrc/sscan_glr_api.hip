@@ -44,7 +44,8 @@ int check_sizes(int64_t batch, int64_t seqlen, int64_t dim, int dtype) {
   return SSCAN_OK;
 }
 
-// The recurrence's launches count their tiles (64 tokens, at least 64 channels) in 31 bits.
+// The recurrence's kernels count their tiles (64 tokens, at least 64 channels) in 31 bits,
+// and its step its workgroups, which are fewer; grid_of gives launches of any such number.
 // A channel's byte offset in a row is held in 32.
 int check_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
   if (dim > (1 << 28)) return fail(SSCAN_ERR_INVALID_ARG, "dim too large");
@@ -54,7 +55,7 @@ int check_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
   return SSCAN_OK;
 }
 
-// One lane each for `n` items, 256 a workgroup, counts its workgroups in 31 bits.
+// One lane each for `n` items, 256 a workgroup, whose number is held in 31 bits.
 int check_lanes(int64_t n) {
   return n / 256 < INT32_MAX ? int(SSCAN_OK) : fail(SSCAN_ERR_INVALID_ARG, "batch*seqlen*dim too large");
 }

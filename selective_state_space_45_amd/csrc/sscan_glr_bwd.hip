@@ -79,14 +79,17 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACKED || GATE || sizeof(Tin) == 4 
   __shared__ float sA[W][64], sB[W][64], sG[W][64], sE[64];
   __shared__ int sReset[W], sTile;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct;
-  const uint32_t chain = glr_chain(blockIdx.x, nchains);
+  const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct, block = workgroup<64 * kGlrWaves>();
+  const uint32_t chain = glr_chain(block, nchains);
   int pos = 0;
   if (ntiles > 1) {
     if (threadIdx.x == 0)
       sTile = static_cast<int>(atomicAdd(&words.tickets[static_cast<size_t>(chain) * kGlrTicket], 1u));
     __syncthreads();
     pos = __builtin_amdgcn_readfirstlane(sTile);
+    if (pos >= ntiles) return;   // a grid that is filled up has more workgroups than tiles
+  } else if (block >= nchains) {
+    return;
   }
   const int tile = ntiles - 1 - pos;
   const int64_t b = chain / nct;
@@ -308,7 +311,9 @@ __global__ __launch_bounds__(1024) void glr_param_kernel(const float* part, cons
                                                          int nct) {
   __shared__ float sum[64][16];
   const int set = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  const int kind = blockIdx.x % 3, quarter = blockIdx.x / 3 % 4, ct = blockIdx.x / 12;
+  const uint32_t block = workgroup<1024>();
+  const int kind = block % 3, quarter = block / 3 % 4, ct = block / 12;
+  if (ct >= nct) return;
   const int64_t n = batch * ntiles;
   auto at = [&](int64_t k) {
     const int64_t b = k / ntiles, tile = k - b * ntiles;
@@ -346,7 +351,7 @@ namespace {
 
 template <typename Tin, bool LINES, bool PACKED, bool GATE>
 void launch_saved(const GlrBwdParams& p, const GlrChainLayout& lo, float* part, int nct, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(lo.chains * lo.tiles)), wg(64 * kGlrWaves);
+  const dim3 grid = grid_of<64 * kGlrWaves>(lo.chains * lo.tiles), wg(64 * kGlrWaves);
   const GlrChainWords w = lo.at(p.workspace);
   const int nt = static_cast<int>(lo.tiles);
   if (p.codes) hipLaunchKernelGGL((glr_bwd_kernel<Tin, LINES, PACKED, GATE, true>), grid, wg, 0, s, p, w, part, nt, nct);
@@ -383,7 +388,7 @@ hipError_t launch_t(const GlrBwdParams& p, hipStream_t s) {
                                                 : launch_lines<Tin, false>(p, lo, part, nct, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(glr_param_kernel, dim3(static_cast<unsigned>(12 * nct)), dim3(1024), 0, s, part, p.lam, p.decay_scale,
+  hipLaunchKernelGGL(glr_param_kernel, grid_of<1024>(int64_t(12) * nct), dim3(1024), 0, s, part, p.lam, p.decay_scale,
                      p.dlam, p.dr_bias, p.di_bias, p.batch, lo.tiles, p.dim, nct);
   return hipGetLastError();
 }

@@ -49,14 +49,17 @@ __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE && sizeof(Tin) == 4
   __shared__ float sA[W][V][64], sB[W][V][64], sH[V][64];
   __shared__ int sReset[W], sTile;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct;
-  const uint32_t chain = glr_chain(blockIdx.x, nchains);
+  const uint32_t nchains = static_cast<uint32_t>(p.batch) * nct, block = workgroup<64 * kGlrWaves>();
+  const uint32_t chain = glr_chain(block, nchains);
   int tile = 0;
   if (ntiles > 1) {
     if (threadIdx.x == 0)
       sTile = static_cast<int>(atomicAdd(&words.tickets[static_cast<size_t>(chain) * kGlrTicket], 1u));
     __syncthreads();
     tile = __builtin_amdgcn_readfirstlane(sTile);
+    if (tile >= ntiles) return;   // a grid that is filled up has more workgroups than tiles
+  } else if (block >= nchains) {
+    return;
   }
   const int64_t b = chain / nct;
   const int64_t c0 = static_cast<int64_t>(chain % nct) * (64 * V);
@@ -270,7 +273,7 @@ namespace {
 template <typename Tin, int V, bool LINES, bool PACKED, bool GATE>
 void launch_save(const GlrFwdParams& p, const GlrChainLayout& lo, hipStream_t s) {
   const int nct = static_cast<int>((p.dim + 64 * V - 1) / (64 * V)), nt = static_cast<int>(lo.tiles);
-  const dim3 grid(static_cast<unsigned>(lo.chains * lo.tiles)), wg(64 * kGlrWaves);
+  const dim3 grid = grid_of<64 * kGlrWaves>(lo.chains * lo.tiles), wg(64 * kGlrWaves);
   const GlrChainWords w = lo.at(p.workspace);
   if (p.codes) hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, LINES, PACKED, GATE, true>), grid, wg, 0, s, p, w, nt, nct);
   else hipLaunchKernelGGL((glr_fwd_kernel<Tin, V, LINES, PACKED, GATE, false>), grid, wg, 0, s, p, w, nt, nct);

@@ -14,9 +14,10 @@ template <typename Tin, int V>
 __global__ __launch_bounds__(64) void glr_step_kernel(GlrStepParams p, int nct) {
   typedef TokVec<Tin, V> Tok;
   typedef typename TokVec<float, V>::reg State;
-  const int64_t b0 = static_cast<int64_t>(blockIdx.x / nct) * kStepRows;
-  const int64_t c = (static_cast<int64_t>(blockIdx.x % nct) * 64 + threadIdx.x) * V;
-  if (c >= p.dim) return;
+  const uint32_t block = workgroup<64>();
+  const int64_t b0 = static_cast<int64_t>(block / nct) * kStepRows;
+  const int64_t c = (static_cast<int64_t>(block % nct) * 64 + threadIdx.x) * V;
+  if (b0 >= p.batch || c >= p.dim) return;
   const uint32_t at = static_cast<uint32_t>(c * sizeof(Tin)), at4 = static_cast<uint32_t>(c * 4);
   const int rows = p.batch - b0 < kStepRows ? static_cast<int>(p.batch - b0) : kStepRows;
 
@@ -71,7 +72,7 @@ void launch(const GlrStepParams& p, hipStream_t s) {
   for (const void* q : {p.x, p.r, p.i, p.z, static_cast<const void*>(p.y)}) bits |= reinterpret_cast<uintptr_t>(q);
   const bool two = bits % (2 * sizeof(Tin)) == 0 && reinterpret_cast<uintptr_t>(p.state) % 8 == 0;
   const int nct = static_cast<int>((p.dim + (two ? 127 : 63)) / (two ? 128 : 64));
-  const dim3 grid(static_cast<unsigned>(nct * ((p.batch + kStepRows - 1) / kStepRows)));
+  const dim3 grid = grid_of<64>(nct * ((p.batch + kStepRows - 1) / kStepRows));
   if (two) hipLaunchKernelGGL((glr_step_kernel<Tin, 2>), grid, dim3(64), 0, s, p, nct);
   else hipLaunchKernelGGL((glr_step_kernel<Tin, 1>), grid, dim3(64), 0, s, p, nct);
 }

@@ -85,3 +85,121 @@ def test_padding_has_no_gradient_beside_nonfinite_tokens(ss, name, dtype, bad, k
             assert torch.equal(g[k][:, :32], g0[k][:, :32]), k
     if name in ("x", "lam", "dy"):                     # it was met (an infinite gate is an open one)
         assert not all(torch.isfinite(g[k][:, 32:101]).all() for k in ("dx", "dr", "di"))
+
+
+def torch_gates(x, r, i, lam):
+    """a, m and the input u in float64, on the GPU (no biases, scale 8)."""
+    rate = 8 * torch.nn.functional.softplus(lam.double(), threshold=60)
+    q = rate * torch.sigmoid(r.double())
+    m = torch.sqrt(-torch.expm1(-2 * q))
+    return torch.exp(-q), m, torch.sigmoid(i.double()) * x.double()
+
+
+def close_there(got, want):
+    err = (got.double() - want).abs()
+    assert bool((err <= 1e-4 * (1 + want.abs())).all()) and float(err.norm()) <= 3e-6 * float(want.norm())
+
+
+def test_more_tiles_than_one_grid_row(ss):  # noqa: F811
+    """2^24 + 3 sequences of one token and channel, each a workgroup of 256 threads of its own:
+    past 2^32 threads, which a launch takes in further rows of its grid only."""
+    B = 2 ** 24 + 3
+    g = torch.Generator("cuda").manual_seed(1)
+    n = lambda: torch.randn(B, 1, 1, generator=g, device="cuda")
+    x, r, i, dy = n(), n(), n(), n()
+    lam, h0 = torch.tensor([-2.0], device="cuda"), n().view(B, 1)
+    ck = torch.empty(ss.glr_checkpoint_bytes(B, 1, 1) // 4, device="cuda")
+    y, last = ss.sscan_glr_fwd(x, r, i, lam, initial_state=h0, checkpoints=ck, return_last_state=True)
+    a, m, u = torch_gates(x, r, i, lam)
+    close_there(y, a * h0.view(B, 1, 1) + m * u)
+    assert torch.equal(y.view(B, 1), last) and torch.equal(ck.view(B, 1), h0)
+    d = ss.sscan_glr_bwd(lam, dy, ck, x=x, r=r, i=i)
+    iota = torch.sigmoid(i.double())
+    close_there(d["dx"], dy.double() * m * iota)
+    close_there(d["di"], dy.double() * m * u * (1 - iota))
+    close_there(d["dinitial_state"], (a * dy.double()).view(B, 1))
+    # a sum of 2^24 terms of random sign, by 64 partial sums of 2^18: 2^18 x 2^-24 of the
+    # magnitudes at the most, which its roundings' random signs leave far below
+    di = dy.double() * m * u * (1 - iota)
+    assert abs(float(d["di_bias"][0]) - float(di.sum())) <= 1e-5 * float(di.abs().sum())
+
+
+def test_more_channels_than_one_grid_row(ss):  # noqa: F811
+    """22.5e6 channels: the parameter sums' 12 workgroups of 1024 threads for each 64 of them
+    pass 2^32 threads."""
+    D = 22_500_001
+    g = torch.Generator("cuda").manual_seed(2)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, r, i, dy = (n(1, 2, D) for _ in range(4))
+    lam = n(D) - 2
+    ck = torch.empty(ss.glr_checkpoint_bytes(1, 2, D) // 4, device="cuda")
+    y = ss.sscan_glr_fwd(x, r, i, lam, checkpoints=ck)
+    d = ss.sscan_glr_bwd(lam, dy, ck, x=x, r=r, i=i)
+    a, m, u = torch_gates(x, r, i, lam)
+    h0 = m[:, 0] * u[:, 0]
+    h = torch.stack([h0, a[:, 1] * h0 + m[:, 1] * u[:, 1]], 1)
+    close_there(y, h)
+    g1 = dy[:, 1].double()
+    gs = torch.stack([dy[:, 0].double() + a[:, 1] * g1, g1], 1)
+    before = torch.stack([torch.zeros_like(h0), h0], 1)
+    dla = gs * (a * before - u * a * a / m)
+    rho = torch.sigmoid(r.double())
+    want = -8 * torch.sigmoid(lam.double()) * (dla * rho).sum((0, 1))
+    size = 8 * torch.sigmoid(lam.double()) * ((gs * a * before).abs() + (gs * u * a * a / m).abs()).sum((0, 1))
+    # each term is off by at most 3e-6 of its two parts, the sum by two roundings more
+    assert bool(((d["dlam"].double() - want).abs() <= 4e-6 * size).all())
+    for k in ("dr", "di"):
+        assert torch.allclose(d[k + "_bias"], d[k][0, 0] + d[k][0, 1], rtol=0, atol=0)
+
+
+def test_more_step_rows_than_one_grid_row(ss):  # noqa: F811
+    """2^28 + 5 rows of one channel: past 2^26 workgroups of 64 threads."""
+    B = 2 ** 28 + 5
+    g = torch.Generator("cuda").manual_seed(3)
+    n = lambda: torch.randn(B, 1, generator=g, device="cuda")
+    x, r, i, state = n(), n(), n(), n()
+    lam, old = torch.tensor([-1.0], device="cuda"), state.clone()
+    y = ss.sscan_glr_step(state, x, r, i, lam)
+    assert torch.equal(y, state)
+    for c in torch.arange(B, device="cuda").split(2 ** 26):
+        s = slice(int(c[0]), int(c[-1]) + 1)
+        a, m, u = torch_gates(x[s], r[s], i[s], lam)
+        close_there(y[s], a * old[s] + m * u)
+
+
+def test_more_packed_lanes_than_one_grid_row(ss):  # noqa: F811
+    """65537 x 65537 single tokens of an odd dim, one lane each: past 2^32 threads.  Whole
+    numbers of at most 7 bits are groups of their own here and come back as they were."""
+    B = D = 65537
+    g = torch.Generator("cuda").manual_seed(4)
+    x = torch.empty(B, 1, D, dtype=torch.bfloat16, device="cuda").random_(-127, 128, generator=g)
+    packed = ss.sscan_act8_pack(x)
+    back = ss.sscan_act8_unpack(packed, (B, 1, D))
+    assert torch.equal(back, x)
+
+
+def test_the_longest_sequence(ss):  # noqa: F811
+    """2^30 tokens of one channel, 2^24 tiles in one chain: windows of it against the float64
+    form run from 512 tokens before to 512 after, over which the decay, about e^-0.5 a token, leaves
+    nothing of what is outside."""
+    L = 2 ** 30
+    g = torch.Generator("cuda").manual_seed(5)
+    x, r, i, dy = (torch.empty(1, L, 1, dtype=BF, device="cuda").normal_(generator=g) for _ in range(4))
+    lam = torch.tensor([-2.0], device="cuda")
+    ck = torch.empty(ss.glr_checkpoint_bytes(1, L, 1) // 4, device="cuda")
+    y, last = ss.sscan_glr_fwd(x, r, i, lam, checkpoints=ck, return_last_state=True)
+    d = ss.sscan_glr_bwd(lam, dy, ck, x=x, r=r, i=i)
+    for lo in (0, 2 ** 29 - 700, 2 ** 29 + 123456, L - 3000):
+        a, b = max(lo - 512, 0), min(lo + 3000 + 512, L)
+        cut = lambda t: t[:, a:b].double().cpu().numpy()
+        w = dict(x=cut(x), r=cut(r), i=cut(i), lam=np.array([-2.0]))
+        ry, rl, _ = glr.fwd(**w)
+        rd = glr.bwd(**w, dy=cut(dy))
+        inner = slice(lo - a, lo - a + 3000)
+        close(y[:, lo:lo + 3000], ry[:, inner], BF, "y")
+        for k in ("dx", "dr", "di"):
+            close(d[k][:, lo:lo + 3000], rd[k][:, inner], BF, k)
+    close(last, rl)
+    # the sum of the rounded gradients, 2^-8 of each apart from the sum that was taken
+    total, size = (float(f(d["di"]).sum(dtype=torch.float64)) for f in (lambda t: t, torch.abs))
+    assert abs(float(d["di_bias"][0]) - total) <= 2.0 ** -8 * size
