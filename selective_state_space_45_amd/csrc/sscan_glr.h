@@ -121,11 +121,18 @@ __device__ __forceinline__ float gate(float v, float nb) { return hw_rcp(1.f + h
 // value, 1/4) where s is close to 1.
 __device__ __forceinline__ float slope(float s) { return fmaf(-s, s, s); }
 
-// softplus(v) = max(v, 0) + log(1 + w), w = e^-|v|, to float32 accuracy at every v:
-// log(1 + w) = 2 atanh(s), s = w / (2 + w) <= 1/3, by its odd series through s^15
-// (the next term is below 2e-9 of the sum).
+// softplus(v) = max(v, 0) + log(1 + w), w = e^-|v|: log(1 + w) = 2 atanh(s),
+// s = w / (2 + w) <= 1/3, by its odd series through s^15 (the next term is below 2e-9 of the
+// sum).  The product |v| log2(e) has a rounding error that grows with |v| (62 units of w's
+// last place at v = -80); what it lacks, with the low part of log2(e) itself, is put back
+// into w to first order, and w keeps a relative error of about three units down to
+// v = -87, below which it is zero.  |v| is bounded for the infinities' sake.
 __device__ __forceinline__ float softplus_acc(float v) {
-  const float w = hw_exp2(-fabsf(v) * kLog2e);
+  constexpr float log2e_low = 1.92596299e-8f;   // log2(e) - kLog2e
+  const float av = fminf(fabsf(v), 128.f), t = av * kLog2e;
+  const float lack = fmaf(av, log2e_low, fmaf(av, kLog2e, -t));
+  float w = hw_exp2(-t);
+  w = fmaf(w, -kLn2 * lack, w);
   const float s = w * hw_rcp(2.f + w);
   const float s2 = s * s;
   float p = fmaf(s2, 1.f / 15.f, 1.f / 13.f);

@@ -203,3 +203,20 @@ def test_the_longest_sequence(ss):  # noqa: F811
     # the sum of the rounded gradients, 2^-8 of each apart from the sum that was taken
     total, size = (float(f(d["di"]).sum(dtype=torch.float64)) for f in (lambda t: t, torch.abs))
     assert abs(float(d["di_bias"][0]) - total) <= 2.0 ** -8 * size
+
+
+def test_decay_rates_at_every_size_of_lam(ss):  # noqa: F811
+    """One step from a zero state with open gates and x = 1 gives sqrt(1 - a^2), which is about
+    the square root of twice the rate: its relative error is half of the rate's, and two units
+    of the last place (2^-24) of the square root's own.  The rate goes through about twelve
+    roundings or one-ulp functions and 1 - a^2 through six more, each at most 2 x 2^-24 (most
+    half of that): below 12 x 2^-24 = 7.2e-7 in all."""
+    lam = np.concatenate([np.linspace(-80, -1, 4001), np.linspace(-1, 3, 500)]).astype(np.float32)
+    D = lam.size
+    f = lambda v: torch.full((1, D), v, device="cuda")
+    state = torch.zeros(1, D, device="cuda")
+    y = ss.sscan_glr_step(state, f(1.0), f(60.0), f(60.0), torch.from_numpy(lam).cuda())
+    rate = 8 * np.log1p(np.exp(lam.astype(np.float64)))
+    ref = np.sqrt(-np.expm1(-2 * rate))
+    err = np.abs(y.double().cpu().numpy()[0] - ref) / ref
+    assert err.max() <= 7.2e-7, (err.max() * 2 ** 24, lam[err.argmax()])
