@@ -464,8 +464,10 @@ sscan_status sscan_glr_fwd(int64_t batch, int64_t seqlen, int64_t dim, int dtype
  *   dr = -decay_scale softplus(lam) dlog_a rho (1 - rho)
  *   dz = dy h silu'(z)                    dinitial_state = a g of the first token
  *   dlam = -decay_scale sigmoid(lam) sum dlog_a rho     (bias gradients: sums of dr and di)
- * Where a rounds to 1 the terms with 1 / sqrt(1 - a^2) take their limit for a vanishing
- * decay rate, zero.
+ * These hold also where a rounds to 1, since 1 - a^2 comes from the decay rate itself.
+ * Only the square root stays at 1e-18 or above, for its reciprocal: where 1 - a^2 is less
+ * than 1e-36 the terms with it vanish with the rate (and iota x up to 1e20 overflows in
+ * none).
  *
  *   checkpoints    : what sscan_glr_fwd wrote for the same inputs (required)
  *   x, r, i, z     : the forward's inputs, or all NULL with `saved`, what the forward

@@ -220,3 +220,26 @@ def test_decay_rates_at_every_size_of_lam(ss):  # noqa: F811
     ref = np.sqrt(-np.expm1(-2 * rate))
     err = np.abs(y.double().cpu().numpy()[0] - ref) / ref
     assert err.max() <= 7.2e-7, (err.max() * 2 ** 24, lam[err.argmax()])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradients_of_tiny_decay_rates(ss, dtype):  # noqa: F811
+    """Rates far below those at which a rounds to 1: the terms with 1 / sqrt(1 - a^2) are the
+    formula's, in proportion to each channel's own size."""
+    w = Work(2, 140, 24, dtype, seed=10, gate=False)
+    lam = np.repeat(np.float32([-75.0, -60.0, -45.0, -30.0, -20.0, -15.0]), 4)
+    w.par["lam"], w.dpar["lam"] = lam, torch.from_numpy(lam).cuda()
+    _, _, ck = run_fwd(ss, w)
+    g = ss.sscan_glr_bwd(dy=w.dy, checkpoints=ck, dlast_state=torch.from_numpy(w.dl).cuda(), **w.inputs(), **w.dpar)
+    before = glr.fwd(**w.refs(), **w.par)[2]
+    ref = glr.bwd(**w.refs(), dy=w.ref["dy"], dlast_state=w.dl, before=before, **w.par)
+    u = 2.0 ** -8 if dtype is BF else 0.0
+    for c in range(24):
+        for k in ("dx", "dr", "di"):
+            got, want = g[k][..., c].double().cpu().numpy(), ref[k][..., c]
+            assert np.linalg.norm(got - want) <= (u + 3e-6) * np.linalg.norm(want), (k, lam[c])
+    rho = 1 / (1 + np.exp(-(w.ref["r"] + w.par["r_bias"])))
+    l64 = lam.astype(np.float64)
+    terms = ref["dr"] / (np.log1p(np.exp(l64)) * (1 + np.exp(-l64)) * (1 - rho))
+    err = np.abs(g["dlam"].double().cpu().numpy() - ref["dlam"])
+    assert (err <= 4e-6 * np.abs(terms).sum((0, 1))).all(), err / np.abs(terms).sum((0, 1))
