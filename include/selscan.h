@@ -379,7 +379,7 @@ sscan_status sscan_bwd_checkpointed(int64_t batch, int64_t seqlen, int64_t dim, 
  * are an empty request, whose last state is its initial one.  Tokens at or past
  * offsets[num_seqs] are padding: y is zero there, and so are their gradients,
  * whatever the inputs hold.  No state passes from one request to the next, infinities
- * and NaN included.  The host does not read offsets; an array that breaks these rules
+ * and NaN included (activations kept in 8 bits share groups, see there).  The host does not read offsets; an array that breaks these rules
  * gives unspecified results, with no access outside the tensors.  "Sequences" below
  * are the batch rows, or the num_seqs requests.
  *
@@ -402,6 +402,13 @@ sscan_status sscan_bwd_checkpointed(int64_t batch, int64_t seqlen, int64_t dim, 
  * in magnitude: the error is at most 2^(e - 7), except for magnitudes within
  * 2^(e - 7) of 2^(e + 1), where it is below 2^(e - 6).  Magnitudes below 2^-126 share
  * e = -126.  A group with an infinity or NaN has the byte 255 and comes back as NaN.
+ *
+ * Groups are cut by position, tokens 16 k .. 16 k + 15, whatever packed requests they
+ * belong to.  Two requests that meet inside a group share its power of two: beside large
+ * values of one the other's are held with less relative precision, and an infinity or NaN
+ * of one turns the other's tokens in the group to NaN, and in a backward pass from 8 bits
+ * their gradients and those that depend on them.  Requests that start at multiples of 16
+ * share nothing.  (The forward's outputs do not come from the 8 bits.)
  *
  * One packed tensor [batch, seqlen, dim] is sscan_act8_bytes bytes: the codes (int8)
  * [batch][seqlen][dim], then, from the next multiple of 256 bytes, the exponent bytes
