@@ -243,3 +243,29 @@ def test_gradients_of_tiny_decay_rates(ss, dtype):  # noqa: F811
     terms = ref["dr"] / (np.log1p(np.exp(l64)) * (1 + np.exp(-l64)) * (1 - rho))
     err = np.abs(g["dlam"].double().cpu().numpy() - ref["dlam"])
     assert (err <= 4e-6 * np.abs(terms).sum((0, 1))).all(), err / np.abs(terms).sum((0, 1))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_8_bit_groups_are_cut_by_position(ss, dtype):  # noqa: F811
+    """In 8 bits the 16 tokens of a group share their power of two whatever requests they belong
+    to: a NaN takes the tokens of its group with it, those of a neighbour too, and the
+    neighbour's gradients that depend on them.  Requests that start at multiples of 16 keep
+    apart."""
+    def grads(offsets, bad):
+        w = Work(1, 96, 5, dtype, seed=3, offsets=offsets)
+        if bad is not None:
+            w.dev["x"][:, bad] = float("nan")
+        saved = torch.empty(ss.glr_saved_bytes(1, 96, 5, True), dtype=torch.uint8, device="cuda")
+        y, _, ck = run_fwd(ss, w, saved=saved)
+        return y, ss.sscan_glr_bwd(dy=w.dy, checkpoints=ck, saved=saved, gated=True, **w.dpar)
+
+    for offsets, spoilt in (([0, 40, 96], range(32, 48)), ([0, 48, 96], range(0))):
+        bad = offsets[1] + 1
+        y0, g0 = grads(offsets, None)
+        y, g = grads(offsets, bad)
+        first = slice(0, offsets[1])
+        assert torch.equal(y[:, first], y0[:, first])           # the forward does not read the 8 bits
+        gone = torch.isnan(g["di"][0, first]).any(1).cpu().numpy()
+        assert np.array_equal(np.flatnonzero(gone), [t for t in spoilt if t < offsets[1]])
+        if not len(spoilt):
+            assert all(torch.equal(g[k][:, first], g0[k][:, first]) for k in ("dx", "dr", "di", "dz"))
