@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import glr
-from test_gpu_glr import BF, F32, Work, close, run_fwd, ss  # noqa: F401
+from test_gpu_glr import BF, F32, Work, check_bwd, check_fwd, close, run_fwd, ss  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -269,3 +269,49 @@ def test_8_bit_groups_are_cut_by_position(ss, dtype):  # noqa: F811
         assert np.array_equal(np.flatnonzero(gone), [t for t in spoilt if t < offsets[1]])
         if not len(spoilt):
             assert all(torch.equal(g[k][:, first], g0[k][:, first]) for k in ("dx", "dr", "di", "dz"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("offsets,L", [([0, 100, 100, 700, 1900], 2000), ([0, 5, 130, 131, 211, 640], 700),
+                                       ([0, 16, 64, 128, 129], 300)])
+def test_packed_rows_of_whole_cache_lines(ss, dtype, gate, fused, offsets, L):  # noqa: F811
+    w = Work(1, L, 128, dtype, seed=6, offsets=offsets, gate=gate, fused=fused)
+    ck, before = check_fwd(ss, w)
+    check_bwd(ss, w, ck, before)
+    n = ss.glr_saved_bytes(1, L, 128, gate)
+    saved = torch.full((n,), 77, dtype=torch.uint8, device="cuda")
+    run_fwd(ss, w, saved=saved)
+    q = {}
+    for k, name in enumerate(w.names):
+        one = ss.act8_bytes(1, L, 128)
+        held = w.ref[name].copy()
+        held[:, offsets[-1]:] = 0.0
+        q[name] = glr.act8(held)
+        v = ss.sscan_act8_unpack(saved[k * one:(k + 1) * one], (1, L, 128), F32)
+        assert np.array_equal(v.double().cpu().numpy(), q[name]), name
+    q = {k: q.get(k) for k in ("x", "r", "i", "z")}
+    check_bwd(ss, w, ck, glr.fwd(**q, **w.par, block_states=before)[2], saved=saved, refs=q)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,L", [(2, 77), (1, 1000), (3, 16)])
+def test_gated_8_bits_in_whole_cache_lines(ss, dtype, B, L):  # noqa: F811
+    w = Work(B, L, 256, dtype, seed=B + L)
+    saved = torch.full((ss.glr_saved_bytes(B, L, 256, True),), 77, dtype=torch.uint8, device="cuda")
+    _, _, ck = run_fwd(ss, w, saved=saved)
+    before = glr.fwd(**w.refs(), **w.par)[2]
+    q = {k: glr.act8(v) for k, v in w.refs().items()}
+    one = ss.act8_bytes(B, L, 256)
+    for k, name in enumerate(w.names):
+        v = ss.sscan_act8_unpack(saved[k * one:(k + 1) * one], (B, L, 256), F32)
+        assert np.array_equal(v.double().cpu().numpy(), q[name]), name
+    check_bwd(ss, w, ck, glr.fwd(**q, **w.par, block_states=before)[2], saved=saved, refs=q)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [70, 33])
+def test_packed_requests_over_groups_of_tiles(ss, dtype, D):  # noqa: F811
+    w = Work(1, 2500, D, dtype, seed=13, offsets=[0, 100, 100, 700, 700, 701, 1900, 2450])
+    check_bwd(ss, w, *check_fwd(ss, w))
