@@ -6,7 +6,7 @@ namespace sscan {
 // A lane holds VEC neighbouring channels of the 16 tokens of a group, so the group's
 // largest magnitude needs no other lane, and loads and stores are whole words.  The work
 // is bound by memory: 2 (float32: 4) bytes an element on one side and 1 + 1/16 on the
-// other.  8 x 4096 x 2048 bf16: packed in 43 us, unpacked in 31 (4.8 and 6.6 TB/s, part of
+// other.  8 x 4096 x 2048 bf16: packed in 45 us, unpacked in 32 (4.6 and 6.4 TB/s, part of
 // the codes still in the last cache); one channel a lane 88 and 142.
 template <typename Tin, int VEC>
 struct ActWords {   // VEC elements, VEC codes

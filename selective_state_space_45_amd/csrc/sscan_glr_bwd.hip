@@ -60,16 +60,18 @@ struct GlrPair<bf16_t, Act> {
 // map with the same factor a, so one exchange through shared memory serves both.
 //
 // 14 bytes an element in bf16 against about 60 vector operations, 7 of them at half rate:
-// counters show the vector units busy half of the time and the memory at 4.2 TB/s; bound
+// counters show the vector units busy half of the time and the memory at 4.5 TB/s; bound
 // by the latency of its phases (a ticket, loads, maps, the wait, stores: 10 us a
 // workgroup) at the waves that the registers allow.  One channel a lane: what the
 // gradients need of each of 16 tokens but the gradient that arrives is formed before the
 // wait for it and stays in registers.  With two channels a lane that does not fit, and
 // formed again after the wait it costs more than the second channel saves (8 x 4096 x 2048
-// bf16, forward and backward: 0.442 ms, and 0.397 with one).  Four waves a SIMD for bf16
-// without a gate (0.361 ms, with three 0.381); the other forms spill at four (2 x 2047 x
-// 1535 float32, gated, in an earlier form: 0.163 ms, with three 0.118).  8 x 4096 x 2048
-// bf16: 0.22 ms.
+// bf16, forward and backward: 0.442 ms, and 0.397 with one).  Four waves a SIMD for dense
+// bf16 without a gate (0.361 ms, with three 0.381), though 5 registers spill; the other
+// forms spill many more at four (2 x 2047 x 1535 float32, gated, in an earlier form: 0.163
+// ms, with three 0.118).  At three the dense forms spill no vector register, gated packed
+// ones 9 or 10 in bf16 and 19 to 21 in float32, and all packed ones about 130 scalar
+// registers, into lanes of vector registers.  8 x 4096 x 2048 bf16: 0.219 ms.
 template <typename Tin, bool LINES, bool PACKED, bool GATE, bool SAVED>
 __global__ __launch_bounds__(64 * kGlrWaves, PACKED || GATE || sizeof(Tin) == 4 ? 3 : 4) void glr_bwd_kernel(GlrBwdParams p, GlrChainWords words, float* part,
                                                                  int ntiles, int nct) {

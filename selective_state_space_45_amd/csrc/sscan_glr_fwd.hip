@@ -39,8 +39,9 @@ __device__ __forceinline__ void glr_save(const typename TokVec<Tin, V>::reg (&ra
 // operations and 6 of the quarter-rate ones, whose time is three quarters of the memory's.
 // The map of a wave's 16 tokens needs each of them once, and so does the output: a and u
 // stay in registers between the two while the state is on its way, and four waves a SIMD
-// cover that wait.  8 x 4096 x 2048 bf16: 0.126 ms, 4.3 TB/s (a large copy reaches 4.9);
-// gated 0.143 ms, 4.7 TB/s; 2 x 2048 x 1536 float32: 20 us, 5.0 TB/s.
+// cover that wait.  8 x 4096 x 2048 bf16: 0.128 ms, 4.2 TB/s (a large copy reaches 4.9);
+// gated 0.145 ms, 4.6 TB/s; 2 x 2048 x 1536 float32: 19 us, 5.3 TB/s.  The gated packed
+// form of two channels a lane spills 2 (float32: 8 to 12) of its registers.
 template <typename Tin, int V, bool LINES, bool PACKED, bool GATE, bool SAVE>
 __global__ __launch_bounds__(64 * kGlrWaves, V == 2 && (GATE && sizeof(Tin) == 4) ? 3 : 4) void glr_fwd_kernel(
     GlrFwdParams p, GlrChainWords words, int ntiles, int nct) {

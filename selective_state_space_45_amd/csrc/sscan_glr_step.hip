@@ -9,7 +9,7 @@ constexpr int kStepRows = 4;   // rows of a workgroup
 // once for them.  A token moves 8 bytes of state a channel besides its inputs and output:
 // bound by memory at large batches and by the launch at small ones.  All loads of a row
 // start before the first is used, the state's after its slot is known.  256 x 5120 bf16,
-// gated: 7.3 us (one row and channel a lane: 8.4); 1 x 1536: 3.9 us, the launch.
+// gated: 7.5 us (one row and channel a lane: 8.4); 1 x 1536: 4.0 us, the launch.
 template <typename Tin, int V>
 __global__ __launch_bounds__(64) void glr_step_kernel(GlrStepParams p, int nct) {
   typedef TokVec<Tin, V> Tok;
