@@ -600,6 +600,8 @@ def sscan_glr_bwd(lam: torch.Tensor, dy: torch.Tensor, checkpoints: torch.Tensor
     else:
         if x is None or r is None or i is None:
             raise ValueError("x, r and i are required without saved")
+        if gated and z is None:
+            raise ValueError("z is required without saved when gated")
         gated = z is not None
         px, sx = _rows(x, "x", dtype, shape)
         pr, sr = _rows(r, "r", dtype, shape)

@@ -30,3 +30,17 @@ def test_packed_lanes(lib):  # noqa: F811
     for n, word in ((most, b"null"), (most + 1, b"too large")):
         assert lib.sscan_act8_pack(n, 1, 1, 0, None, 0, None, 0, None) == INVALID and word in lib.sscan_last_error()
         assert lib.sscan_act8_unpack(n, 1, 1, 0, None, 0, None, None) == INVALID and word in lib.sscan_last_error()
+
+
+def test_binding_refuses_a_gate_without_z():
+    import torch
+    import selective_state_space_45_amd as ss
+
+    class OnGpu(torch.Tensor):                    # as far as the host's checks see
+        is_cuda = True
+
+    x = torch.zeros(1, 4, 8).as_subclass(OnGpu)
+    with pytest.raises(ValueError, match="z is required"):
+        ss.sscan_glr_bwd(torch.zeros(8), x, torch.zeros(8), x=x, r=x, i=x, gated=True)
+    with pytest.raises(ValueError, match="GPU"):
+        ss.sscan_glr_bwd(torch.zeros(8), torch.zeros(1, 4, 8), torch.zeros(8), x=x, r=x, i=x, z=x, gated=True)
