@@ -315,3 +315,30 @@ def test_gated_8_bits_in_whole_cache_lines(ss, dtype, B, L):  # noqa: F811
 def test_packed_requests_over_groups_of_tiles(ss, dtype, D):  # noqa: F811
     w = Work(1, 2500, D, dtype, seed=13, offsets=[0, 100, 100, 700, 700, 701, 1900, 2450])
     check_bwd(ss, w, *check_fwd(ss, w))
+
+
+def test_a_grid_filled_up_beyond_its_tiles(ss):  # noqa: F811
+    """2^22 + 5 sequences of two tiles: 2^23 + 10 workgroups, whose grid of two rows holds nearly
+    twice as many; the last states go over the initial ones."""
+    B, L = 2 ** 22 + 5, 65
+    g = torch.Generator("cuda").manual_seed(6)
+    x, r, i, dy = (torch.empty(B, L, 1, device="cuda").normal_(generator=g) for _ in range(4))
+    lam = torch.tensor([-3.0], device="cuda")
+    state = torch.empty(B, 1, device="cuda").normal_(generator=g)
+    h0 = state.double()
+    ck = torch.empty(ss.glr_checkpoint_bytes(B, L, 1) // 4, device="cuda")
+    y = ss.sscan_glr_fwd(x, r, i, lam, initial_state=state, last_state=state, checkpoints=ck)
+    d = ss.sscan_glr_bwd(lam, dy, ck, x=x, r=r, i=i)
+    a, m, u = torch_gates(x, r, i, lam)
+    h, want = h0, torch.empty_like(a)
+    for t in range(L):
+        h = a[:, t] * h + m[:, t] * u[:, t]
+        want[:, t] = h
+    close_there(y, want)
+    close_there(state, h)
+    e, grad = torch.zeros_like(h), torch.empty_like(a)
+    for t in reversed(range(L)):
+        grad[:, t] = dy[:, t].double() + e
+        e = a[:, t] * grad[:, t]
+    close_there(d["dinitial_state"], e)
+    close_there(d["dx"], grad * m * torch.sigmoid(i.double()))
