@@ -542,7 +542,8 @@ def sscan_glr_fwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.
     GPU): batch is 1 and its tokens are packed requests, the rest padding.  initial_state,
     last_state: [batch or sequences, dim] float32.  checkpoints (``glr_checkpoint_bytes``
     bytes) and saved (``glr_saved_bytes`` bytes) are filled for ``sscan_glr_bwd``, the latter
-    with the activations in 8 bits.  Returns y, or (y, last_state)."""
+    with the activations in 8 bits, whose groups of 16 tokens are cut by position: packed
+    requests that meet inside one share its scale, and a NaN.  Returns y, or (y, last_state)."""
     if x.dim() != 3:
         raise ValueError("x must be [batch, seqlen, dim]")
     if x.dtype not in _DTYPES:
