@@ -39,7 +39,8 @@
  *  - dstate (N) must be in [1, SSCAN_MAX_DSTATE]; seqlen at most SSCAN_MAX_SEQLEN.
  *  - `flags` selects variants of the method (SSCAN_FLAG_*); 0 is the method
  *    as defined above.
- * The gated linear recurrence and the 8-bit activations at the end of this header
+ * The gated linear recurrence and the 8-bit activations, and what stands around
+ * the recurrence in a layer (norm, 8-bit products, convolution), at the end of this header
  * follow the same conventions, with shapes of their own and no flags.
  */
 #ifndef SELSCAN_H
@@ -52,7 +53,7 @@
 extern "C" {
 #endif
 
-#define SSCAN_VERSION 420
+#define SSCAN_VERSION 430
 #define SSCAN_MAX_DSTATE 16
 #define SSCAN_MAX_DCONV 4
 /* Longest sequence sscan_fwd* and sscan_bwd* accept (2^30 steps): the kernels count
@@ -519,6 +520,169 @@ sscan_status sscan_glr_step(int64_t batch, int64_t dim, int dtype, float* state,
                             const int32_t* slots, const int32_t* slots_out, const void* x, const void* r,
                             const void* i, const void* z, const int64_t* strides, const float* lam,
                             const float* r_bias, const float* i_bias, float decay_scale, void* y, void* stream);
+
+/*
+ * What stands around the recurrence in a layer: the norm with the residual's addition,
+ * projections in 8-bit integers, and the short convolution for packed requests and with
+ * its backward pass.  Conventions as above; "rows" are tokens (batch * seqlen of them, or
+ * a decode batch), and a row stride is in elements, 0 for dense.
+ */
+
+/* Channels of a row that sscan_rms_fwd, sscan_rms_bwd and sscan_i8_quant accept. */
+#define SSCAN_RMS_MAX_DIM 65536
+
+/*
+ * Root-mean-square norm with the residual's addition.  For each row:
+ *
+ *   s = x + residual, rounded to residual_dtype (what is kept, and what is normed)
+ *   r = 1 / sqrt(mean(s^2) + eps)          y = s r weight
+ *
+ *   x            : [rows, dim] (dtype), row stride x_stride
+ *   residual     : [rows, dim] (residual_dtype), NULL: s = x rounded to residual_dtype
+ *   weight       : [dim] (float32), NULL: ones
+ *   y            : [rows, dim] (dtype), NULL: not written
+ *   residual_out : [rows, dim] (residual_dtype), s, NULL: not written; may be residual
+ *   codes, scales: y in 8 bits as sscan_i8_quant gives it (from y before its rounding to
+ *                  dtype), both or neither; codes has the row stride codes_stride
+ * residual_dtype is SSCAN_F32, or dtype.  eps is at least 0 and finite.  Sums are float32:
+ * a row whose sum of squares passes float32's range has r = 0.
+ */
+sscan_status sscan_rms_fwd(int64_t rows, int64_t dim, int dtype, int residual_dtype, const void* x, int64_t x_stride,
+                           const void* residual, const float* weight, float eps, void* y, void* residual_out,
+                           int8_t* codes, int64_t codes_stride, float* scales, void* stream);
+
+/* Workspace bytes of sscan_rms_bwd. */
+size_t sscan_rms_bwd_workspace_size(int64_t rows, int64_t dim);
+
+/*
+ * Backward pass of sscan_rms_fwd, given dy = dLoss/dy and, optionally, dresidual_out =
+ * dLoss/ds from the layers that follow.  With g = dy weight:
+ *
+ *   ds = dresidual_out + r g - s r^3 mean(g s)        dweight = sum over rows of dy s r
+ *
+ * ds is the gradient of x and of the residual alike (the rounding of s passes it on).
+ *
+ *   s             : [rows, dim] (residual_dtype), what the forward kept (x itself, of type
+ *                   residual_dtype, if there was no residual), row stride s_stride
+ *   dy            : [rows, dim] (dtype)
+ *   dresidual_out : [rows, dim] (residual_dtype), NULL: zero
+ *   dx            : [rows, dim] (dtype), row stride dx_stride, NULL: not written
+ *   dresidual     : [rows, dim] (residual_dtype), NULL: not written; may be dresidual_out
+ *   dweight       : [dim] (float32), NULL: not written
+ *   workspace     : sscan_rms_bwd_workspace_size, 256-byte aligned (needed for dweight)
+ * Results are bitwise reproducible.
+ */
+sscan_status sscan_rms_bwd(int64_t rows, int64_t dim, int dtype, int residual_dtype, const void* s, int64_t s_stride,
+                           const float* weight, float eps, const void* dy, const void* dresidual_out, void* dx,
+                           int64_t dx_stride, void* dresidual, float* dweight, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Rows in 8-bit integers with a float32 scale for each:
+ *
+ *   scale = max(max |x| / 127, 2^-126)     code = the whole number nearest to x / scale
+ *
+ * (the quotient of the real numbers, ties to even; at most 127 in magnitude).  A row with
+ * an infinity or NaN has the scale NaN and codes 0, so it comes out of a product as NaN.
+ * Weights are brought into this form once, each output's row by itself; activations at each
+ * call, or by sscan_rms_fwd.
+ *
+ *   x      : [rows, dim] (dtype), row stride x_stride
+ *   codes  : [rows, dim] (int8), row stride codes_stride; bytes between rows are not written
+ *   scales : [rows] (float32)
+ */
+sscan_status sscan_i8_quant(int64_t rows, int64_t dim, int dtype, const void* x, int64_t x_stride, int8_t* codes,
+                            int64_t codes_stride, float* scales, void* stream);
+
+/* Products of a row that sscan_i8_matmul sums: any codes (-128 included) stay inside 32 bits. */
+#define SSCAN_I8_MAX_K 131071
+
+/* Workspace bytes of sscan_i8_matmul (0: none needed).  With less, or none, it runs without
+ * splitting the sums over workgroups: the same result, slower. */
+size_t sscan_i8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/*
+ * Product of rows in 8-bit integers, with the scales of both sides:
+ *
+ *   out[i, j] = (sum_l a[i, l] b[j, l]) * (a_scales[i] * b_scales[j]) + bias[j]
+ *
+ * The sums are whole numbers of 32 bits, exact in any order; the rest is float32, rounded
+ * once to dtype at the end.
+ *
+ *   a, a_scales : [m, k] (int8), row stride a_stride; [m] (float32)
+ *   b, b_scales : [n, k] (int8), row stride b_stride; [n] (float32)
+ *   bias        : [n] (float32), NULL: zero
+ *   out         : [m, n] (dtype), row stride out_stride
+ *   workspace   : sscan_i8_matmul_workspace_size, 256-byte aligned, NULL: none
+ * Any strides and alignment work; rows at multiples of 16 bytes are read fastest.  k is at
+ * most SSCAN_I8_MAX_K, m and n at most 2^31 - 1.  With k == 0 the sums are zero.
+ */
+sscan_status sscan_i8_matmul(int64_t m, int64_t n, int64_t k, const int8_t* a, int64_t a_stride,
+                             const float* a_scales, const int8_t* b, int64_t b_stride, const float* b_scales,
+                             const float* bias, int dtype, void* out, int64_t out_stride, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Depthwise causal convolution over time, the prologue of sscan_fwd_conv as an operator of
+ * its own: in front of either recurrence, for packed requests, and with a backward pass.
+ *
+ *   v[t] = conv_b + sum_{k < dconv} conv_w[k] xx[t - (dconv - 1) + k]
+ *   y[t] = v[t], or silu(v[t]) with silu != 0
+ *
+ * where xx is the sequence's x with initial_state (its dconv - 1 raw inputs before, oldest
+ * first; zeros when NULL) in front.  Dense batches or packed requests, offsets and padding
+ * as in sscan_glr_fwd; no value passes from one request to the next.
+ *
+ *   x              : [batch, seqlen, dim] (dtype), token stride x_stride (0: dense)
+ *   conv_w, conv_b : [dim, dconv], [dim] (float32); conv_b NULL: zero
+ *   initial_state  : [sequences, dim, dconv - 1] (float32), NULL: zeros
+ *   y              : [batch, seqlen, dim] (dtype)
+ *   last_state     : [sequences, dim, dconv - 1] (float32): the last dconv - 1 raw inputs
+ *                    (of the initial state where the sequence is shorter), NULL: not
+ *                    written; apart from initial_state
+ * 1 <= dconv <= SSCAN_MAX_DCONV (else SSCAN_ERR_UNSUPPORTED).  Limits as sscan_glr_fwd's.
+ */
+sscan_status sscan_dwconv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t dconv, int dtype, int silu,
+                              const void* x, int64_t x_stride, const float* conv_w, const float* conv_b,
+                              const float* initial_state, const int32_t* offsets, int64_t num_seqs, void* y,
+                              float* last_state, void* stream);
+
+/* Workspace bytes of sscan_dwconv_bwd. */
+size_t sscan_dwconv_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t dconv);
+
+/*
+ * Backward pass, given dy and optionally dlast_state = dLoss/d(last_state).  With
+ * dv = dy, or dy silu'(v), and within each sequence:
+ *
+ *   dx[u] = sum_k conv_w[k] dv[u + (dconv - 1) - k]   (+ dlast_state of the tokens it holds)
+ *   dconv_w[k] = sum_t dv[t] xx[t - (dconv - 1) + k]     dconv_b = sum_t dv[t]
+ *   dinitial_state: the same as dx, of the tokens before the sequence
+ *
+ *   x, conv_w, conv_b, initial_state, offsets, silu: the forward's
+ *   dy             : [batch, seqlen, dim] (dtype)
+ *   dx             : [batch, seqlen, dim] (dtype), token stride dx_stride (0: dense)
+ *   dconv_w        : [dim, dconv] (float32), dconv_b [dim] (NULL: not written)
+ *   dinitial_state : [sequences, dim, dconv - 1] (float32), NULL: not written
+ *   workspace      : sscan_dwconv_bwd_workspace_size, 256-byte aligned
+ * Padding has zero gradients whatever the inputs hold there.  Results are bitwise
+ * reproducible.
+ */
+sscan_status sscan_dwconv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t dconv, int dtype, int silu,
+                              const void* x, int64_t x_stride, const float* conv_w, const float* conv_b,
+                              const float* initial_state, const int32_t* offsets, int64_t num_seqs, const void* dy,
+                              const float* dlast_state, void* dx, int64_t dx_stride, float* dconv_w, float* dconv_b,
+                              float* dinitial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for every row of a decode batch, against a pool of states:
+ *
+ *   state            : [num_slots, dim, dconv - 1] (float32; may be NULL when dconv == 1)
+ *   slots, slots_out : as in sscan_glr_step
+ *   x, y             : [batch, dim] (dtype), x with the row stride x_stride
+ */
+sscan_status sscan_dwconv_step(int64_t batch, int64_t dim, int64_t dconv, int dtype, int silu, float* state,
+                               int64_t num_slots, const int32_t* slots, const int32_t* slots_out, const void* x,
+                               int64_t x_stride, const float* conv_w, const float* conv_b, void* y, void* stream);
 
 #ifdef __cplusplus
 }

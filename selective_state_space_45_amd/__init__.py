@@ -671,3 +671,6 @@ def sscan_glr_step(state: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: tor
     if rc:
         _check(rc)
     return y
+
+
+from .layer_ops import *  # noqa: E402,F401,F403  (norm, 8-bit products, convolution: uses what is above)

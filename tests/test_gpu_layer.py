@@ -1,0 +1,521 @@
+"""Norm, 8-bit rows and products and the short convolution on the GPU against their float64
+forms (oracle/layer.py), whose *_error functions bound the kernels' float32 arithmetic; the
+rounding of a result to its type adds at most half a step, finfo(type).eps / 2 of its value."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+HALF = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+TINY = 1e-37          # results below float32's normal numbers
+
+
+@pytest.fixture(scope="module")
+def ss():
+    import selective_state_space_45_amd as m
+    return m
+
+
+def dev(a, dtype=F32):
+    return None if a is None else torch.as_tensor(np.ascontiguousarray(a)).to("cuda", dtype)
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def normal(seed, *shape, dtype=F32, size=1.0):
+    """Values of the type, on the GPU."""
+    return dev(np.random.default_rng(seed).standard_normal(shape) * size, dtype)
+
+
+def close(got, want, err, name):
+    """Within err, and half a step of got's type."""
+    g = host(got)
+    assert np.isfinite(g).all() == np.isfinite(want).all(), name
+    off = np.abs(g - want) - (err + HALF[got.dtype] * (np.abs(want) + err) + TINY)
+    assert not (off > 0).any(), f"{name}: {off.max():.3g} over its bound at {np.unravel_index(off.argmax(), off.shape)}"
+
+
+def same(got, want, name):
+    assert torch.equal(got, want), name
+
+
+# ---------------------------------------------------------------------------------------
+# Norm
+# ---------------------------------------------------------------------------------------
+
+TYPES = [(F32, F32), (BF16, BF16), (BF16, F32)]
+ROWS = [(1, 1), (1, 7), (3, 64), (5, 65), (2, 512), (70, 513), (9, 1535), (33, 2048), (4, 2560), (3, 4097), (2, 8192), (3, 20001),
+        (1, 65536)]
+
+
+def kept_of(x, residual, rtype):
+    return (x.float() if residual is None else x.float() + residual.float()).to(rtype)
+
+
+@pytest.mark.parametrize("rows,dim", ROWS)
+@pytest.mark.parametrize("dtype,rtype", TYPES)
+def test_norm(ss, rows, dim, dtype, rtype):
+    x, res, w = normal(1, rows, dim, dtype=dtype), normal(2, rows, dim, dtype=rtype), normal(3, dim)
+    out = ss.sscan_rms_fwd(x, w, residual=res, want_codes=True)
+    kept = kept_of(x, res, rtype)
+    same(out["residual"], kept, "residual")
+    y, _ = layer.rms_fwd(host(kept), host(w))
+    err = layer.rms_fwd_error(host(kept), host(w))
+    close(out["y"], y, err, "y")
+    codes, scales = host(out["codes"]), host(out["scales"])[:, None]
+    top = np.abs(y).max(1, keepdims=True)
+    assert (np.abs(scales * 127 - top) <= top * 2.0 ** -23 + err.max(1, keepdims=True)).all()
+    assert (np.abs(codes * scales - y) <= 0.5 * scales + err + scales * 127 * 2.0 ** -23).all()
+    assert np.abs(codes).max(1).min() == 127
+    # without the residual, and without anything but y
+    alone = ss.sscan_rms_fwd(kept.to(dtype), w, eps=1e-5)
+    y, _ = layer.rms_fwd(host(kept.to(dtype)), host(w))
+    close(alone["y"], y, layer.rms_fwd_error(host(kept.to(dtype)), host(w)), "y alone")
+    assert set(alone) == {"y"}
+
+
+@pytest.mark.parametrize("rows,dim", ROWS)
+@pytest.mark.parametrize("dtype,rtype", TYPES)
+def test_norm_backward(ss, rows, dim, dtype, rtype):
+    s, dy, dk, w = (normal(1, rows, dim, dtype=rtype), normal(2, rows, dim, dtype=dtype), normal(3, rows, dim, dtype=rtype),
+                    normal(4, dim))
+    g = ss.sscan_rms_bwd(s, w, dy, dresidual=dk, want_dresidual=True)
+    ds, dw = layer.rms_bwd(host(s), host(dy), host(w), host(dk))
+    eds, edw = layer.rms_bwd_error(host(s), host(dy), host(w), host(dk))
+    close(g["dx"], ds, eds, "dx")
+    close(g["dresidual"], ds, eds, "dresidual")
+    close(g["dweight"], dw, edw, "dweight")
+    g = ss.sscan_rms_bwd(s, None, dy)
+    assert set(g) == {"dx"}
+    close(g["dx"], layer.rms_bwd(host(s), host(dy))[0], layer.rms_bwd_error(host(s), host(dy))[0], "dx without weight")
+    g = ss.sscan_rms_bwd(s, w, dy, want_dx=False)
+    same(g["dweight"], ss.sscan_rms_bwd(s, w, dy, dresidual=dk)["dweight"], "dweight alone")
+
+
+@pytest.mark.parametrize("rows", [255, 1000, 2051, 9000])
+def test_norm_weight_gradient_over_many_rows(ss, rows):
+    s, dy, w = normal(1, rows, 96, dtype=BF16), normal(2, rows, 96, dtype=BF16), normal(3, 96)
+    g = [ss.sscan_rms_bwd(s, w, dy) for _ in range(2)]
+    _, dw = layer.rms_bwd(host(s), host(dy), host(w))
+    close(g[0]["dweight"], dw, layer.rms_bwd_error(host(s), host(dy), host(w))[1], "dweight")
+    same(g[0]["dweight"], g[1]["dweight"], "twice")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,dim,start", [(6, 40, 0), (6, 40, 1), (5, 513, 3), (1, 33, 2)])
+def test_norm_of_columns(ss, dtype, rows, dim, start):
+    """Rows that are columns of a wider tensor, at any element of it, in three dimensions."""
+    wide = normal(1, 2, rows, 3 * dim + 5, dtype=dtype)
+    x, w = wide[..., start:start + dim], normal(2, dim)
+    a = ss.sscan_rms_fwd(x, w, want_codes=True)
+    b = ss.sscan_rms_fwd(x.contiguous(), w, want_codes=True)
+    for k in ("y", "codes", "scales"):
+        same(a[k], b[k], k)
+    dy = normal(3, 2, rows, dim, dtype=dtype)
+    into = torch.full_like(wide, 7.0)
+    g = ss.sscan_rms_bwd(x, w, dy, out=dict(dx=into[..., start:start + dim]))
+    h = ss.sscan_rms_bwd(x.contiguous(), w, dy)
+    same(g["dx"], h["dx"], "dx")
+    same(g["dweight"], h["dweight"], "dweight")
+    into[..., start:start + dim] = 7.0
+    assert bool((into == 7.0).all())
+
+
+def test_norm_in_place(ss):
+    x, res, w = normal(1, 9, 300, dtype=BF16), normal(2, 9, 300), normal(3, 300)
+    want = ss.sscan_rms_fwd(x, w, residual=res)
+    stream = res.clone()
+    got = ss.sscan_rms_fwd(x, w, residual=stream, out=dict(residual=stream))
+    same(got["y"], want["y"], "y")
+    same(stream, want["residual"], "residual")
+    dy, dk = normal(4, 9, 300, dtype=BF16), normal(5, 9, 300)
+    want = ss.sscan_rms_bwd(stream, w, dy, dresidual=dk, want_dresidual=True)
+    got = ss.sscan_rms_bwd(stream, w, dy, dresidual=dk, want_dresidual=True, out=dict(dresidual=dk))
+    same(dk, want["dresidual"], "dresidual")
+    same(got["dx"], want["dx"], "dx")
+
+
+@pytest.mark.parametrize("dim", [5, 700, 2048, 9000])
+def test_norm_of_rows_that_are_not_ordinary(ss, dim):
+    x = normal(1, 7, dim)
+    x[0] = 0
+    x[1, dim // 2] = float("inf")
+    x[2, dim - 1] = float("nan")
+    x[3] *= 1e15
+    x[4] *= 1e-15
+    out = ss.sscan_rms_fwd(x, want_codes=True)
+    y, codes, scales = out["y"], out["codes"], out["scales"]
+    assert not y[0].any() and not codes[0].any() and scales[0].item() == 2.0 ** -126
+    assert y[1, dim // 2].isnan() and y[2].isnan().all()
+    assert scales[1:3].isnan().all() and not codes[1:3].any()
+    want, _ = layer.rms_fwd(host(x[3:]))
+    close(y[3:], want, layer.rms_fwd_error(host(x[3:])), "large and small rows")
+    assert codes[3:].abs().max(1).values.eq(127).all()
+
+
+def test_norm_by_differences(ss):
+    """dx against the forward's own differences, in float32: a step h gives h^2 of the third
+    derivative and 2^-24 / h of rounding, and h = 2^-8 keeps both below 2^-12 here."""
+    s, w, dy = normal(1, 4, 24), normal(2, 24), normal(3, 4, 24)
+    g = ss.sscan_rms_bwd(s, w, dy)
+    u = normal(4, 4, 24)
+    h = 2.0 ** -8
+    f = lambda v, q: (ss.sscan_rms_fwd(v, q)["y"].double() * dy.double()).sum().item()
+    size = dy.abs().double().sum().item()
+    d = (f(s + h * u, w) - f(s - h * u, w)) / (2 * h)
+    assert abs(d - (g["dx"].double() * u.double()).sum().item()) < 2.0 ** -12 * size
+    d = (f(s, w + h * u[0]) - f(s, w - h * u[0])) / (2 * h)
+    assert abs(d - (g["dweight"].double() * u[0].double()).sum().item()) < 2.0 ** -12 * size
+
+
+def test_norm_of_nothing(ss):
+    g = ss.sscan_rms_bwd(normal(1, 0, 8), normal(2, 8), normal(3, 0, 8))
+    assert not g["dweight"].any()
+    assert ss.sscan_rms_fwd(normal(1, 0, 8))["y"].shape == (0, 8)
+
+
+# ---------------------------------------------------------------------------------------
+# Rows in 8 bits, and their products
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,dim", ROWS)
+def test_quant(ss, rows, dim, dtype):
+    r = np.random.default_rng(5)
+    x = dev(r.standard_normal((rows, dim)) * np.exp(r.normal(size=(rows, 1)) * 10), dtype)
+    codes, scales = ss.sscan_i8_quant(x)
+    want, s = layer.i8_rows(host(x))
+    np.testing.assert_array_equal(host(scales), s)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want)
+
+
+def test_quant_at_its_borders(ss):
+    """Ties in every code, tiny rows, the largest numbers, rows with infinities and NaN."""
+    rows = [np.arange(-254, 255) / 2.0, np.arange(-254, 255) / 2.0 * 2.0 ** -133, np.arange(-254, 255) * 2.0 ** -149,
+            np.arange(-254, 255) * 1.3e36, np.zeros(509), np.full(509, 2.0 ** -149), np.full(509, 3e38)]
+    for bad in (np.inf, -np.inf, np.nan):
+        rows.append(np.ones(509))
+        rows[-1][300] = bad
+    # quotients next to a tie on either side: half-codes times an odd scale, a unit up and down
+    scale = np.float32(0.0123456)
+    v = (np.arange(-254, 255) / 2.0 * np.float64(scale)).astype(np.float32)
+    for to in (np.inf, -np.inf):
+        u = np.nextafter(v, np.float32(to))
+        u[0] = np.float32(127) * scale
+        rows.append(u.astype(np.float64))
+    x = torch.tensor(np.array(rows, dtype=np.float32), device="cuda")
+    codes, scales = ss.sscan_i8_quant(x)
+    want, s = layer.i8_rows(host(x))
+    np.testing.assert_array_equal(host(scales), s)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want)
+    codes, _ = ss.sscan_i8_quant(x[:, :0])
+    assert codes.shape == (x.shape[0], 0)
+
+
+def test_quant_leaves_what_is_between_rows(ss):
+    room = torch.full((5, 64), 55, dtype=torch.int8, device="cuda")
+    x = normal(1, 5, 33)
+    codes, _ = ss.sscan_i8_quant(x, codes=room[:, 7:40])
+    same(codes, ss.sscan_i8_quant(x)[0], "codes")
+    assert bool((room[:, :7] == 55).all()) and bool((room[:, 40:] == 55).all())
+
+
+def code_rows(seed, rows, k, low=-127, pad=0, shift=0):
+    """Codes whose rows are k + pad bytes apart and start `shift` bytes into an allocation."""
+    r = np.random.default_rng(seed)
+    room = torch.as_tensor(r.integers(-128, 128, shift + rows * (k + pad) + 64).astype(np.int8)).cuda()
+    c = torch.as_strided(room, (rows, k), (k + pad, 1), shift)
+    c.copy_(torch.as_tensor(r.integers(low, 128, (rows, k)).astype(np.int8)))
+    return c, dev(r.random(rows) + 0.1)
+
+
+def product(ss, m, n, k, dtype, bias=True, layout=(0, 0), seed=6, low=-127, **kw):
+    a, sa = code_rows(seed, m, k, low, *layout)
+    b, sb = code_rows(seed + 1, n, k, low, *layout)
+    bias = normal(seed + 2, n) if bias else None
+    got = ss.sscan_i8_matmul(a, sa, b, sb, bias=bias, dtype=dtype, **kw)
+    args = (a.cpu().numpy(), host(sa), b.cpu().numpy(), host(sb), None if bias is None else host(bias))
+    close(got, layer.i8_matmul(*args), layer.i8_matmul_error(*args), f"{m} x {n} x {k}")
+    return got
+
+
+PRODUCTS = [(1, 1, 1), (1, 16, 64), (1, 5120, 2560), (2, 17, 63), (3, 100, 65), (15, 33, 128), (16, 16, 127), (17, 40, 129), (31, 64, 300),
+            (33, 65, 96), (63, 250, 257), (64, 64, 64), (65, 129, 191), (100, 1, 700), (128, 128, 128), (129, 255, 1000), (255, 257, 384),
+            (256, 256, 256), (257, 300, 513), (300, 1000, 1535), (512, 512, 640), (700, 260, 4096), (1000, 777, 129)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,n,k", PRODUCTS)
+def test_products(ss, m, n, k, dtype):
+    product(ss, m, n, k, dtype)
+
+
+@pytest.mark.parametrize("layout", [(0, 0), (1, 0), (0, 1), (3, 7), (16, 16), (32, 8)])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 80), (1, 40, 81), (20, 50, 96), (70, 130, 127), (130, 300, 128), (260, 270, 400), (300, 514, 399)])
+def test_products_of_rows_anywhere(ss, m, n, k, layout):
+    product(ss, m, n, k, F32, bias=False, layout=layout)
+
+
+@pytest.mark.parametrize("m", [1, 5, 64, 200, 600])
+def test_products_at_the_ends_of_the_sums(ss, m):
+    """k = 0, and the longest sums of the largest codes."""
+    a = torch.empty(m, 0, dtype=torch.int8, device="cuda")
+    b, one, bias = torch.empty(9, 0, dtype=torch.int8, device="cuda"), torch.ones(m, device="cuda"), normal(1, 9)
+    same(ss.sscan_i8_matmul(a, one, b, one[:1].expand(9).contiguous(), bias=bias, dtype=F32), bias.expand(m, 9), "k = 0")
+    k = 131071
+    a = torch.full((m, k), -128, dtype=torch.int8, device="cuda")
+    b = torch.full((3, k), -128, dtype=torch.int8, device="cuda")
+    b[1], b[2] = 127, 0
+    got = ss.sscan_i8_matmul(a, one, b, one[:1].expand(3).contiguous(), dtype=F32)
+    want = torch.tensor([16384.0 * k, -16256.0 * k, 0.0], dtype=torch.float64).float().cuda()
+    same(got, want.expand(m, 3), "longest sums")
+
+
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_products_of_rows_with_nan(ss, m):
+    a, sa = code_rows(1, m, 64)
+    b, sb = code_rows(2, 20, 64)
+    sa[m - 1] = float("nan")
+    a[m - 1] = 0
+    sb[3] = float("inf")
+    out = ss.sscan_i8_matmul(a, sa, b, sb, dtype=F32)
+    assert out[m - 1].isnan().all() and (m == 1 or not out[:m - 1, 4:].isnan().any())
+    sums = a[:m - 1, :].double() @ b[3].double()
+    assert (out[:m - 1, 3].isinf() == (sums != 0)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 64), (33, 70, 128), (300, 513, 256), (257, 250, 2000)])
+def test_products_into_columns(ss, m, n, k, dtype):
+    for start in (0, 1, 8):
+        wide = torch.full((m, n + 19), 3.0, dtype=dtype, device="cuda")
+        got = product(ss, m, n, k, dtype, out=wide[:, start:start + n])
+        same(got, product(ss, m, n, k, dtype), "columns")
+        wide[:, start:start + n] = 3.0
+        assert bool((wide == 3.0).all())
+
+
+def test_products_with_and_without_workspace(ss):
+    """A split of the sums changes nothing: they are whole numbers."""
+    lib = ss.library()
+    for m, n, k in ((256, 2560, 5120), (100, 256, 20000), (5, 64, 100000), (256, 256, 8192)):
+        a, sa = code_rows(1, m, k)
+        b, sb = code_rows(2, n, k)
+        want = ss.sscan_i8_matmul(a, sa, b, sb, dtype=F32)
+        got = torch.empty_like(want)
+        rc = lib.sscan_i8_matmul(m, n, k, a.data_ptr(), 0, sa.data_ptr(), b.data_ptr(), 0, sb.data_ptr(), None, 0,
+                                 got.data_ptr(), 0, None, 0, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        same(got, want, (m, n, k))
+        close(got, layer.i8_matmul(a.cpu().numpy(), host(sa), b.cpu().numpy(), host(sb)),
+              layer.i8_matmul_error(a.cpu().numpy(), host(sa), b.cpu().numpy(), host(sb)), (m, n, k))
+
+
+def test_products_in_three_dimensions(ss):
+    a, sa = code_rows(1, 6, 48)
+    b, sb = code_rows(2, 10, 48)
+    got = ss.sscan_i8_matmul(a.view(2, 3, 48), sa.view(2, 3), b, sb)
+    same(got.view(6, 10), ss.sscan_i8_matmul(a, sa, b, sb), "three dimensions")
+
+
+# ---------------------------------------------------------------------------------------
+# Convolution
+# ---------------------------------------------------------------------------------------
+
+OFFSETS = {
+    "none": None,
+    "one": [0, 200],
+    "ragged": [0, 0, 1, 3, 6, 10, 64, 64, 64, 65, 127, 128, 131, 190, 190],
+    "short": list(range(0, 60, 1)) + [60],
+    "padded": [0, 5, 5],
+    "empty": [0, 0, 0, 0],
+    "ends": [0, 63, 64, 128, 130, 192, 193],
+}
+
+
+def conv_case(case, dtype, K, dim, seed=7, seqlen=200, batch=1):
+    off = OFFSETS[case]
+    rows = batch if off is None else len(off) - 1
+    x, w, b = normal(seed, batch, seqlen, dim, dtype=dtype), normal(seed + 1, dim, K), normal(seed + 2, dim)
+    h0, dy, dlast = normal(seed + 3, rows, dim, K - 1), normal(seed + 4, batch, seqlen, dim, dtype=dtype), normal(seed + 5, rows, dim, K - 1)
+    return x, w, b, h0, dy, dlast, None if off is None else torch.tensor(off, dtype=torch.int32, device="cuda"), off
+
+
+@pytest.mark.parametrize("case", list(OFFSETS))
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("silu", [True, False])
+def test_convolution(ss, case, K, dtype, silu):
+    for dim in (1, 5, 64, 130, 264):
+        x, w, b, h0, dy, dlast, doff, off = conv_case(case, dtype, K, dim)
+        y, last = ss.sscan_dwconv_fwd(x, w, conv_b=b, silu=silu, initial_state=h0, offsets=doff, return_last_state=True)
+        args = (host(x), host(w), host(b), silu, host(h0), off)
+        want, wlast = layer.conv_fwd(*args)
+        close(y, want, layer.conv_fwd_error(*args), "y")
+        np.testing.assert_array_equal(host(last), wlast)
+        g = ss.sscan_dwconv_bwd(x, w, dy, conv_b=b, silu=silu, initial_state=h0, offsets=doff, dlast_state=dlast)
+        r = layer.conv_bwd(host(x), host(w), host(dy), host(b), silu, host(h0), off, host(dlast))
+        for k in ("dx", "dconv_w", "dconv_b", "dinitial_state"):
+            close(g[k], r[k], r["error"][k], k)
+        if off is not None:                          # padding: zeros whatever is there
+            assert not y[0, off[-1]:].any() and not g["dx"][0, off[-1]:].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("batch,seqlen,dim", [(1, 1, 1), (3, 2, 7), (2, 61, 1535), (2, 64, 128), (4, 65, 96), (1, 300, 512), (3, 257, 33),
+                                              (1, 1025, 8), (2, 2047, 24)])
+def test_convolution_dense(ss, dtype, batch, seqlen, dim):
+    for K, state in ((4, True), (4, False), (2, True), (3, False)):
+        x, w, b, h0, dy, dlast, _, _ = conv_case("none", dtype, K, dim, 11, seqlen, batch)
+        if not state:
+            h0 = dlast = b = None
+        hh = lambda t: None if t is None else host(t)
+        y, last = ss.sscan_dwconv_fwd(x, w, conv_b=b, initial_state=h0, return_last_state=True)
+        want, wlast = layer.conv_fwd(host(x), host(w), hh(b), True, hh(h0))
+        close(y, want, layer.conv_fwd_error(host(x), host(w), hh(b), True, hh(h0)), "y")
+        np.testing.assert_array_equal(host(last), wlast)
+        g = ss.sscan_dwconv_bwd(x, w, dy, conv_b=b, initial_state=h0, dlast_state=dlast)
+        r = layer.conv_bwd(host(x), host(w), host(dy), hh(b), True, hh(h0), None, hh(dlast))
+        for k in ("dx", "dconv_w", "dconv_b", "dinitial_state"):
+            close(g[k], r[k], r["error"][k], k)
+        bare = ss.sscan_dwconv_bwd(x, w, dy, conv_b=b, initial_state=h0, dlast_state=dlast, want_dbias=False,
+                                   want_dinitial_state=False)
+        assert set(bare) == {"dx", "dconv_w"}
+        same(bare["dx"], g["dx"], "dx alone")
+        same(bare["dconv_w"], g["dconv_w"], "dconv_w alone")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", ["none", "ragged"])
+@pytest.mark.parametrize("dim,start", [(40, 0), (40, 40), (64, 1), (130, 3), (8, 8)])
+def test_convolution_of_columns(ss, dtype, case, dim, start):
+    x, w, b, h0, dy, dlast, doff, _ = conv_case(case, dtype, 4, dim)
+    wide = normal(1, 1, 200, 3 * dim, dtype=dtype)
+    cols = wide[..., start:start + dim]
+    cols.copy_(x)
+    kw = dict(conv_b=b, initial_state=h0, offsets=doff)
+    same(ss.sscan_dwconv_fwd(cols, w, **kw), ss.sscan_dwconv_fwd(x, w, **kw), "y")
+    into = torch.full_like(wide, 7.0)
+    g = ss.sscan_dwconv_bwd(cols, w, dy, dlast_state=dlast, out=dict(dx=into[..., start:start + dim]), **kw)
+    h = ss.sscan_dwconv_bwd(x, w, dy, dlast_state=dlast, **kw)
+    for k in h:
+        same(g[k], h[k], k)
+    into[..., start:start + dim] = 7.0
+    assert bool((into == 7.0).all())
+
+
+def test_convolution_keeps_requests_and_padding_apart(ss):
+    """Infinities and NaN of one request, and of padding, reach nothing else."""
+    x, w, b, h0, dy, dlast, doff, off = conv_case("ragged", BF16, 4, 72)
+    kw = dict(conv_b=b, initial_state=h0, offsets=doff)
+    y = ss.sscan_dwconv_fwd(x, w, **kw)
+    g = ss.sscan_dwconv_bwd(x, w, dy, dlast_state=dlast, **kw)
+    bad, bdy, bh = x.clone(), dy.clone(), h0.clone()
+    bad[0, 190:], bdy[0, 190:] = float("nan"), float("inf")
+    bad[0, 64] = float("inf")                                    # request 8 is the one token 64
+    bdy[0, 64] = float("nan")
+    bh[8] = float("nan")
+    kw["initial_state"] = bh
+    yb = ss.sscan_dwconv_fwd(bad, w, **kw)
+    gb = ss.sscan_dwconv_bwd(bad, w, bdy, dlast_state=dlast, **kw)
+    rest = torch.arange(200, device="cuda") != 64
+    same(yb[:, rest], y[:, rest], "y")
+    same(gb["dx"][:, rest], g["dx"][:, rest], "dx")
+    seqs = torch.arange(14, device="cuda") != 8
+    same(gb["dinitial_state"][seqs], g["dinitial_state"][seqs], "dinitial_state")
+    assert yb[0, 64].isnan().any()
+    clean = ss.sscan_dwconv_bwd(torch.where(torch.arange(200, device="cuda")[:, None] >= 190, bad, x), w,
+                                torch.where(torch.arange(200, device="cuda")[:, None] >= 190, bdy, dy), conv_b=b,
+                                initial_state=h0, offsets=doff, dlast_state=dlast)
+    for k in g:
+        same(clean[k], g[k], k + " beside bad padding")
+
+
+def test_convolution_with_offsets_that_break_the_rules(ss):
+    """Unspecified results, and no access outside the tensors (which the guards around them show
+    for writes)."""
+    for off in ([5, 3, 500], [-7, -3, 90], [0, 1000, 2000], [100, 50, 0], [2 ** 31 - 1, -2 ** 31, 7]):
+        o = torch.tensor(off, dtype=torch.int32, device="cuda")
+        x, w, dy = normal(1, 1, 130, 40), normal(2, 40, 4), normal(3, 1, 130, 40)
+        room = torch.full((3, 130, 40), 9.0, device="cuda")
+        states = torch.full((4, 2, 40, 3), 9.0, device="cuda")
+        ss.sscan_dwconv_fwd(x, w, offsets=o, out=room[1:2], last_state=states[1])
+        ss.sscan_dwconv_bwd(x, w, dy, offsets=o, out=dict(dx=room[1:2], dinitial_state=states[2]))
+        torch.cuda.synchronize()
+        assert bool((room[0] == 9).all()) and bool((room[2] == 9).all()) and bool((states[0] == 9).all()) and bool((states[3] == 9).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("batch,dim", [(1, 1), (1, 2560), (3, 65), (5, 130), (33, 264), (64, 1535)])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+def test_convolution_step(ss, dtype, batch, dim, K):
+    for silu in (True, False):
+        pool = 2 * batch + 3
+        st, x, w, b = normal(1, pool, dim, K - 1), normal(2, batch, dim, dtype=dtype), normal(3, dim, K), normal(4, dim)
+        order = np.random.default_rng(5).permutation(pool)
+        slots, to = order[:batch].astype(np.int32), order[batch:2 * batch].astype(np.int32)
+        if batch > 2:
+            slots[1], to[2] = -1, pool
+        for a, o in ((slots, to), (slots, None), (None, None)):
+            mine = st.clone()
+            y = ss.sscan_dwconv_step(mine, x, w, conv_b=b, silu=silu, slots=dev(a, torch.int32), slots_out=dev(o, torch.int32))
+            want, new = layer.conv_step(host(st), host(x), host(w), host(b), silu, a, o)
+            err = layer.conv_fwd_error(host(x)[:, None], host(w), host(b), silu,
+                                       host(st)[np.arange(batch) if a is None else a])[:, 0]
+            close(y, want, err, "y")
+            np.testing.assert_array_equal(host(mine), new)
+
+
+def test_convolution_steps_are_the_convolution(ss):
+    x, w, b, h0, *_ = conv_case("none", BF16, 4, 136, seqlen=20, batch=3)
+    y, last = ss.sscan_dwconv_fwd(x, w, conv_b=b, initial_state=h0, return_last_state=True)
+    pool = h0.clone()
+    for t in range(20):
+        same(ss.sscan_dwconv_step(pool, x[:, t], w, conv_b=b), y[:, t], t)
+    same(pool, last, "state")
+
+
+def test_convolution_by_differences(ss):
+    """Gradients against the forward's own differences, as for the norm."""
+    x, w, b, h0, dy, dlast, doff, _ = conv_case("ragged", F32, 4, 6)
+    p = dict(x=x, conv_w=w, conv_b=b, initial_state=h0)
+    g = ss.sscan_dwconv_bwd(x, w, dy, conv_b=b, initial_state=h0, offsets=doff, dlast_state=dlast)
+
+    def f(q):
+        y, last = ss.sscan_dwconv_fwd(offsets=doff, return_last_state=True, **q)
+        return (y.double() * dy.double()).sum().item() + (last.double() * dlast.double()).sum().item()
+
+    size = 10 * (dy.abs().double().sum() + dlast.abs().double().sum()).item()
+    h = 2.0 ** -8
+    for k, name in (("x", "dx"), ("conv_w", "dconv_w"), ("conv_b", "dconv_b"), ("initial_state", "dinitial_state")):
+        u = normal(9, *p[k].shape)
+        d = (f({**p, k: p[k] + h * u}) - f({**p, k: p[k] - h * u})) / (2 * h)
+        assert abs(d - (g[name].double() * u.double()).sum().item()) < 2.0 ** -12 * size, k
+
+
+@pytest.mark.parametrize("batch,seqlen", [(2, 0), (0, 5)])
+def test_convolution_of_nothing(ss, batch, seqlen):
+    x, w, dy = normal(1, batch, seqlen, 8), normal(2, 8, 4), normal(3, batch, seqlen, 8)
+    h0, dlast = normal(4, batch, 8, 3), normal(5, batch, 8, 3)
+    y, last = ss.sscan_dwconv_fwd(x, w, initial_state=h0, return_last_state=True)
+    same(last, h0, "last_state")
+    g = ss.sscan_dwconv_bwd(x, w, dy, initial_state=h0, dlast_state=dlast)
+    assert not g["dconv_w"].any() and not g["dconv_b"].any()
+    same(g["dinitial_state"], dlast, "dinitial_state")
+
+
+def test_convolution_is_the_scans_prologue(ss):
+    """The operator, then the scan of its output, against the scan with its fused prologue:
+    in float32 the same sums in the same order up to the fused kernel's own rounding."""
+    B, L, D, N = 2, 70, 32, 16
+    x, w, b = normal(1, B, L, D), normal(2, D, 4, size=0.5), normal(3, D)
+    dt, A = normal(4, B, L, D) - 3, -(torch.arange(N, device="cuda") + 1.0).expand(D, N).contiguous()
+    Bm, C = normal(5, B, L, N), normal(6, B, L, N)
+    fused = ss.sscan_fwd(x, dt, A, Bm, C, conv_w=w, conv_b=b)
+    y = ss.sscan_fwd(ss.sscan_dwconv_fwd(x, w, conv_b=b), dt, A, Bm, C)
+    assert ((y - fused).abs() <= 1e-4 * (1 + fused.abs())).all()

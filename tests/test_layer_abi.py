@@ -1,0 +1,195 @@
+"""Refusals of the norm, the 8-bit rows and products and the convolution: every argument is
+checked on the host, so none of this needs a GPU."""
+import ctypes
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "selective_state_space_45_amd", "libselscan.so")
+P = ctypes.c_void_p
+MB = 1 << 20
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(LIB):
+        from selective_state_space_45_amd import build as b
+        b.build()
+    import selective_state_space_45_amd as ss
+    return ss.library()
+
+
+def at(k):
+    """An address that no call here reaches: each fails its checks first, or is empty."""
+    return P((k + 1) * MB)
+
+
+def call(fn, defaults, kw):
+    assert set(kw) <= set(defaults), kw
+    return fn(*{**defaults, **kw}.values())
+
+
+def rms_fwd(lib, **kw):
+    return call(lib.sscan_rms_fwd, dict(rows=4, dim=8, dtype=1, rdtype=0, x=at(0), sx=0, res=at(1), w=at(2), eps=1e-5,
+                                        y=at(3), kept=at(4), codes=at(5), sc=0, scales=at(6), stream=None), kw)
+
+
+def rms_bwd(lib, **kw):
+    return call(lib.sscan_rms_bwd, dict(rows=4, dim=8, dtype=1, rdtype=0, s=at(0), ss=0, w=at(2), eps=1e-5, dy=at(3),
+                                        dk=at(4), dx=at(5), sdx=0, dres=at(6), dw=at(7), ws=at(8), nws=1 << 20, stream=None), kw)
+
+
+def quant(lib, **kw):
+    return call(lib.sscan_i8_quant, dict(rows=4, dim=8, dtype=1, x=at(0), sx=0, codes=at(1), sc=0, scales=at(2), stream=None), kw)
+
+
+def matmul(lib, **kw):
+    return call(lib.sscan_i8_matmul, dict(m=4, n=6, k=8, a=at(0), sa=0, as_=at(1), b=at(2), sb=0, bs=at(3), bias=at(4),
+                                          dtype=1, out=at(5), so=0, ws=None, nws=0, stream=None), kw)
+
+
+def conv_fwd(lib, **kw):
+    return call(lib.sscan_dwconv_fwd, dict(batch=2, seqlen=9, dim=4, dconv=4, dtype=0, silu=1, x=at(0), sx=0, w=at(1),
+                                           b=at(2), h0=at(3), off=None, nseq=0, y=at(4), last=at(5), stream=None), kw)
+
+
+def conv_bwd(lib, **kw):
+    return call(lib.sscan_dwconv_bwd, dict(batch=2, seqlen=9, dim=4, dconv=4, dtype=0, silu=1, x=at(0), sx=0, w=at(1),
+                                           b=at(2), h0=at(3), off=None, nseq=0, dy=at(4), dlast=at(5), dx=at(6), sdx=0,
+                                           dw=at(7), db=at(8), dh0=at(9), ws=at(10), nws=1 << 20, stream=None), kw)
+
+
+def conv_step(lib, **kw):
+    return call(lib.sscan_dwconv_step, dict(batch=2, dim=4, dconv=4, dtype=0, silu=1, state=at(0), pool=3, slots=at(1),
+                                            out=at(2), x=at(3), sx=0, w=at(4), b=at(5), y=at(6), stream=None), kw)
+
+
+def refused(lib, fn, kw, code, word):
+    assert fn(lib, **kw) == code, lib.sscan_last_error()
+    assert word in lib.sscan_last_error()
+
+
+ROWS = [(dict(dtype=7), UNSUPPORTED, b"dtype"), (dict(rows=-1), INVALID, b"negative"), (dict(dim=-1), INVALID, b"negative"),
+        (dict(dim=65537), INVALID, b"SSCAN_RMS_MAX_DIM"), (dict(rows=1 << 31), INVALID, b"too large")]
+
+
+@pytest.mark.parametrize("kw,code,word", ROWS + [
+    (dict(rdtype=1, dtype=0), UNSUPPORTED, b"residual_dtype"), (dict(rdtype=9), UNSUPPORTED, b"residual_dtype"),
+    (dict(eps=-1.0), INVALID, b"eps"), (dict(eps=float("nan")), INVALID, b"eps"), (dict(eps=float("inf")), INVALID, b"eps"),
+    (dict(x=None), INVALID, b"null"), (dict(y=None, kept=None, codes=None, scales=None), INVALID, b"null"),
+    (dict(codes=None), INVALID, b"exactly"), (dict(scales=None), INVALID, b"exactly"), (dict(sx=7), INVALID, b"stride of x"),
+    (dict(sc=7), INVALID, b"stride of codes"), (dict(sx=1 << 50), INVALID, b"too large"), (dict(x=P(MB + 1)), INVALID, b"align"),
+    (dict(res=P(MB + 2)), INVALID, b"align"), (dict(w=P(MB + 2)), INVALID, b"align"), (dict(scales=P(MB + 2)), INVALID, b"align"),
+    (dict(y=at(0)), INVALID, b"overlap"), (dict(kept=at(0)), INVALID, b"overlap"), (dict(kept=P(2 * MB + 4)), INVALID, b"overlap"),
+    (dict(codes=at(1)), INVALID, b"overlap"), (dict(scales=at(2)), INVALID, b"overlap"), (dict(y=at(4)), INVALID, b"overlap"),
+    (dict(codes=at(6)), INVALID, b"overlap")])
+def test_norm_refuses(lib, kw, code, word):
+    refused(lib, rms_fwd, kw, code, word)
+
+
+@pytest.mark.parametrize("kw,code,word", ROWS + [
+    (dict(rdtype=1, dtype=0), UNSUPPORTED, b"residual_dtype"), (dict(eps=-1.0), INVALID, b"eps"),
+    (dict(s=None), INVALID, b"null"), (dict(dy=None), INVALID, b"null"), (dict(dx=None, dres=None, dw=None), INVALID, b"null"),
+    (dict(ss=7), INVALID, b"stride of s"), (dict(sdx=7), INVALID, b"stride of dx"), (dict(s=P(MB + 2)), INVALID, b"align"),
+    (dict(dw=P(MB + 2)), INVALID, b"align"), (dict(ws=None), INVALID, b"workspace"), (dict(nws=16), INVALID, b"too small"),
+    (dict(ws=P(MB + 128)), INVALID, b"align"), (dict(dx=at(0)), INVALID, b"overlap"), (dict(dx=at(3)), INVALID, b"overlap"),
+    (dict(dres=P(5 * MB + 4)), INVALID, b"overlap"), (dict(dres=at(0)), INVALID, b"overlap"), (dict(dw=at(2)), INVALID, b"overlap"),
+    (dict(dx=at(6)), INVALID, b"overlap"), (dict(ws=at(3)), INVALID, b"overlap")])
+def test_norm_backward_refuses(lib, kw, code, word):
+    refused(lib, rms_bwd, kw, code, word)
+
+
+@pytest.mark.parametrize("kw,code,word", ROWS + [
+    (dict(x=None), INVALID, b"null"), (dict(codes=None), INVALID, b"null"), (dict(scales=None), INVALID, b"null"),
+    (dict(sx=7), INVALID, b"stride of x"), (dict(sc=7), INVALID, b"stride of codes"), (dict(codes=at(0)), INVALID, b"overlap"),
+    (dict(scales=P(2 * MB + 16)), INVALID, b"overlap"), (dict(x=P(MB + 1)), INVALID, b"align")])
+def test_quant_refuses(lib, kw, code, word):
+    refused(lib, quant, kw, code, word)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(dtype=2), UNSUPPORTED, b"dtype"), (dict(m=-1), INVALID, b"negative"), (dict(n=-1), INVALID, b"negative"),
+    (dict(k=-1), INVALID, b"negative"), (dict(k=131072), INVALID, b"SSCAN_I8_MAX_K"), (dict(m=1 << 31), INVALID, b"too large"),
+    (dict(m=(1 << 31) - 1, n=1024), INVALID, b"too large"), (dict(a=None), INVALID, b"null"), (dict(as_=None), INVALID, b"null"),
+    (dict(b=None), INVALID, b"null"), (dict(bs=None), INVALID, b"null"), (dict(out=None), INVALID, b"null"),
+    (dict(sa=7), INVALID, b"stride of a"), (dict(sb=7), INVALID, b"stride of b"), (dict(so=5), INVALID, b"stride of out"),
+    (dict(out=P(MB + 1)), INVALID, b"align"), (dict(bias=P(MB + 2)), INVALID, b"align"), (dict(as_=P(MB + 2)), INVALID, b"align"),
+    (dict(ws=P(MB + 128), nws=1 << 20), INVALID, b"align"), (dict(out=at(0)), INVALID, b"overlap"),
+    (dict(out=at(2)), INVALID, b"overlap"), (dict(out=at(4)), INVALID, b"overlap"), (dict(out=at(1)), INVALID, b"overlap")])
+def test_matmul_refuses(lib, kw, code, word):
+    refused(lib, matmul, kw, code, word)
+
+
+CONV = [(dict(dtype=7), UNSUPPORTED, b"dtype"), (dict(batch=-1), INVALID, b"negative"), (dict(dim=-1), INVALID, b"negative"),
+        (dict(dconv=0), UNSUPPORTED, b"dconv"), (dict(dconv=5), UNSUPPORTED, b"dconv"), (dict(sx=3), INVALID, b"stride of x"),
+        (dict(dim=(1 << 28) + 1), INVALID, b"too large"), (dict(x=None), INVALID, b"null"), (dict(w=None), INVALID, b"null"),
+        (dict(x=P(MB + 2)), INVALID, b"align"), (dict(w=P(MB + 2)), INVALID, b"align"), (dict(b=P(MB + 2)), INVALID, b"align")]
+SEQ = [(dict(seqlen=-1), INVALID, b"negative"), (dict(seqlen=(1 << 30) + 1), INVALID, b"SSCAN_MAX_SEQLEN"),
+       (dict(off=at(30), nseq=3), INVALID, b"batch 1"), (dict(off=at(30), nseq=0, batch=1), INVALID, b"num_seqs"),
+       (dict(off=P(2), nseq=1, batch=1), INVALID, b"align"), (dict(h0=P(31 * MB + 2)), INVALID, b"align"),
+       (dict(batch=1 << 40, dim=1 << 40), INVALID, b"too large")]
+
+
+@pytest.mark.parametrize("kw,code,word", CONV + SEQ + [
+    (dict(y=None), INVALID, b"null"), (dict(last=P(MB + 2)), INVALID, b"align"), (dict(y=at(0)), INVALID, b"overlap"),
+    (dict(last=at(3)), INVALID, b"overlap"), (dict(last=at(4)), INVALID, b"overlap"), (dict(y=at(2)), INVALID, b"overlap")])
+def test_convolution_refuses(lib, kw, code, word):
+    refused(lib, conv_fwd, kw, code, word)
+
+
+@pytest.mark.parametrize("kw,code,word", CONV + SEQ + [
+    (dict(dy=None), INVALID, b"null"), (dict(dx=None), INVALID, b"null"), (dict(dw=None), INVALID, b"null"),
+    (dict(sdx=3), INVALID, b"stride of dx"), (dict(ws=None), INVALID, b"workspace"), (dict(nws=16), INVALID, b"too small"),
+    (dict(ws=P(MB + 128)), INVALID, b"align"), (dict(dx=at(4)), INVALID, b"overlap"), (dict(dx=at(0)), INVALID, b"overlap"),
+    (dict(dw=at(1)), INVALID, b"overlap"), (dict(db=at(7)), INVALID, b"overlap"), (dict(dh0=at(5)), INVALID, b"overlap"),
+    (dict(dlast=P(31 * MB + 2)), INVALID, b"align"), (dict(dh0=P(31 * MB + 2)), INVALID, b"align")])
+def test_convolution_backward_refuses(lib, kw, code, word):
+    refused(lib, conv_bwd, kw, code, word)
+
+
+@pytest.mark.parametrize("kw,code,word", CONV + [
+    (dict(y=None), INVALID, b"null"), (dict(state=None), INVALID, b"null"), (dict(slots=None, batch=4), INVALID, b"num_slots"),
+    (dict(pool=-1), INVALID, b"num_slots"), (dict(slots=P(2)), INVALID, b"align"), (dict(out=P(2)), INVALID, b"align"),
+    (dict(y=at(0)), INVALID, b"overlap"), (dict(x=P(MB + 32)), INVALID, b"overlap"), (dict(y=at(3)), INVALID, b"overlap")])
+def test_convolution_step_refuses(lib, kw, code, word):
+    refused(lib, conv_step, kw, code, word)
+
+
+def test_empty_calls_do_nothing(lib):
+    assert rms_fwd(lib, rows=0) == OK and rms_fwd(lib, dim=0) == OK and rms_bwd(lib, dim=0) == OK
+    assert rms_bwd(lib, rows=0, dw=None) == OK and quant(lib, rows=0) == OK
+    assert matmul(lib, m=0) == OK and matmul(lib, n=0) == OK
+    assert conv_fwd(lib, batch=0) == OK and conv_fwd(lib, dim=0) == OK and conv_bwd(lib, dim=0) == OK
+    assert conv_step(lib, batch=0) == OK and conv_step(lib, dim=0) == OK
+
+
+def test_sizes(lib):
+    for f, args in ((lib.sscan_rms_bwd_workspace_size, (-1, 5)), (lib.sscan_rms_bwd_workspace_size, (5, 65537)),
+                    (lib.sscan_rms_bwd_workspace_size, (1 << 31, 5)), (lib.sscan_i8_matmul_workspace_size, (-1, 5, 5)),
+                    (lib.sscan_i8_matmul_workspace_size, (5, 5, 131072)), (lib.sscan_dwconv_bwd_workspace_size, (1, 5, 5, 5)),
+                    (lib.sscan_dwconv_bwd_workspace_size, (-1, 5, 5, 4)), (lib.sscan_dwconv_bwd_workspace_size, (1, (1 << 30) + 1, 5, 4))):
+        assert f(*args) == 0
+    assert lib.sscan_rms_bwd_workspace_size(32768, 2048) > 0 and lib.sscan_dwconv_bwd_workspace_size(8, 4096, 2048, 4) > 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    import torch
+    import selective_state_space_45_amd as ss
+    x, w = torch.zeros(2, 8), torch.zeros(8, 4)
+    c = torch.zeros(2, 8, dtype=torch.int8)
+    for f in (lambda: ss.sscan_rms_fwd(x), lambda: ss.sscan_rms_bwd(x, None, x), lambda: ss.sscan_i8_quant(x),
+              lambda: ss.sscan_i8_matmul(c, x[:, 0], c, x[:, 0]), lambda: ss.sscan_dwconv_fwd(x[None], w),
+              lambda: ss.sscan_dwconv_bwd(x[None], w, x[None]), lambda: ss.sscan_dwconv_step(torch.zeros(2, 8, 3), x, w)):
+        with pytest.raises(ValueError, match="GPU"):
+            f()
+    for f, word in ((lambda: ss.sscan_rms_fwd(x[0]), "rows, dim"), (lambda: ss.sscan_rms_fwd(x.double()), "float32 or bfloat16"),
+                    (lambda: ss.sscan_rms_fwd(x, residual=x.bfloat16()), "float32 or of x's type"),
+                    (lambda: ss.sscan_rms_fwd(x.bfloat16(), residual=x, residual_dtype=torch.bfloat16), "residual must be"),
+                    (lambda: ss.sscan_rms_bwd(x.bfloat16(), None, x), "float32 or of dy's type"),
+                    (lambda: ss.sscan_i8_matmul(c, x[:, 0], c, x[:, 0], dtype=torch.float16), "float32 or bfloat16"),
+                    (lambda: ss.sscan_i8_matmul(c, x[:, 0], c[None], x[:, 0]), r"b must be \[n, k\]"),
+                    (lambda: ss.sscan_dwconv_fwd(x, w), "batch, seqlen, dim"), (lambda: ss.sscan_dwconv_step(x, x[None], w), "batch, dim")):
+        with pytest.raises(ValueError, match=word):
+            f()
