@@ -529,7 +529,7 @@ sscan_status sscan_glr_step(int64_t batch, int64_t dim, int dtype, float* state,
  */
 
 /* Channels of a row that sscan_rms_fwd, sscan_rms_bwd and sscan_i8_quant accept. */
-#define SSCAN_RMS_MAX_DIM 65536
+#define SSCAN_RMS_MAX_DIM 32768
 
 /*
  * Root-mean-square norm with the residual's addition.  For each row:
