@@ -1,60 +1,286 @@
 // Products of rows in 8-bit integers with the scales of both sides.
+//
+// out[m, n] = (sum_k a[m, k] b[n, k]) (as[m] bs[n]) + bias[n].  Both sides have k along their
+// rows, so both go through LDS the same way: 128 bytes of each row at a time, in 16-byte
+// chunks, which are what a lane of a matrix instruction takes (v_mfma_i32_32x32x32_i8: lane l
+// holds row l % 32, bytes 16 (l / 32) .. + 15 of 32).  The order of k is the same on both
+// sides and otherwise free, since the sums are whole numbers.
 #include "sscan_layer.h"
 
 namespace sscan {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef i32x4 i32x4_any __attribute__((aligned(1)));
 
-// A workgroup of four waves has a tile of 64 x 64 sums; k goes through LDS 64 bytes at a time.
-// Lane l of a matrix instruction holds row l % 16 of either side, bytes 16 (l / 16) .. + 15,
-// and of the result column l % 16, rows 4 (l / 16) .. + 3.
-template <typename Tout>
-__global__ __launch_bounds__(256) void i8_matmul_kernel(MatmulParams p, int ntn) {
-  constexpr int kPitch = 80;
-  __shared__ __attribute__((aligned(16))) int8_t la[64 * kPitch];
-  __shared__ __attribute__((aligned(16))) int8_t lb[64 * kPitch];
-  const int64_t tile = workgroup<256>();
-  const int64_t m0 = tile / ntn * 64, n0 = tile % ntn * 64;
-  if (m0 >= p.m) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  i32x4 acc[4] = {};
-  for (int k0 = 0; k0 < p.k; k0 += 64) {
-    __syncthreads();
+constexpr int kDepth = 128;            // bytes of k staged at a time
+constexpr int kChunk16 = 16;           // bytes of a chunk
+constexpr int kTileLanes = 256;        // lanes of a workgroup: four waves, two by two
+
+// All waves of the workgroup are here, with nothing of theirs under way but the newest VM
+// loads into LDS.  What the compiler sees as memory stays on its side.
+template <int VM>
+__device__ __forceinline__ void all_here() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | 7 << 4 | 0 << 8 | (VM >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// 16 bytes for each lane straight to LDS, in the lanes' order from the wave's address `to`, from
+// an address of its own or from a common one and an offset.  In assembly, since the compiler
+// takes any reading of LDS to wait for all such loads; all_here() waits for them.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved, and is what such a load goes by
+__device__ __forceinline__ void bring(uint32_t to, uintptr_t from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "m0");
+}
+__device__ __forceinline__ void bring(uint32_t to, uintptr_t base, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(at), "s"(base) : "m0");
+}
+#pragma clang diagnostic pop
+
+__device__ __attribute__((aligned(16))) const int8_t g_zeros[kChunk16] = {};
+
+// One side's rows of a tile on their way to LDS.  A chunk of row r goes to slot
+// (chunk ^ r) & 7 of the row's 128 bytes, so that 8 lanes that read one chunk of 8 rows
+// take all banks once.  Lane l of a wave brings chunk (l ^ l / 8) & 7 of row l / 8 of 8 rows:
+// LDS is then filled in the lanes' order, which is what a load straight to LDS does.
+template <int ROWS, bool DIRECT>
+struct Side {
+  static constexpr int kLoads = ROWS / 32;
+  const int8_t* base;
+  uint32_t at[kLoads];       // DIRECT: bytes from base to the lane's rows
+  int64_t stride;
+  int row0, last, chunk;     // the lane's first row, the last row there is, its chunk
+  i32x4 held[DIRECT ? 1 : kLoads];
+
+  __device__ __forceinline__ Side(const int8_t* p, int64_t st, int64_t r0, int rows) : stride(st) {
+    const int lane = threadIdx.x & 63;
+    base = p + r0 * st;
+    row0 = (threadIdx.x >> 6) * 8 + (lane >> 3);
+    last = static_cast<int>(rows - r0 < ROWS ? rows - r0 : ROWS) - 1;
+    chunk = (lane ^ (lane >> 3)) & 7;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int at = j * 256 + threadIdx.x, r = at >> 6, c = at & 63;
-      const bool in = k0 + c < p.k;
-      la[r * kPitch + c] = in && m0 + r < p.m ? p.a[(m0 + r) * p.sa + k0 + c] : 0;
-      lb[r * kPitch + c] = in && n0 + r < p.n ? p.b[(n0 + r) * p.sb + k0 + c] : 0;
-    }
-    __syncthreads();
-    const int at = (lane & 15) * kPitch + (lane >> 4) * 16;
-    const i32x4 a = *reinterpret_cast<const i32x4*>(la + wave * 16 * kPitch + at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, *reinterpret_cast<const i32x4*>(lb + j * 16 * kPitch + at), acc[j], 0, 0, 0);
+    for (int i = 0; i < kLoads; ++i) at[i] = static_cast<uint32_t>(row(i) * st + chunk * kChunk16);
   }
+  // rows past the end repeat the last one: their sums are not written
+  __device__ __forceinline__ int row(int i) const { return row0 + 32 * i < last ? row0 + 32 * i : last; }
+
+  // Bytes k .. k + kDepth of the rows, of which `left` are there; zeros for the others.
+  __device__ __forceinline__ void load(int8_t* lds, int k, int left) {
+    if (DIRECT) {
+      const uint32_t to = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+          reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)lds) + (threadIdx.x >> 6) * 8 * kDepth));
+      const uintptr_t from = reinterpret_cast<uintptr_t>(base + k);
+      if (left >= kDepth) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t n = n0 + j * 16 + (lane & 15);
+        for (int i = 0; i < kLoads; ++i) bring(to + i * 32 * kDepth, from, at[i]);
+      } else {
+        const uintptr_t zeros = reinterpret_cast<uintptr_t>(g_zeros);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + wave * 16 + (lane >> 4) * 4 + i;
-      if (m < p.m && n < p.n)
-        store_val(static_cast<Tout*>(p.out) + m * p.so + n,
-                  fmaf(static_cast<float>(acc[j][i]), p.as[m] * p.bs[n], p.bias ? p.bias[n] : 0.f));
+        for (int i = 0; i < kLoads; ++i) bring(to + i * 32 * kDepth, chunk * kChunk16 < left ? from + at[i] : zeros);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int8_t* from = base + row(i) * stride + k + chunk * kChunk16;
+        const int n = left - chunk * kChunk16;
+        if (n >= kChunk16) {
+          held[i] = *reinterpret_cast<const i32x4_any*>(from);
+        } else {
+          uint32_t w[4] = {};
+          for (int j = 0; j < n; ++j) w[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(from[j])) << 8 * (j % 4);
+          held[i] = i32x4{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
+        }
+      }
     }
+  }
+  // What load() left in registers, to LDS.
+  __device__ __forceinline__ void put(int8_t* lds) {
+    if (DIRECT) return;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      *reinterpret_cast<i32x4*>(lds + (i * 32 + (threadIdx.x >> 6) * 8) * kDepth + (threadIdx.x & 63) * kChunk16) = held[i];
+  }
+};
+
+// Four neighbouring outputs of a row in Tout.
+__device__ __forceinline__ void stage(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void stage(bf16_t* p, f32x4 v) {
+  typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+  typedef uint16_t u4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<u4*>(p) = __builtin_bit_cast(u4, __builtin_convertvector(v, b4));
+}
+
+// A workgroup's tile of BM x BN sums; wave (wm, wn) of two by two has a quarter, MI x NI blocks of
+// 32 x 32.  LDS holds two depths of k: while one is multiplied the next is on its way.  The
+// instruction's rows are n and its columns m, so that a lane ends with neighbouring outputs.
+template <typename Tout, int BM, int BN, bool DIRECT>
+__global__ __launch_bounds__(kTileLanes) void i8_tile_kernel(MatmulParams p, int ntm, int ntn) {
+  constexpr int MI = BM / 64, NI = BN / 64, kLoads = (BM + BN) / 32;
+  constexpr int kA = BM * kDepth, kStage = (BM + BN) * kDepth;
+  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage];
+  __shared__ __attribute__((aligned(16))) float cols[2][BN];        // the columns' scales and biases
+  const int tile = static_cast<int>(xcd_remap(blockIdx.x, static_cast<int64_t>(ntm) * ntn));
+  // tiles go down 4 rows of tiles, then along n: the 32 tiles that an XCD has at a time share
+  // 4 tiles' rows of a and 8 of b
+  const int group = tile / (4 * ntn), in = tile - group * 4 * ntn;
+  const int high = ntm - group * 4 < 4 ? ntm - group * 4 : 4;
+  const int tm = group * 4 + in % high, tn = in / high;
+  const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+
+  for (int c = threadIdx.x; c < BN; c += kTileLanes) {
+    const int64_t n = n0 + c < p.n ? n0 + c : p.n - 1;
+    cols[0][c] = p.bs[n];
+    cols[1][c] = p.bias ? p.bias[n] : 0.f;
+  }
+  Side<BM, DIRECT> sa(p.a, p.sa, m0, p.m);
+  Side<BN, DIRECT> sb(p.b, p.sb, n0, p.n);
+  i32x16 acc[MI][NI] = {};
+  i32x4 fa[2][MI], fb[2][NI];
+
+  // block i's chunk 2 ks + l / 32 of row l % 32
+  const int r = lane & 31, h = lane >> 5;
+  const auto read = [&](const int8_t* from, int ks, int to) {
+    const int slot = ((2 * ks + h) ^ r) & 7;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      fa[to][i] = *reinterpret_cast<const i32x4*>(from + (wm * (BM / 2) + i * 32 + r) * kDepth + slot * kChunk16);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      fb[to][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * (BN / 2) + i * 32 + r) * kDepth + slot * kChunk16);
+  };
+  const auto multiply = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[from][j], fa[from][i], acc[i][j], 0, 0, 0);
+  };
+
+  const int depths = (p.k + kDepth - 1) / kDepth;
+  const auto left = [&](int t) { return p.k - t * kDepth < kDepth ? p.k - t * kDepth : kDepth; };
+  const auto load = [&](int8_t* to, int t) {
+    sa.load(to, t * kDepth, left(t));
+    sb.load(to + kA, t * kDepth, left(t));
+  };
+  const auto put = [&](int8_t* to) {
+    sa.put(to);
+    sb.put(to + kA);
+  };
+  if (depths > 0) {
+    load(lds, 0);
+    put(lds);
+    if (DIRECT && depths > 1) {
+      load(lds + kStage, 1);
+      all_here<kLoads>();
+    } else {
+      all_here<0>();
+    }
+    read(lds, 0, 0);
+  }
+  // Each step's blocks are read while the step before is multiplied, across depths too: the
+  // barrier comes before a depth's last step, when all of its blocks are in registers.
+  for (int t = 0; t < depths; ++t) {
+    int8_t* now = lds + (t & 1) * kStage;
+    int8_t* next = lds + (~t & 1) * kStage;
+    if (!DIRECT && t + 1 < depths) load(next, t + 1);
+    read(now, 1, 1);
+    multiply(0);
+    read(now, 2, 0);
+    multiply(1);
+    if (t + 1 < depths) put(next);
+    read(now, 3, 1);
+    multiply(0);
+    if (t + 1 < depths) {
+      all_here<0>();
+      if (DIRECT && t + 2 < depths) load(now, t + 2);
+      read(next, 0, 0);
+    }
+    multiply(1);
+  }
+
+  // Outputs: 32 rows of a wave's quarter at a time through LDS of its own, so that a row's
+  // outputs leave in 16-byte words.
+  all_here<0>();
+  constexpr int kCols = BN / 2, kPitch = kCols + 16 / sizeof(Tout), kPer = 16 / sizeof(Tout), kChunks = kCols / kPer;
+  Tout* room = reinterpret_cast<Tout*>(lds + wave * (kStage / 2));
+  static_assert(32 * kPitch * sizeof(Tout) <= kStage / 2, "room for 32 rows");
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t mi = m0 + wm * (BM / 2) + i * 32;
+    const float as = p.as[mi + r < p.m ? mi + r : p.m - 1];
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = j * 32 + g * 8 + h * 4;
+        const f32x4 bs = *reinterpret_cast<const f32x4*>(&cols[0][wn * kCols + c]);
+        const f32x4 bias = *reinterpret_cast<const f32x4*>(&cols[1][wn * kCols + c]);
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(static_cast<float>(acc[i][j][4 * g + e]), as * bs[e], bias[e]);
+        stage(room + r * kPitch + c, v);
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < 32 * kChunks / 64; ++q) {
+      const int at = q * 64 + lane, row = at / kChunks, c = at % kChunks * kPer;
+      const int64_t m = mi + row;
+      const int n = static_cast<int>(n0) + wn * kCols + c;
+      typedef Tout word __attribute__((ext_vector_type(kPer)));
+      typedef word word_any __attribute__((aligned(sizeof(Tout))));
+      const word v = *reinterpret_cast<const word*>(room + row * kPitch + c);
+      if (m >= p.m) continue;
+      Tout* to = static_cast<Tout*>(p.out) + m * p.so + n;
+      if (n + kPer <= p.n) {
+        *reinterpret_cast<word_any*>(to) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (n + e < p.n) to[e] = v[e];
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
 size_t i8_matmul_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
-hipError_t launch_i8_matmul(const MatmulParams& p, size_t, bool bf16, hipStream_t s) {
-  const int ntn = (p.n + 63) / 64;
-  const int64_t tiles = static_cast<int64_t>(ntn) * ((p.m + 63) / 64);
-  if (bf16) hipLaunchKernelGGL((i8_matmul_kernel<bf16_t>), grid_of<256>(tiles), dim3(256), 0, s, p, ntn);
-  else hipLaunchKernelGGL((i8_matmul_kernel<float>), grid_of<256>(tiles), dim3(256), 0, s, p, ntn);
+namespace {
+
+// Rows that loads straight to LDS can take: whole 16-byte chunks, and a tile's rows within 32 bits.
+bool direct(const MatmulParams& p) {
+  const auto fine = [&](const int8_t* q, int64_t stride, int rows) {
+    return reinterpret_cast<uintptr_t>(q) % 16 == 0 && (rows == 1 || (stride % 16 == 0 && stride < (1 << 23)));
+  };
+  return p.k % 16 == 0 && fine(p.a, p.sa, p.m) && fine(p.b, p.sb, p.n);
+}
+
+template <typename Tout, int BM, int BN, bool DIRECT>
+hipError_t tiles(const MatmulParams& p, hipStream_t s) {
+  const int ntm = (p.m - 1) / BM + 1, ntn = (p.n - 1) / BN + 1;
+  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, DIRECT>), dim3(static_cast<unsigned>(ntm) * ntn), dim3(kTileLanes), 0, s, p, ntm, ntn);
   return hipGetLastError();
+}
+
+template <typename Tout>
+hipError_t product(const MatmulParams& p, hipStream_t s) {
+  const int64_t big = static_cast<int64_t>((p.m - 1) / 256 + 1) * ((p.n - 1) / 256 + 1);
+  const int64_t mid = static_cast<int64_t>((p.m - 1) / 128 + 1) * ((p.n - 1) / 128 + 1);
+  if (!direct(p)) return mid >= 256 ? tiles<Tout, 128, 128, false>(p, s) : tiles<Tout, 64, 64, false>(p, s);
+  if (big >= 256) return tiles<Tout, 256, 256, true>(p, s);
+  return mid >= 256 ? tiles<Tout, 128, 128, true>(p, s) : tiles<Tout, 64, 64, true>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_i8_matmul(const MatmulParams& p, size_t, bool bf16, hipStream_t s) {
+  return bf16 ? product<bf16_t>(p, s) : product<float>(p, s);
 }
 
 }  // namespace sscan
