@@ -68,17 +68,24 @@ struct Side {
   // rows past the end repeat the last one: their sums are not written
   __device__ __forceinline__ int row(int i) const { return row0 + 32 * i < last ? row0 + 32 * i : last; }
 
+  // Where in LDS the wave's first load of the rows goes.
+  static __device__ __forceinline__ uint32_t place(int8_t* lds) {
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)lds) + (threadIdx.x >> 6) * 8 * kDepth));
+  }
+  // Load i of bytes k .. k + kDepth, all there.
+  __device__ __forceinline__ void one(uint32_t to, int k, int i) const {
+    bring(to + i * 32 * kDepth, reinterpret_cast<uintptr_t>(base + k), at[i]);
+  }
   // Bytes k .. k + kDepth of the rows, of which `left` are there; zeros for the others.
   __device__ __forceinline__ void load(int8_t* lds, int k, int left) {
     if (DIRECT) {
-      const uint32_t to = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
-          reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)lds) + (threadIdx.x >> 6) * 8 * kDepth));
-      const uintptr_t from = reinterpret_cast<uintptr_t>(base + k);
+      const uint32_t to = place(lds);
       if (left >= kDepth) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) bring(to + i * 32 * kDepth, from, at[i]);
+        for (int i = 0; i < kLoads; ++i) one(to, k, i);
       } else {
-        const uintptr_t zeros = reinterpret_cast<uintptr_t>(g_zeros);
+        const uintptr_t from = reinterpret_cast<uintptr_t>(base + k), zeros = reinterpret_cast<uintptr_t>(g_zeros);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) bring(to + i * 32 * kDepth, chunk * kChunk16 < left ? from + at[i] : zeros);
       }
@@ -145,28 +152,38 @@ __global__ __launch_bounds__(kTileLanes) void i8_tile_kernel(MatmulParams p, int
 
   // block i's chunk 2 ks + l / 32 of row l % 32
   const int r = lane & 31, h = lane >> 5;
-  const auto read = [&](const int8_t* from, int ks, int to) {
+  const auto fetch = [&](const int8_t* from, int ks, int to, int i) {
     const int slot = ((2 * ks + h) ^ r) & 7;
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-      fa[to][i] = *reinterpret_cast<const i32x4*>(from + (wm * (BM / 2) + i * 32 + r) * kDepth + slot * kChunk16);
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
+    if (i < NI)
       fb[to][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * (BN / 2) + i * 32 + r) * kDepth + slot * kChunk16);
+    else
+      fa[to][i - NI] = *reinterpret_cast<const i32x4*>(from + (wm * (BM / 2) + (i - NI) * 32 + r) * kDepth + slot * kChunk16);
   };
-  const auto multiply = [&](int from) {
+  // A step: blocks `with` are multiplied while those of step ks of `from` are read and, one at a
+  // time, loads for a later depth are begun.  The order is fixed: left to itself the compiler
+  // reads blocks when they are needed, and the matrix unit waits for them.
+  constexpr int Q = MI * NI, R = MI + NI;
+  const auto step = [&](int with, const int8_t* from, int ks, auto&& begin) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int q = 0; q < Q; ++q) {
 #pragma unroll
-      for (int j = 0; j < NI; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[from][j], fa[from][i], acc[i][j], 0, 0, 0);
+      for (int i = 2 * q * R / Q; i < 2 * (q + 1) * R / Q && i < R; ++i) fetch(from, ks, with ^ 1, i);
+#pragma unroll
+      for (int i = q * kLoads / Q; i < (q + 1) * kLoads / Q; ++i) begin(i);
+      acc[q / NI][q % NI] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[with][q % NI], fa[with][q / NI], acc[q / NI][q % NI], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
+  const auto nothing = [](int) {};
 
-  const int depths = (p.k + kDepth - 1) / kDepth;
-  const auto left = [&](int t) { return p.k - t * kDepth < kDepth ? p.k - t * kDepth : kDepth; };
+  // The depths of k: what k has beyond whole depths comes first, filled up with zeros, so that
+  // all later ones are whole.
+  const int rest = p.k % kDepth, depths = (p.k + kDepth - 1) / kDepth;
+  const auto start = [&](int t) { return t == 0 ? 0 : t * kDepth - (rest ? kDepth - rest : 0); };
   const auto load = [&](int8_t* to, int t) {
-    sa.load(to, t * kDepth, left(t));
-    sb.load(to + kA, t * kDepth, left(t));
+    const int n = t == 0 && rest ? rest : kDepth;
+    sa.load(to, start(t), n);
+    sb.load(to + kA, start(t), n);
   };
   const auto put = [&](int8_t* to) {
     sa.put(to);
@@ -181,27 +198,29 @@ __global__ __launch_bounds__(kTileLanes) void i8_tile_kernel(MatmulParams p, int
     } else {
       all_here<0>();
     }
-    read(lds, 0, 0);
+#pragma unroll
+    for (int i = 0; i < R; ++i) fetch(lds, 0, 0, i);
   }
   // Each step's blocks are read while the step before is multiplied, across depths too: the
-  // barrier comes before a depth's last step, when all of its blocks are in registers.
+  // barrier comes before a depth's last step, when all of its blocks are in registers.  (The
+  // last depth reads what is not there yet, and does not use it.)
   for (int t = 0; t < depths; ++t) {
     int8_t* now = lds + (t & 1) * kStage;
     int8_t* next = lds + (~t & 1) * kStage;
     if (!DIRECT && t + 1 < depths) load(next, t + 1);
-    read(now, 1, 1);
-    multiply(0);
-    read(now, 2, 0);
-    multiply(1);
-    if (t + 1 < depths) put(next);
-    read(now, 3, 1);
-    multiply(0);
-    if (t + 1 < depths) {
-      all_here<0>();
-      if (DIRECT && t + 2 < depths) load(now, t + 2);
-      read(next, 0, 0);
-    }
-    multiply(1);
+    step(0, now, 1, nothing);
+    step(1, now, 2, nothing);
+    if (!DIRECT && t + 1 < depths) put(next);
+    step(0, now, 3, nothing);
+    all_here<0>();
+    const bool more = DIRECT && t + 2 < depths;
+    const uint32_t ta = Side<BM, DIRECT>::place(now), tb = Side<BN, DIRECT>::place(now + kA);
+    const int k = start(t + 2);
+    step(1, next, 0, [&](int i) {
+      if (!more) return;
+      if (i < BM / 32) sa.one(ta, k, i);
+      else sb.one(tb, k, i - BM / 32);
+    });
   }
 
   // Outputs: 32 rows of a wave's quarter at a time through LDS of its own, so that a row's
