@@ -6,6 +6,7 @@
 // holds row l % 32, bytes 16 (l / 32) .. + 15 of 32).  The order of k is the same on both
 // sides and otherwise free, since the sums are whole numbers.
 #include "sscan_layer.h"
+#include <cstdlib>
 
 namespace sscan {
 
@@ -14,9 +15,7 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef i32x4 i32x4_any __attribute__((aligned(1)));
 
-constexpr int kDepth = 128;            // bytes of k staged at a time
 constexpr int kChunk16 = 16;           // bytes of a chunk
-constexpr int kTileLanes = 256;        // lanes of a workgroup: four waves, two by two
 
 // All waves of the workgroup are here, with nothing of theirs under way but the newest VM
 // loads into LDS.  What the compiler sees as memory stays on its side.
@@ -43,13 +42,20 @@ __device__ __forceinline__ void bring(uint32_t to, uintptr_t base, uint32_t at) 
 
 __device__ __attribute__((aligned(16))) const int8_t g_zeros[kChunk16] = {};
 
-// One side's rows of a tile on their way to LDS.  A chunk of row r goes to slot
-// (chunk ^ r) & 7 of the row's 128 bytes, so that 8 lanes that read one chunk of 8 rows
-// take all banks once.  Lane l of a wave brings chunk (l ^ l / 8) & 7 of row l / 8 of 8 rows:
-// LDS is then filled in the lanes' order, which is what a load straight to LDS does.
-template <int ROWS, bool DIRECT>
+// One side's rows of a tile on their way to LDS, DEPTH bytes of k at a time.  A chunk of row r
+// goes to a slot of the row's DEPTH bytes that differs from row to row (slot_of), so that 16
+// lanes that read one chunk of 16 rows take all 64 banks once.  The lanes of a wave bring
+// slot after slot of row after row: LDS is then filled in the lanes' order, which is what a
+// load straight to LDS does.
+template <int DEPTH>
+__device__ __forceinline__ int slot_of(int row, int chunk) {
+  return DEPTH == 128 ? (chunk ^ (row >> 1)) & 7 : (chunk ^ (row >> 2)) & 3;
+}
+template <int ROWS, int WAVES, int DEPTH, bool DIRECT>
 struct Side {
-  static constexpr int kLoads = ROWS / 32;
+  static constexpr int kChunks = DEPTH / kChunk16, kStep = 64 / kChunks * WAVES;   // rows of one load of all waves
+  static constexpr int kLoads = ROWS / kStep;
+  static_assert(ROWS % kStep == 0 && kStep % 16 == 0, "the lane's chunk is the same in all its rows");
   const int8_t* base;
   uint32_t at[kLoads];       // DIRECT: bytes from base to the lane's rows
   int64_t stride;
@@ -57,37 +63,36 @@ struct Side {
   i32x4 held[DIRECT ? 1 : kLoads];
 
   __device__ __forceinline__ Side(const int8_t* p, int64_t st, int64_t r0, int rows) : stride(st) {
-    const int lane = threadIdx.x & 63;
     base = p + r0 * st;
-    row0 = (threadIdx.x >> 6) * 8 + (lane >> 3);
+    row0 = threadIdx.x / kChunks;
     last = static_cast<int>(rows - r0 < ROWS ? rows - r0 : ROWS) - 1;
-    chunk = (lane ^ (lane >> 3)) & 7;
+    chunk = slot_of<DEPTH>(row0, threadIdx.x % kChunks);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) at[i] = static_cast<uint32_t>(row(i) * st + chunk * kChunk16);
   }
   // rows past the end repeat the last one: their sums are not written
-  __device__ __forceinline__ int row(int i) const { return row0 + 32 * i < last ? row0 + 32 * i : last; }
+  __device__ __forceinline__ int row(int i) const { return row0 + kStep * i < last ? row0 + kStep * i : last; }
 
   // Where in LDS the wave's first load of the rows goes.
   static __device__ __forceinline__ uint32_t place(int8_t* lds) {
     return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
-        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)lds) + (threadIdx.x >> 6) * 8 * kDepth));
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)lds) + (threadIdx.x >> 6) * 64 * kChunk16));
   }
-  // Load i of bytes k .. k + kDepth, all there.
+  // Load i of bytes k .. k + DEPTH, all there.
   __device__ __forceinline__ void one(uint32_t to, int k, int i) const {
-    bring(to + i * 32 * kDepth, reinterpret_cast<uintptr_t>(base + k), at[i]);
+    bring(to + i * kStep * DEPTH, reinterpret_cast<uintptr_t>(base + k), at[i]);
   }
-  // Bytes k .. k + kDepth of the rows, of which `left` are there; zeros for the others.
+  // Bytes k .. k + DEPTH of the rows, of which `left` are there; zeros for the others.
   __device__ __forceinline__ void load(int8_t* lds, int k, int left) {
     if (DIRECT) {
       const uint32_t to = place(lds);
-      if (left >= kDepth) {
+      if (left >= DEPTH) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) one(to, k, i);
       } else {
         const uintptr_t from = reinterpret_cast<uintptr_t>(base + k), zeros = reinterpret_cast<uintptr_t>(g_zeros);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) bring(to + i * 32 * kDepth, chunk * kChunk16 < left ? from + at[i] : zeros);
+        for (int i = 0; i < kLoads; ++i) bring(to + i * kStep * DEPTH, chunk * kChunk16 < left ? from + at[i] : zeros);
       }
     } else {
 #pragma unroll
@@ -109,7 +114,7 @@ struct Side {
     if (DIRECT) return;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<i32x4*>(lds + (i * 32 + (threadIdx.x >> 6) * 8) * kDepth + (threadIdx.x & 63) * kChunk16) = held[i];
+      *reinterpret_cast<i32x4*>(lds + i * kStep * DEPTH + threadIdx.x * kChunk16) = held[i];
   }
 };
 
@@ -121,14 +126,17 @@ __device__ __forceinline__ void stage(bf16_t* p, f32x4 v) {
   *reinterpret_cast<u4*>(p) = __builtin_bit_cast(u4, __builtin_convertvector(v, b4));
 }
 
-// A workgroup's tile of BM x BN sums; wave (wm, wn) of two by two has a quarter, MI x NI blocks of
-// 32 x 32.  LDS holds two depths of k: while one is multiplied the next is on its way.  The
+// A workgroup's tile of BM x BN sums; its WM x WN waves have a part of MI x NI blocks of 32 x 32
+// each.  LDS holds two depths of k: while one is multiplied the next is on its way.  The
 // instruction's rows are n and its columns m, so that a lane ends with neighbouring outputs.
-template <typename Tout, int BM, int BN, bool DIRECT>
-__global__ __launch_bounds__(kTileLanes) void i8_tile_kernel(MatmulParams p, int ntm, int ntn) {
-  constexpr int MI = BM / 64, NI = BN / 64, kLoads = (BM + BN) / 32;
-  constexpr int kA = BM * kDepth, kStage = (BM + BN) * kDepth;
-  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage];
+template <typename Tout, int BM, int BN, int WM, int WN, int DEPTH, int GROUPS, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_kernel(MatmulParams p, int ntm, int ntn) {
+  constexpr int kWaves = WM * WN, kRows = BM / WM, kCols = BN / WN, MI = kRows / 32, NI = kCols / 32;
+  typedef Side<BM, kWaves, DEPTH, DIRECT> A;
+  typedef Side<BN, kWaves, DEPTH, DIRECT> B;
+  constexpr int kLoads = A::kLoads + B::kLoads, kA = BM * DEPTH, kStage = (BM + BN) * DEPTH;
+  constexpr int kPitch = kCols + 16 / sizeof(Tout), kRoom = 32 * kPitch * sizeof(Tout);   // outputs of 32 rows
+  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage > kWaves * kRoom ? 2 * kStage : kWaves * kRoom];
   __shared__ __attribute__((aligned(16))) float cols[2][BN];        // the columns' scales and biases
   const int tile = static_cast<int>(xcd_remap(blockIdx.x, static_cast<int64_t>(ntm) * ntn));
   // tiles go down 4 rows of tiles, then along n: the 32 tiles that an XCD has at a time share
@@ -138,26 +146,26 @@ __global__ __launch_bounds__(kTileLanes) void i8_tile_kernel(MatmulParams p, int
   const int tm = group * 4 + in % high, tn = in / high;
   const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
 
-  for (int c = threadIdx.x; c < BN; c += kTileLanes) {
+  for (int c = threadIdx.x; c < BN; c += 64 * kWaves) {
     const int64_t n = n0 + c < p.n ? n0 + c : p.n - 1;
     cols[0][c] = p.bs[n];
     cols[1][c] = p.bias ? p.bias[n] : 0.f;
   }
-  Side<BM, DIRECT> sa(p.a, p.sa, m0, p.m);
-  Side<BN, DIRECT> sb(p.b, p.sb, n0, p.n);
+  A sa(p.a, p.sa, m0, p.m);
+  B sb(p.b, p.sb, n0, p.n);
   i32x16 acc[MI][NI] = {};
   i32x4 fa[2][MI], fb[2][NI];
 
   // block i's chunk 2 ks + l / 32 of row l % 32
   const int r = lane & 31, h = lane >> 5;
   const auto fetch = [&](const int8_t* from, int ks, int to, int i) {
-    const int slot = ((2 * ks + h) ^ r) & 7;
+    const int slot = slot_of<DEPTH>(r, 2 * ks + h);
     if (i < NI)
-      fb[to][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * (BN / 2) + i * 32 + r) * kDepth + slot * kChunk16);
+      fb[to][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * kCols + i * 32 + r) * DEPTH + slot * kChunk16);
     else
-      fa[to][i - NI] = *reinterpret_cast<const i32x4*>(from + (wm * (BM / 2) + (i - NI) * 32 + r) * kDepth + slot * kChunk16);
+      fa[to][i - NI] = *reinterpret_cast<const i32x4*>(from + (wm * kRows + (i - NI) * 32 + r) * DEPTH + slot * kChunk16);
   };
   // A step: blocks `with` are multiplied while those of step ks of `from` are read and, one at a
   // time, loads for a later depth are begun.  The order is fixed: left to itself the compiler
@@ -178,10 +186,10 @@ __global__ __launch_bounds__(kTileLanes) void i8_tile_kernel(MatmulParams p, int
 
   // The depths of k: what k has beyond whole depths comes first, filled up with zeros, so that
   // all later ones are whole.
-  const int rest = p.k % kDepth, depths = (p.k + kDepth - 1) / kDepth;
-  const auto start = [&](int t) { return t == 0 ? 0 : t * kDepth - (rest ? kDepth - rest : 0); };
+  const int rest = p.k % DEPTH, depths = (p.k + DEPTH - 1) / DEPTH;
+  const auto start = [&](int t) { return t == 0 ? 0 : t * DEPTH - (rest ? DEPTH - rest : 0); };
   const auto load = [&](int8_t* to, int t) {
-    const int n = t == 0 && rest ? rest : kDepth;
+    const int n = t == 0 && rest ? rest : DEPTH;
     sa.load(to, start(t), n);
     sb.load(to + kA, start(t), n);
   };
@@ -209,29 +217,28 @@ __global__ __launch_bounds__(kTileLanes) void i8_tile_kernel(MatmulParams p, int
     int8_t* next = lds + (~t & 1) * kStage;
     if (!DIRECT && t + 1 < depths) load(next, t + 1);
     step(0, now, 1, nothing);
-    step(1, now, 2, nothing);
+    if (DEPTH == 128) step(1, now, 2, nothing);
     if (!DIRECT && t + 1 < depths) put(next);
-    step(0, now, 3, nothing);
+    if (DEPTH == 128) step(0, now, 3, nothing);
     all_here<0>();
     const bool more = DIRECT && t + 2 < depths;
-    const uint32_t ta = Side<BM, DIRECT>::place(now), tb = Side<BN, DIRECT>::place(now + kA);
+    const uint32_t ta = A::place(now), tb = B::place(now + kA);
     const int k = start(t + 2);
     step(1, next, 0, [&](int i) {
       if (!more) return;
-      if (i < BM / 32) sa.one(ta, k, i);
-      else sb.one(tb, k, i - BM / 32);
+      if (i < A::kLoads) sa.one(ta, k, i);
+      else sb.one(tb, k, i - A::kLoads);
     });
   }
 
-  // Outputs: 32 rows of a wave's quarter at a time through LDS of its own, so that a row's
+  // Outputs: 32 rows of a wave's part at a time through LDS of its own, so that a row's
   // outputs leave in 16-byte words.
   all_here<0>();
-  constexpr int kCols = BN / 2, kPitch = kCols + 16 / sizeof(Tout), kPer = 16 / sizeof(Tout), kChunks = kCols / kPer;
-  Tout* room = reinterpret_cast<Tout*>(lds + wave * (kStage / 2));
-  static_assert(32 * kPitch * sizeof(Tout) <= kStage / 2, "room for 32 rows");
+  constexpr int kPer = 16 / sizeof(Tout), kChunks = kCols / kPer;
+  Tout* room = reinterpret_cast<Tout*>(lds + wave * kRoom);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int64_t mi = m0 + wm * (BM / 2) + i * 32;
+    const int64_t mi = m0 + wm * kRows + i * 32;
     const float as = p.as[mi + r < p.m ? mi + r : p.m - 1];
 #pragma unroll
     for (int j = 0; j < NI; ++j)
@@ -280,10 +287,11 @@ bool direct(const MatmulParams& p) {
   return p.k % 16 == 0 && fine(p.a, p.sa, p.m) && fine(p.b, p.sb, p.n);
 }
 
-template <typename Tout, int BM, int BN, bool DIRECT>
+template <typename Tout, int BM, int BN, int WM, int WN, int DEPTH, int GROUPS, bool DIRECT>
 hipError_t tiles(const MatmulParams& p, hipStream_t s) {
   const int ntm = (p.m - 1) / BM + 1, ntn = (p.n - 1) / BN + 1;
-  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, DIRECT>), dim3(static_cast<unsigned>(ntm) * ntn), dim3(kTileLanes), 0, s, p, ntm, ntn);
+  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, DEPTH, GROUPS, DIRECT>), dim3(static_cast<unsigned>(ntm) * ntn),
+                     dim3(64 * WM * WN), 0, s, p, ntm, ntn);
   return hipGetLastError();
 }
 
@@ -291,9 +299,20 @@ template <typename Tout>
 hipError_t product(const MatmulParams& p, hipStream_t s) {
   const int64_t big = static_cast<int64_t>((p.m - 1) / 256 + 1) * ((p.n - 1) / 256 + 1);
   const int64_t mid = static_cast<int64_t>((p.m - 1) / 128 + 1) * ((p.n - 1) / 128 + 1);
-  if (!direct(p)) return mid >= 256 ? tiles<Tout, 128, 128, false>(p, s) : tiles<Tout, 64, 64, false>(p, s);
-  if (big >= 256) return tiles<Tout, 256, 256, true>(p, s);
-  return mid >= 256 ? tiles<Tout, 128, 128, true>(p, s) : tiles<Tout, 64, 64, true>(p, s);
+  if (!direct(p)) return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 128, 2, false>(p, s) : tiles<Tout, 64, 64, 2, 2, 128, 2, false>(p, s);
+  const char* e = getenv("MM_V");
+  const int v = e ? atoi(e) : 0;
+  if (v == 1) return tiles<Tout, 256, 256, 2, 2, 128, 1, true>(p, s);
+  if (v == 2) return tiles<Tout, 256, 256, 2, 4, 128, 1, true>(p, s);
+  if (v == 3) return tiles<Tout, 256, 128, 2, 2, 64, 2, true>(p, s);
+  if (v == 4) return tiles<Tout, 128, 128, 2, 2, 128, 2, true>(p, s);
+  if (v == 5) return tiles<Tout, 128, 128, 2, 2, 64, 3, true>(p, s);
+  if (v == 6) return tiles<Tout, 128, 256, 2, 2, 64, 2, true>(p, s);
+  if (v == 7) return tiles<Tout, 256, 128, 4, 2, 128, 1, true>(p, s);
+  if (v == 8) return tiles<Tout, 64, 64, 2, 2, 128, 2, true>(p, s);
+  if (v == 9) return tiles<Tout, 128, 64, 2, 2, 128, 2, true>(p, s);
+  if (big >= 256) return tiles<Tout, 256, 256, 2, 2, 128, 1, true>(p, s);
+  return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 128, 2, true>(p, s) : tiles<Tout, 64, 64, 2, 2, 128, 2, true>(p, s);
 }
 
 }  // namespace
