@@ -2,19 +2,22 @@
 //
 // out[m, n] = (sum_k a[m, k] b[n, k]) (as[m] bs[n]) + bias[n].  Both sides have k along their
 // rows, so both go through LDS the same way: 128 bytes of each row at a time, in 16-byte
-// chunks, which are what a lane of a matrix instruction takes (v_mfma_i32_32x32x32_i8: lane l
-// holds row l % 32, bytes 16 (l / 32) .. + 15 of 32).  The order of k is the same on both
+// chunks, which are what a lane of a matrix instruction takes (v_mfma_i32_16x16x64_i8: lane l
+// holds row l % 16, bytes 16 (l / 16) .. + 15 of 64).  The order of k is the same on both
 // sides and otherwise free, since the sums are whole numbers.
+//
+// Large products are bound by power: the matrix units alone, on random codes, reach 4100
+// TOP/s with this instruction and 3450 with v_mfma_i32_32x32x32_i8, on zeros 4850 and 4970.
 #include "sscan_layer.h"
 #include <cstdlib>
 
 namespace sscan {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef i32x4 i32x4_any __attribute__((aligned(1)));
 
+constexpr int kUnits = 256;            // compute units
 constexpr int kChunk16 = 16;           // bytes of a chunk
 
 // All waves of the workgroup are here, with nothing of theirs under way but the newest VM
@@ -62,7 +65,9 @@ struct Side {
   int row0, last, chunk;     // the lane's first row, the last row there is, its chunk
   i32x4 held[DIRECT ? 1 : kLoads];
 
-  __device__ __forceinline__ Side(const int8_t* p, int64_t st, int64_t r0, int rows) : stride(st) {
+  // The rows from r0 on of `rows` rows.
+  __device__ __forceinline__ void aim(const int8_t* p, int64_t st, int64_t r0, int rows) {
+    stride = st;
     base = p + r0 * st;
     row0 = threadIdx.x / kChunks;
     last = static_cast<int>(rows - r0 < ROWS ? rows - r0 : ROWS) - 1;
@@ -78,40 +83,28 @@ struct Side {
     return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)lds) + (threadIdx.x >> 6) * 64 * kChunk16));
   }
-  // Load i of bytes k .. k + DEPTH, all there.
-  __device__ __forceinline__ void one(uint32_t to, int k, int i) const {
-    bring(to + i * kStep * DEPTH, reinterpret_cast<uintptr_t>(base + k), at[i]);
+  // DIRECT: load i of bytes k .. k + DEPTH, of which `left` are there; zeros for the others.
+  __device__ __forceinline__ void one(uint32_t to, int k, int left, int i) const {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(base + k);
+    if (left == DEPTH) bring(to + i * kStep * DEPTH, from, at[i]);
+    else bring(to + i * kStep * DEPTH, chunk * kChunk16 < left ? from + at[i] : reinterpret_cast<uintptr_t>(g_zeros));
   }
-  // Bytes k .. k + DEPTH of the rows, of which `left` are there; zeros for the others.
-  __device__ __forceinline__ void load(int8_t* lds, int k, int left) {
-    if (DIRECT) {
-      const uint32_t to = place(lds);
-      if (left >= DEPTH) {
+  // The same by way of registers, from any address.
+  __device__ __forceinline__ void hold(int k, int left) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) one(to, k, i);
+    for (int i = 0; i < kLoads; ++i) {
+      const int8_t* from = base + row(i) * stride + k + chunk * kChunk16;
+      const int n = left - chunk * kChunk16;
+      if (n >= kChunk16) {
+        held[i] = *reinterpret_cast<const i32x4_any*>(from);
       } else {
-        const uintptr_t from = reinterpret_cast<uintptr_t>(base + k), zeros = reinterpret_cast<uintptr_t>(g_zeros);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) bring(to + i * kStep * DEPTH, chunk * kChunk16 < left ? from + at[i] : zeros);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int8_t* from = base + row(i) * stride + k + chunk * kChunk16;
-        const int n = left - chunk * kChunk16;
-        if (n >= kChunk16) {
-          held[i] = *reinterpret_cast<const i32x4_any*>(from);
-        } else {
-          uint32_t w[4] = {};
-          for (int j = 0; j < n; ++j) w[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(from[j])) << 8 * (j % 4);
-          held[i] = i32x4{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
-        }
+        uint32_t w[4] = {};
+        for (int j = 0; j < n; ++j) w[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(from[j])) << 8 * (j % 4);
+        held[i] = i32x4{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
       }
     }
   }
-  // What load() left in registers, to LDS.
-  __device__ __forceinline__ void put(int8_t* lds) {
-    if (DIRECT) return;
+  __device__ __forceinline__ void put(int8_t* lds) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       *reinterpret_cast<i32x4*>(lds + i * kStep * DEPTH + threadIdx.x * kChunk16) = held[i];
@@ -119,159 +112,251 @@ struct Side {
 };
 
 // Four neighbouring outputs of a row in Tout.
-__device__ __forceinline__ void stage(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
-__device__ __forceinline__ void stage(bf16_t* p, f32x4 v) {
+__device__ __forceinline__ void stage_out(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void stage_out(bf16_t* p, f32x4 v) {
   typedef __bf16 b4 __attribute__((ext_vector_type(4)));
   typedef uint16_t u4 __attribute__((ext_vector_type(4)));
   *reinterpret_cast<u4*>(p) = __builtin_bit_cast(u4, __builtin_convertvector(v, b4));
 }
 
-// A workgroup's tile of BM x BN sums; its WM x WN waves have a part of MI x NI blocks of 32 x 32
-// each.  LDS holds two depths of k: while one is multiplied the next is on its way.  The
+// Workgroups take tiles of BM x BN sums one after another; their WM x WN waves have a part of
+// MI x NI blocks of 16 x 16 each.  LDS holds two depths of k: while one is multiplied the next
+// is on its way, and the next tile's first ones while a tile's outputs leave.  The
 // instruction's rows are n and its columns m, so that a lane ends with neighbouring outputs.
 template <typename Tout, int BM, int BN, int WM, int WN, int DEPTH, int GROUPS, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_kernel(MatmulParams p, int ntm, int ntn) {
-  constexpr int kWaves = WM * WN, kRows = BM / WM, kCols = BN / WN, MI = kRows / 32, NI = kCols / 32;
+  constexpr int kWaves = WM * WN, kLanes = 64 * kWaves, kRows = BM / WM, kCols = BN / WN, MI = kRows / 16, NI = kCols / 16;
   typedef Side<BM, kWaves, DEPTH, DIRECT> A;
   typedef Side<BN, kWaves, DEPTH, DIRECT> B;
   constexpr int kLoads = A::kLoads + B::kLoads, kA = BM * DEPTH, kStage = (BM + BN) * DEPTH;
-  constexpr int kPitch = kCols + 16 / sizeof(Tout), kRoom = 32 * kPitch * sizeof(Tout);   // outputs of 32 rows
-  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage > kWaves * kRoom ? 2 * kStage : kWaves * kRoom];
-  __shared__ __attribute__((aligned(16))) float cols[2][BN];        // the columns' scales and biases
-  const int tile = static_cast<int>(xcd_remap(blockIdx.x, static_cast<int64_t>(ntm) * ntn));
-  // tiles go down 4 rows of tiles, then along n: the 32 tiles that an XCD has at a time share
-  // 4 tiles' rows of a and 8 of b
-  const int group = tile / (4 * ntn), in = tile - group * 4 * ntn;
-  const int high = ntm - group * 4 < 4 ? ntm - group * 4 : 4;
-  const int tm = group * 4 + in % high, tn = in / high;
-  const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
+  constexpr int kPer = 16 / sizeof(Tout), kSpan = 4 * kPer, kPitch = kSpan + kPer;   // outputs of a row that leave at a time
+  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage];
+  __shared__ __attribute__((aligned(16))) float scale[3][2 * BN + BM];   // of three tiles: b's scales, biases, a's
+  __shared__ __attribute__((aligned(16))) Tout room[kWaves][32 * kPitch];
+  const int tiles = ntm * ntn;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-
-  for (int c = threadIdx.x; c < BN; c += 64 * kWaves) {
-    const int64_t n = n0 + c < p.n ? n0 + c : p.n - 1;
-    cols[0][c] = p.bs[n];
-    cols[1][c] = p.bias ? p.bias[n] : 0.f;
-  }
-  A sa(p.a, p.sa, m0, p.m);
-  B sb(p.b, p.sb, n0, p.n);
-  i32x16 acc[MI][NI] = {};
-  i32x4 fa[2][MI], fb[2][NI];
-
-  // block i's chunk 2 ks + l / 32 of row l % 32
-  const int r = lane & 31, h = lane >> 5;
-  const auto fetch = [&](const int8_t* from, int ks, int to, int i) {
-    const int slot = slot_of<DEPTH>(r, 2 * ks + h);
-    if (i < NI)
-      fb[to][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * kCols + i * 32 + r) * DEPTH + slot * kChunk16);
-    else
-      fa[to][i - NI] = *reinterpret_cast<const i32x4*>(from + (wm * kRows + (i - NI) * 32 + r) * DEPTH + slot * kChunk16);
+  // Where the workgroup's tile of turn v begins.  Tiles go down 4 rows of tiles, then along n:
+  // the 32 tiles that an XCD has at a time share 4 tiles' rows of a and 8 of b.
+  const auto place = [&](int v, int64_t& m0, int64_t& n0) {
+    const int tile = static_cast<int>(xcd_remap(v, tiles));
+    const int group = tile / (4 * ntn), in = tile - group * 4 * ntn;
+    const int high = ntm - group * 4 < 4 ? ntm - group * 4 : 4;
+    m0 = static_cast<int64_t>(group * 4 + in % high) * BM;
+    n0 = static_cast<int64_t>(in / high) * BN;
   };
-  // A step: blocks `with` are multiplied while those of step ks of `from` are read and, one at a
-  // time, loads for a later depth are begun.  The order is fixed: left to itself the compiler
-  // reads blocks when they are needed, and the matrix unit waits for them.
-  constexpr int Q = MI * NI, R = MI + NI;
-  const auto step = [&](int with, const int8_t* from, int ks, auto&& begin) {
+
+  // A depth is S slots, each a block of a's rows times all of b's: the order within a slot, and
+  // of slots, is fixed (left to itself the compiler reads blocks when they are needed, and the
+  // matrix unit waits for them).  A slot reads a's block for kAhead slots later, the last kAhead
+  // slots of a step also b's blocks of the next step.
+  constexpr int KS = DEPTH / 64, S = KS * MI, kAhead = MI > 3 ? 3 : MI - 1, kRing = kAhead + 1;
+  static_assert(S % kRing == 0 && KS % 2 == 0 && MI % 2 == 0, "places of blocks are constants");
+  i32x4 acc[MI][NI] = {}, fa[kRing], fb[2][NI];
+  // a block's chunk 4 ks + l / 16 of row l % 16
+  const int r = lane & 15, h = lane >> 4;
+  const auto fetch_a = [&](const int8_t* from, int s) {
+    fa[s % kRing] = *reinterpret_cast<const i32x4*>(from + (wm * kRows + s % MI * 16 + r) * DEPTH + slot_of<DEPTH>(r, s / MI * 4 + h) * kChunk16);
+  };
+  const auto fetch_b = [&](const int8_t* from, int ks, int i) {
+    fb[ks & 1][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * kCols + i * 16 + r) * DEPTH + slot_of<DEPTH>(r, ks * 4 + h) * kChunk16);
+  };
+  const auto slot = [&](const int8_t* now, const int8_t* next, int s, auto&& begin) {
+    const int ks = s / MI, late = s % MI - (MI - kAhead);   // 0 .. kAhead - 1 in the last slots of a step
+    if (s + kAhead < S) fetch_a(now, s + kAhead);
+    else fetch_a(next, s + kAhead - S);
+    if (late >= 0) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
+      for (int i = late * NI / kAhead; i < (late + 1) * NI / kAhead; ++i) fetch_b(ks + 1 < KS ? now : next, (ks + 1) % KS, i);
+      if (ks + 1 == KS) {
 #pragma unroll
-      for (int i = 2 * q * R / Q; i < 2 * (q + 1) * R / Q && i < R; ++i) fetch(from, ks, with ^ 1, i);
-#pragma unroll
-      for (int i = q * kLoads / Q; i < (q + 1) * kLoads / Q; ++i) begin(i);
-      acc[q / NI][q % NI] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[with][q % NI], fa[with][q / NI], acc[q / NI][q % NI], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int i = late * kLoads / kAhead; i < (late + 1) * kLoads / kAhead; ++i) begin(i);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      acc[s % MI][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[ks & 1][j], fa[s % kRing], acc[s % MI][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
   };
   const auto nothing = [](int) {};
 
-  // The depths of k: what k has beyond whole depths comes first, filled up with zeros, so that
-  // all later ones are whole.
-  const int rest = p.k % DEPTH, depths = (p.k + DEPTH - 1) / DEPTH;
-  const auto start = [&](int t) { return t == 0 ? 0 : t * DEPTH - (rest ? DEPTH - rest : 0); };
-  const auto load = [&](int8_t* to, int t) {
-    const int n = t == 0 && rest ? rest : DEPTH;
-    sa.load(to, start(t), n);
-    sb.load(to + kA, start(t), n);
+  // The depths of k: what k has beyond whole depths comes first, filled up with zeros.  The
+  // workgroup loads depth after depth, tile after tile; (lv, lt) is the next to load.
+  const int rest = p.k % DEPTH ? p.k % DEPTH : DEPTH, depths = (p.k + DEPTH - 1) / DEPTH;
+  A sa;
+  B sb;
+  int lv = blockIdx.x, lt = 0;
+  const auto aim = [&]() {
+    int64_t m0, n0;
+    place(lv, m0, n0);
+    sa.aim(p.a, p.sa, m0, p.m);
+    sb.aim(p.b, p.sb, n0, p.n);
+  };
+  const auto k_of = [&]() { return lt == 0 ? 0 : rest + (lt - 1) * DEPTH; };
+  const auto left_of = [&]() { return lt == 0 ? rest : DEPTH; };
+  const auto begin = [&](uint32_t ta, uint32_t tb, int k, int left, int i) {
+    if (i < A::kLoads) sa.one(ta, k, left, i);
+    else sb.one(tb, k, left, i - A::kLoads);
+  };
+  const auto hold = [&]() {
+    sa.hold(k_of(), left_of());
+    sb.hold(k_of(), left_of());
   };
   const auto put = [&](int8_t* to) {
     sa.put(to);
     sb.put(to + kA);
   };
+  const auto advance = [&]() {
+    if (++lt < depths) return;
+    lt = 0;
+    lv += gridDim.x;
+    if (lv < tiles) aim();
+  };
   if (depths > 0) {
-    load(lds, 0);
-    put(lds);
-    if (DIRECT && depths > 1) {
-      load(lds + kStage, 1);
-      all_here<kLoads>();
-    } else {
-      all_here<0>();
-    }
+    aim();
+    if (DIRECT) {
+      for (int d = 0; d < 2 && lv < tiles; ++d) {
+        const uint32_t ta = A::place(lds + d * kStage), tb = B::place(lds + d * kStage + kA);
 #pragma unroll
-    for (int i = 0; i < R; ++i) fetch(lds, 0, 0, i);
+        for (int i = 0; i < kLoads; ++i) begin(ta, tb, k_of(), left_of(), i);
+        advance();
+      }
+    } else {
+      hold();
+      put(lds);
+      advance();
+    }
   }
-  // Each step's blocks are read while the step before is multiplied, across depths too: the
-  // barrier comes before a depth's last step, when all of its blocks are in registers.  (The
-  // last depth reads what is not there yet, and does not use it.)
-  for (int t = 0; t < depths; ++t) {
-    int8_t* now = lds + (t & 1) * kStage;
-    int8_t* next = lds + (~t & 1) * kStage;
-    if (!DIRECT && t + 1 < depths) load(next, t + 1);
-    step(0, now, 1, nothing);
-    if (DEPTH == 128) step(1, now, 2, nothing);
-    if (!DIRECT && t + 1 < depths) put(next);
-    if (DEPTH == 128) step(0, now, 3, nothing);
-    all_here<0>();
-    const bool more = DIRECT && t + 2 < depths;
-    const uint32_t ta = A::place(now), tb = B::place(now + kA);
-    const int k = start(t + 2);
-    step(1, next, 0, [&](int i) {
-      if (!more) return;
-      if (i < A::kLoads) sa.one(ta, k, i);
-      else sb.one(tb, k, i - A::kLoads);
-    });
+  // A tile's scales go to LDS in the last depth of the tile before, in three places in turn: a
+  // wave that is still with the outputs of the tile before that keeps its own.
+  float sc[(2 * BN + BM + kLanes - 1) / kLanes];
+  const auto get_scales = [&](int v) {
+    int64_t m0, n0;
+    place(v, m0, n0);
+#pragma unroll
+    for (int i = 0; i * kLanes < 2 * BN + BM; ++i) {
+      const int at = i * kLanes + threadIdx.x;
+      const int64_t n = n0 + at % BN < p.n ? n0 + at % BN : p.n - 1, m = m0 + at - 2 * BN < p.m ? m0 + at - 2 * BN : p.m - 1;
+      sc[i] = at < BN ? p.bs[n] : at < 2 * BN ? (p.bias ? p.bias[n] : 0.f) : at < 2 * BN + BM ? p.as[m] : 0.f;
+    }
+  };
+  const auto put_scales = [&](int turn) {
+#pragma unroll
+    for (int i = 0; i * kLanes < 2 * BN + BM; ++i)
+      if (i * kLanes + static_cast<int>(threadIdx.x) < 2 * BN + BM) scale[turn][i * kLanes + threadIdx.x] = sc[i];
+  };
+  get_scales(blockIdx.x);
+  put_scales(0);
+  all_here<0>();
+  if (depths > 0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch_a(lds, i);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) fetch_b(lds, 0, i);
   }
 
-  // Outputs: 32 rows of a wave's part at a time through LDS of its own, so that a row's
-  // outputs leave in 16-byte words.
-  all_here<0>();
-  constexpr int kPer = 16 / sizeof(Tout), kChunks = kCols / kPer;
-  Tout* room = reinterpret_cast<Tout*>(lds + wave * kRoom);
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t mi = m0 + wm * kRows + i * 32;
-    const float as = p.as[mi + r < p.m ? mi + r : p.m - 1];
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int c = j * 32 + g * 8 + h * 4;
-        const f32x4 bs = *reinterpret_cast<const f32x4*>(&cols[0][wn * kCols + c]);
-        const f32x4 bias = *reinterpret_cast<const f32x4*>(&cols[1][wn * kCols + c]);
-        f32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(static_cast<float>(acc[i][j][4 * g + e]), as * bs[e], bias[e]);
-        stage(room + r * kPitch + c, v);
+  // Stores of a whole tile's outputs that may be under way at its next barrier: what that waits
+  // for was begun before them.
+  constexpr int kStores = MI / 2 * (kCols / kSpan) * 2;
+  bool storing = false;
+  int stage = 0, turn = 0;
+  for (int v = blockIdx.x; v < tiles; v += gridDim.x) {
+    int64_t m0, n0;
+    place(v, m0, n0);
+    const int then = turn == 2 ? 0 : turn + 1;
+    const bool another = v + static_cast<int>(gridDim.x) < tiles;
+    // Blocks are read ahead across depths and tiles too: the barrier comes before the last kAhead
+    // slots of a depth, when all of its blocks are in registers.  (The workgroup's last depth
+    // reads what is not there, and does not use it.)
+    for (int t = 0; t < depths; ++t, stage ^= 1) {
+      int8_t* now = lds + stage * kStage;
+      int8_t* next = lds + (stage ^ 1) * kStage;
+      const bool scales = t == depths - 1 && another;
+      if (scales) get_scales(v + gridDim.x);
+      const bool held = !DIRECT && lv < tiles;
+      if (held) {
+        hold();
+        advance();
       }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int q = 0; q < 32 * kChunks / 64; ++q) {
-      const int at = q * 64 + lane, row = at / kChunks, c = at % kChunks * kPer;
-      const int64_t m = mi + row;
-      const int n = static_cast<int>(n0) + wn * kCols + c;
-      typedef Tout word __attribute__((ext_vector_type(kPer)));
-      typedef word word_any __attribute__((aligned(sizeof(Tout))));
-      const word v = *reinterpret_cast<const word*>(room + row * kPitch + c);
-      if (m >= p.m) continue;
-      Tout* to = static_cast<Tout*>(p.out) + m * p.so + n;
-      if (n + kPer <= p.n) {
-        *reinterpret_cast<word_any*>(to) = v;
-      } else {
+      for (int i = 0; i < S - kAhead; ++i) slot(now, next, i, nothing);
+      if (held) put(next);
+      if (scales) put_scales(then);
+      if (DIRECT && t == 0 && storing) all_here<kStores>();
+      else all_here<0>();
+      const bool more = DIRECT && lv < tiles;
+      const uint32_t ta = A::place(now), tb = B::place(now + kA);
+      const int k = k_of(), left = left_of();
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (n + e < p.n) to[e] = v[e];
-      }
+      for (int i = S - kAhead; i < S; ++i)
+        slot(now, next, i, [&](int l) {
+          if (more) begin(ta, tb, k, left, l);
+        });
+      if (more) advance();
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+
+    if (depths == 0 && another) {
+      get_scales(v + gridDim.x);
+      put_scales(then);
+      all_here<0>();
+    }
+
+    // Outputs: 32 rows of 64 bytes at a time through LDS of the wave's own, so that they leave in
+    // 16-byte words, four to a row.
+    const float* bs = scale[turn] + wn * kCols;
+    Tout* mine = room[wave];
+    const auto outputs = [&](auto whole) {
+#pragma unroll
+      for (int i = 0; i < MI / 2; ++i) {
+        const int64_t mi = m0 + wm * kRows + i * 32;
+        float as[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) as[u] = scale[turn][2 * BN + wm * kRows + i * 32 + u * 16 + r];
+#pragma unroll
+        for (int j = 0; j < kCols / kSpan; ++j) {
+#pragma unroll
+          for (int g = 0; g < kSpan / 16; ++g) {
+            const int c = j * kSpan + g * 16 + h * 4;
+            const f32x4 vb = *reinterpret_cast<const f32x4*>(bs + c), bias = *reinterpret_cast<const f32x4*>(bs + BN + c);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              f32x4 out;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                out[e] = fmaf(static_cast<float>(acc[2 * i + u][j * kSpan / 16 + g][e]), as[u] * vb[e], bias[e]);
+              stage_out(mine + (u * 16 + r) * kPitch + g * 16 + h * 4, out);
+            }
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int row = q * 16 + lane / 4, c = lane % 4 * kPer;
+            const int64_t m = mi + row;
+            const int n = static_cast<int>(n0) + wn * kCols + j * kSpan + c;
+            typedef Tout word __attribute__((ext_vector_type(kPer)));
+            typedef word word_any __attribute__((aligned(sizeof(Tout))));
+            const word w = *reinterpret_cast<const word*>(mine + row * kPitch + c);
+            Tout* to = static_cast<Tout*>(p.out) + m * p.so + n;
+            if (decltype(whole)::value || (m < p.m && n + kPer <= p.n)) {
+              *reinterpret_cast<word_any*>(to) = w;
+            } else if (m < p.m) {
+#pragma unroll
+              for (int e = 0; e < kPer; ++e)
+                if (n + e < p.n) to[e] = w[e];
+            }
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+      }
+    };
+    storing = m0 + BM <= p.m && n0 + BN <= p.n && depths > 1;
+    if (m0 + BM <= p.m && n0 + BN <= p.n) outputs(std::true_type{});
+    else outputs(std::false_type{});
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = i32x4{};
+    turn = then;
   }
 }
 
@@ -290,7 +375,8 @@ bool direct(const MatmulParams& p) {
 template <typename Tout, int BM, int BN, int WM, int WN, int DEPTH, int GROUPS, bool DIRECT>
 hipError_t tiles(const MatmulParams& p, hipStream_t s) {
   const int ntm = (p.m - 1) / BM + 1, ntn = (p.n - 1) / BN + 1;
-  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, DEPTH, GROUPS, DIRECT>), dim3(static_cast<unsigned>(ntm) * ntn),
+  const int64_t n = static_cast<int64_t>(ntm) * ntn, most = kUnits * GROUPS;
+  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, DEPTH, GROUPS, DIRECT>), dim3(static_cast<unsigned>(n < most ? n : most)),
                      dim3(64 * WM * WN), 0, s, p, ntm, ntn);
   return hipGetLastError();
 }
@@ -304,13 +390,10 @@ hipError_t product(const MatmulParams& p, hipStream_t s) {
   const int v = e ? atoi(e) : 0;
   if (v == 1) return tiles<Tout, 256, 256, 2, 2, 128, 1, true>(p, s);
   if (v == 2) return tiles<Tout, 256, 256, 2, 4, 128, 1, true>(p, s);
-  if (v == 3) return tiles<Tout, 256, 128, 2, 2, 64, 2, true>(p, s);
+  if (v == 3) return tiles<Tout, 256, 256, 4, 2, 128, 1, true>(p, s);
   if (v == 4) return tiles<Tout, 128, 128, 2, 2, 128, 2, true>(p, s);
-  if (v == 5) return tiles<Tout, 128, 128, 2, 2, 64, 3, true>(p, s);
-  if (v == 6) return tiles<Tout, 128, 256, 2, 2, 64, 2, true>(p, s);
   if (v == 7) return tiles<Tout, 256, 128, 4, 2, 128, 1, true>(p, s);
-  if (v == 8) return tiles<Tout, 64, 64, 2, 2, 128, 2, true>(p, s);
-  if (v == 9) return tiles<Tout, 128, 64, 2, 2, 128, 2, true>(p, s);
+  if (v == 8) return tiles<Tout, 256, 128, 2, 2, 128, 1, true>(p, s);
   if (big >= 256) return tiles<Tout, 256, 256, 2, 2, 128, 1, true>(p, s);
   return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 128, 2, true>(p, s) : tiles<Tout, 64, 64, 2, 2, 128, 2, true>(p, s);
 }
