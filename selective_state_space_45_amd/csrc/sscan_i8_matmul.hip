@@ -30,20 +30,23 @@ __device__ __forceinline__ void all_here() {
   asm volatile("" ::: "memory");
 }
 
-// 16 bytes for each lane straight to LDS, in the lanes' order from the wave's address `to`, from
-// an address of its own or from a common one and an offset.  In assembly, since the compiler
-// takes any reading of LDS to wait for all such loads; all_here() waits for them.
+// A load straight to LDS, in the lanes' order from the wave's address `to`: 16 bytes for each
+// lane at an offset from a common address.  In assembly, since the compiler takes any reading
+// of LDS to wait for all such loads; all_here() waits for them.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved, and is what such a load goes by
-__device__ __forceinline__ void bring(uint32_t to, uintptr_t from) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "m0");
-}
 __device__ __forceinline__ void bring(uint32_t to, uintptr_t base, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(at), "s"(base) : "m0");
 }
 #pragma clang diagnostic pop
 
-__device__ __attribute__((aligned(16))) const int8_t g_zeros[kChunk16] = {};
+// Where a load to LDS goes that begins at p for the workgroup's first wave, BYTES of a wave after
+// another.
+template <int BYTES>
+__device__ __forceinline__ uint32_t place_of(int8_t* p) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)p) + (threadIdx.x >> 6) * BYTES));
+}
 
 // One side's rows of a tile on their way to LDS, DEPTH bytes of k at a time.  A chunk of row r
 // goes to a slot of the row's DEPTH bytes that differs from row to row (slot_of), so that 16
@@ -78,18 +81,19 @@ struct Side {
   // rows past the end repeat the last one: their sums are not written
   __device__ __forceinline__ int row(int i) const { return row0 + kStep * i < last ? row0 + kStep * i : last; }
 
-  // Where in LDS the wave's first load of the rows goes.
-  static __device__ __forceinline__ uint32_t place(int8_t* lds) {
-    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
-        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)lds) + (threadIdx.x >> 6) * 64 * kChunk16));
-  }
-  // DIRECT: load i of bytes k .. k + DEPTH, of which `left` are there; zeros for the others.
+  // DIRECT: load i of bytes k .. k + DEPTH of the rows.  Where only `left` are there (all of
+  // which are whole chunks), the chunks past them bring the row's first one of these instead.
   __device__ __forceinline__ void one(uint32_t to, int k, int left, int i) const {
-    const uintptr_t from = reinterpret_cast<uintptr_t>(base + k);
-    if (left == DEPTH) bring(to + i * kStep * DEPTH, from, at[i]);
-    else bring(to + i * kStep * DEPTH, chunk * kChunk16 < left ? from + at[i] : reinterpret_cast<uintptr_t>(g_zeros));
+    const uint32_t back = chunk * kChunk16 < left ? 0 : chunk * kChunk16;
+    bring(to + i * kStep * DEPTH, reinterpret_cast<uintptr_t>(base + k), at[i] - back);
   }
-  // The same by way of registers, from any address.
+  // Zeros in their place.
+  __device__ __forceinline__ void clear(int8_t* lds, int left) const {
+    if (chunk * kChunk16 < left) return;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) *reinterpret_cast<i32x4*>(lds + i * kStep * DEPTH + threadIdx.x * kChunk16) = i32x4{};
+  }
+  // The bytes by way of registers, from any address, zeros past `left`.
   __device__ __forceinline__ void hold(int k, int left) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -112,6 +116,7 @@ struct Side {
 };
 
 // Four neighbouring outputs of a row in Tout.
+__device__ __forceinline__ void stage_out(int32_t* p, f32x4 v) { *reinterpret_cast<i32x4*>(p) = __builtin_bit_cast(i32x4, v); }
 __device__ __forceinline__ void stage_out(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void stage_out(bf16_t* p, f32x4 v) {
   typedef __bf16 b4 __attribute__((ext_vector_type(4)));
@@ -129,11 +134,19 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   typedef Side<BM, kWaves, DEPTH, DIRECT> A;
   typedef Side<BN, kWaves, DEPTH, DIRECT> B;
   constexpr int kLoads = A::kLoads + B::kLoads, kA = BM * DEPTH, kStage = (BM + BN) * DEPTH;
+  constexpr bool kPart = std::is_same<Tout, int32_t>::value;       // sums of a part of k, as they are
   constexpr int kPer = 16 / sizeof(Tout), kSpan = 4 * kPer, kPitch = kSpan + kPer;   // outputs of a row that leave at a time
   __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage];
   __shared__ __attribute__((aligned(16))) float scale[3][2 * BN + BM];   // of three tiles: b's scales, biases, a's
   __shared__ __attribute__((aligned(16))) Tout room[kWaves][32 * kPitch];
   const int tiles = ntm * ntn;
+  if (gridDim.y > 1) {      // this row of the grid sums its part of k, in whole depths
+    const int each = ((p.k + DEPTH - 1) / DEPTH + gridDim.y - 1) / gridDim.y * DEPTH, from = blockIdx.y * each;
+    p.a += from;
+    p.b += from;
+    p.k = p.k - from < each ? p.k - from : each;
+    p.out = static_cast<Tout*>(p.out) + static_cast<int64_t>(blockIdx.y) * p.m * p.n;
+  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   // Where the workgroup's tile of turn v begins.  Tiles go down 4 rows of tiles, then along n:
@@ -206,17 +219,22 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     sa.put(to);
     sb.put(to + kA);
   };
+  // (Past the workgroup's last depth its loads repeat that one, and nothing reads them.)
   const auto advance = [&]() {
     if (++lt < depths) return;
+    if (lv + static_cast<int>(gridDim.x) >= tiles) {
+      lt = depths - 1;
+      return;
+    }
     lt = 0;
     lv += gridDim.x;
-    if (lv < tiles) aim();
+    aim();
   };
   if (depths > 0) {
     aim();
     if (DIRECT) {
-      for (int d = 0; d < 2 && lv < tiles; ++d) {
-        const uint32_t ta = A::place(lds + d * kStage), tb = B::place(lds + d * kStage + kA);
+      for (int d = 0; d < 2; ++d) {
+        const uint32_t ta = place_of<1024>(lds + d * kStage), tb = place_of<1024>(lds + d * kStage + kA);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) begin(ta, tb, k_of(), left_of(), i);
         advance();
@@ -248,6 +266,11 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   get_scales(blockIdx.x);
   put_scales(0);
   all_here<0>();
+  if (DIRECT && rest < DEPTH && depths > 0) {
+    sa.clear(lds, rest);
+    if (depths == 1) sa.clear(lds + kStage, rest);
+    all_here<0>();
+  }
   if (depths > 0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch_a(lds, i);
@@ -273,7 +296,7 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
       int8_t* next = lds + (stage ^ 1) * kStage;
       const bool scales = t == depths - 1 && another;
       if (scales) get_scales(v + gridDim.x);
-      const bool held = !DIRECT && lv < tiles;
+      const bool held = !DIRECT && (t + 1 < depths || another);
       if (held) {
         hold();
         advance();
@@ -282,17 +305,24 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
       for (int i = 0; i < S - kAhead; ++i) slot(now, next, i, nothing);
       if (held) put(next);
       if (scales) put_scales(then);
-      if (DIRECT && t == 0 && storing) all_here<kStores>();
-      else all_here<0>();
-      const bool more = DIRECT && lv < tiles;
-      const uint32_t ta = A::place(now), tb = B::place(now + kA);
+      if (!DIRECT) {
+        all_here<0>();
+      } else {      // all but the stores
+        if (t == 0 && storing) all_here<kStores>();
+        else all_here<0>();
+        if (rest < DEPTH && t == depths - 1) {
+          sa.clear(next, rest);
+          all_here<0>();
+        }
+      }
+      const uint32_t ta = place_of<1024>(now), tb = place_of<1024>(now + kA);
       const int k = k_of(), left = left_of();
 #pragma unroll
       for (int i = S - kAhead; i < S; ++i)
         slot(now, next, i, [&](int l) {
-          if (more) begin(ta, tb, k, left, l);
+          if (DIRECT) begin(ta, tb, k, left, l);
         });
-      if (more) advance();
+      if (DIRECT) advance();
     }
 
     if (depths == 0 && another) {
@@ -322,8 +352,10 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
             for (int u = 0; u < 2; ++u) {
               f32x4 out;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                out[e] = fmaf(static_cast<float>(acc[2 * i + u][j * kSpan / 16 + g][e]), as[u] * vb[e], bias[e]);
+              for (int e = 0; e < 4; ++e) {
+                const int32_t sum = acc[2 * i + u][j * kSpan / 16 + g][e];
+                out[e] = kPart ? __int_as_float(sum) : fmaf(static_cast<float>(sum), as[u] * vb[e], bias[e]);
+              }
               stage_out(mine + (u * 16 + r) * kPitch + g * 16 + h * 4, out);
             }
           }
@@ -358,9 +390,85 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
       for (int j = 0; j < NI; ++j) acc[i][j] = i32x4{};
     turn = then;
   }
+  if (DIRECT) all_here<0>();   // no load to LDS outlives the workgroup
 }
 
-size_t i8_matmul_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+// Outputs from the sums of the parts of k.
+template <typename Tout>
+__global__ __launch_bounds__(256) void i8_join_kernel(MatmulParams p, int parts, int64_t words) {
+  const int64_t id = static_cast<int64_t>(workgroup<256>()) * 256 + threadIdx.x;
+  if (id >= words) return;
+  const int nw = (p.n + 3) / 4;
+  const int64_t m = id / nw;
+  const int n = static_cast<int>(id - m * nw) * 4, have = p.n - n < 4 ? p.n - n : 4;
+  const int64_t all = static_cast<int64_t>(p.m) * p.n;
+  const int32_t* from = p.partial + m * p.n + n;
+  i32x4 sum = {};
+  for (int s = 0; s < parts; ++s, from += all) {
+    if (have == 4) {
+      sum += *reinterpret_cast<const i32x4_any*>(from);
+    } else {
+      for (int e = 0; e < have; ++e) sum[e] += from[e];
+    }
+  }
+  const float as = p.as[m];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < have)
+      store_val(static_cast<Tout*>(p.out) + m * p.so + n + e,
+                fmaf(static_cast<float>(sum[e]), as * p.bs[n + e], p.bias ? p.bias[n + e] : 0.f));
+}
+
+// Few rows of a (at most 16 MI): b is read once, from memory into registers, and the launch and one
+// latency of memory are most of the time.  A workgroup has 16 rows of b; its waves split k, in
+// steps of 64 bytes, and their sums are joined in LDS.  Any alignment: a lane's 16 bytes of a
+// row are loaded as they lie, the last ones of k byte by byte.
+constexpr int kFewWaves = 8;
+template <typename Tout, int MI>
+__global__ __launch_bounds__(64 * kFewWaves) void i8_few_kernel(MatmulParams p) {
+  __shared__ i32x4 sums[kFewWaves][MI][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, h = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(workgroup<64 * kFewWaves>()) * 16;
+  if (n0 >= p.n) return;
+  const int8_t* b = p.b + (n0 + r < p.n ? n0 + r : p.n - 1) * p.sb;
+  const int8_t* a[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) a[i] = p.a + static_cast<int64_t>(i * 16 + r < p.m ? i * 16 + r : p.m - 1) * p.sa;
+  const auto get = [&](const int8_t* row, int k) {
+    if (k + kChunk16 <= p.k) return i32x4(*reinterpret_cast<const i32x4_any*>(row + k));
+    uint32_t w[4] = {};
+    for (int j = 0; k + j < p.k; ++j) w[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + j])) << 8 * (j % 4);
+    return i32x4{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
+  };
+  const int steps = (p.k + 63) / 64, each = (steps + kFewWaves - 1) / kFewWaves;
+  const int begin = wave * each, end = begin + each < steps ? begin + each : steps;
+  i32x4 acc[MI] = {};
+#pragma unroll 4
+  for (int s = begin; s < end; ++s) {
+    const int k = s * 64 + h * kChunk16;
+    const i32x4 fb = get(b, k);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb, get(a[i], k), acc[i], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i) sums[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int i = wave; i < MI; i += kFewWaves) {
+    i32x4 sum = sums[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) sum += sums[w][i][lane];
+    const int m = i * 16 + r;
+    if (m >= p.m) continue;
+    const float as = p.as[m];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t n = n0 + h * 4 + e;
+      if (n < p.n)
+        store_val(static_cast<Tout*>(p.out) + m * p.so + n,
+                  fmaf(static_cast<float>(sum[e]), as * p.bs[n], p.bias ? p.bias[n] : 0.f));
+    }
+  }
+}
 
 namespace {
 
@@ -372,33 +480,74 @@ bool direct(const MatmulParams& p) {
   return p.k % 16 == 0 && fine(p.a, p.sa, p.m) && fine(p.b, p.sb, p.n);
 }
 
-template <typename Tout, int BM, int BN, int WM, int WN, int DEPTH, int GROUPS, bool DIRECT>
-hipError_t tiles(const MatmulParams& p, hipStream_t s) {
+template <typename Tout, int BM, int BN, int WM, int WN, int GROUPS, bool DIRECT>
+void tiles(const MatmulParams& p, int parts, hipStream_t s) {
   const int ntm = (p.m - 1) / BM + 1, ntn = (p.n - 1) / BN + 1;
   const int64_t n = static_cast<int64_t>(ntm) * ntn, most = kUnits * GROUPS;
-  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, DEPTH, GROUPS, DIRECT>), dim3(static_cast<unsigned>(n < most ? n : most)),
+  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, 128, GROUPS, DIRECT>), dim3(static_cast<unsigned>(n < most ? n : most), parts),
                      dim3(64 * WM * WN), 0, s, p, ntm, ntn);
-  return hipGetLastError();
+}
+
+template <typename Tout>
+void by_tiles(const MatmulParams& p, int parts, hipStream_t s) {
+  const int64_t big = static_cast<int64_t>((p.m - 1) / 256 + 1) * ((p.n - 1) / 256 + 1);
+  const int64_t mid = static_cast<int64_t>((p.m - 1) / 128 + 1) * ((p.n - 1) / 128 + 1);
+  if (!direct(p)) return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 2, false>(p, parts, s) : tiles<Tout, 64, 64, 2, 2, 2, false>(p, parts, s);
+  const char* e = getenv("MM_V");
+  const int v = e ? atoi(e) : 0;
+  if (v == 2) return tiles<Tout, 256, 256, 2, 4, 1, true>(p, parts, s);
+  if (v == 4) return tiles<Tout, 128, 128, 2, 2, 2, true>(p, parts, s);
+  if (v == 6) return tiles<Tout, 64, 64, 2, 2, 3, true>(p, parts, s);
+  if (v == 7) return tiles<Tout, 256, 128, 4, 2, 1, true>(p, parts, s);
+  if (v == 8) return tiles<Tout, 128, 64, 2, 2, 2, true>(p, parts, s);
+  if (big >= 256) return tiles<Tout, 256, 256, 2, 4, 1, true>(p, parts, s);
+  return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 2, true>(p, parts, s) : tiles<Tout, 64, 64, 2, 2, 3, true>(p, parts, s);
+}
+
+template <typename Tout>
+void few(const MatmulParams& p, hipStream_t s) {
+  const dim3 grid = grid_of<64 * kFewWaves>((static_cast<int64_t>(p.n) + 15) / 16), block(64 * kFewWaves);
+  if (p.m <= 16) hipLaunchKernelGGL((i8_few_kernel<Tout, 1>), grid, block, 0, s, p);
+  else if (p.m <= 32) hipLaunchKernelGGL((i8_few_kernel<Tout, 2>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((i8_few_kernel<Tout, 4>), grid, block, 0, s, p);
+}
+
+int parts_of(int64_t m, int64_t n, int64_t k) {
+  const char* e = getenv("MM_S");
+  if (m <= 64 && !getenv("MM_V")) return 1;
+  int parts = e ? atoi(e) : 1;
+  const int depths = static_cast<int>((k + 127) / 128);
+  if (parts > depths) parts = depths > 0 ? depths : 1;
+  const int each = (depths + parts - 1) / parts;
+  return each > 0 ? (depths + each - 1) / each : 1;       // none of them empty
 }
 
 template <typename Tout>
 hipError_t product(const MatmulParams& p, hipStream_t s) {
-  const int64_t big = static_cast<int64_t>((p.m - 1) / 256 + 1) * ((p.n - 1) / 256 + 1);
-  const int64_t mid = static_cast<int64_t>((p.m - 1) / 128 + 1) * ((p.n - 1) / 128 + 1);
-  if (!direct(p)) return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 128, 2, false>(p, s) : tiles<Tout, 64, 64, 2, 2, 128, 2, false>(p, s);
-  const char* e = getenv("MM_V");
-  const int v = e ? atoi(e) : 0;
-  if (v == 1) return tiles<Tout, 256, 256, 2, 2, 128, 1, true>(p, s);
-  if (v == 2) return tiles<Tout, 256, 256, 2, 4, 128, 1, true>(p, s);
-  if (v == 3) return tiles<Tout, 256, 256, 4, 2, 128, 1, true>(p, s);
-  if (v == 4) return tiles<Tout, 128, 128, 2, 2, 128, 2, true>(p, s);
-  if (v == 7) return tiles<Tout, 256, 128, 4, 2, 128, 1, true>(p, s);
-  if (v == 8) return tiles<Tout, 256, 128, 2, 2, 128, 1, true>(p, s);
-  if (big >= 256) return tiles<Tout, 256, 256, 2, 2, 128, 1, true>(p, s);
-  return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 128, 2, true>(p, s) : tiles<Tout, 64, 64, 2, 2, 128, 2, true>(p, s);
+  if (p.m <= 64 && !getenv("MM_V")) {
+    few<Tout>(p, s);
+    return hipGetLastError();
+  }
+  const int parts = p.partial ? parts_of(p.m, p.n, p.k) : 1;
+  if (parts == 1) {
+    by_tiles<Tout>(p, 1, s);
+    return hipGetLastError();
+  }
+  MatmulParams q = p;
+  q.out = p.partial;
+  q.so = p.n;
+  by_tiles<int32_t>(q, parts, s);
+  const int64_t words = static_cast<int64_t>(p.m) * ((p.n + 3) / 4);
+  hipLaunchKernelGGL((i8_join_kernel<Tout>), grid_of<256>((words + 255) / 256), dim3(256), 0, s, p, parts, words);
+  return hipGetLastError();
 }
 
 }  // namespace
+
+size_t i8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  const int parts = parts_of(m, n, k);
+  return parts > 1 ? static_cast<size_t>(parts) * m * n * 4 : 0;
+}
 
 hipError_t launch_i8_matmul(const MatmulParams& p, size_t, bool bf16, hipStream_t s) {
   return bf16 ? product<bf16_t>(p, s) : product<float>(p, s);
