@@ -30,13 +30,16 @@ __device__ __forceinline__ void all_here() {
   asm volatile("" ::: "memory");
 }
 
-// A load straight to LDS, in the lanes' order from the wave's address `to`: 16 bytes for each
-// lane at an offset from a common address.  In assembly, since the compiler takes any reading
-// of LDS to wait for all such loads; all_here() waits for them.
+// Loads straight to LDS, in the lanes' order from the wave's address `to`: 16 bytes for each lane
+// at an offset from a common address, or 4 at an address of its own.  In assembly, since the
+// compiler takes any reading of LDS to wait for all such loads; all_here() waits for them.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved, and is what such a load goes by
 __device__ __forceinline__ void bring(uint32_t to, uintptr_t base, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(at), "s"(base) : "m0");
+}
+__device__ __forceinline__ void bring_word(uint32_t to, const void* from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "m0");
 }
 #pragma clang diagnostic pop
 
@@ -48,20 +51,20 @@ __device__ __forceinline__ uint32_t place_of(int8_t* p) {
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)p) + (threadIdx.x >> 6) * BYTES));
 }
 
-// One side's rows of a tile on their way to LDS, DEPTH bytes of k at a time.  A chunk of row r
-// goes to a slot of the row's DEPTH bytes that differs from row to row (slot_of), so that 16
-// lanes that read one chunk of 16 rows take all 64 banks once.  The lanes of a wave bring
-// slot after slot of row after row: LDS is then filled in the lanes' order, which is what a
-// load straight to LDS does.
-template <int DEPTH>
-__device__ __forceinline__ int slot_of(int row, int chunk) {
-  return DEPTH == 128 ? (chunk ^ (row >> 1)) & 7 : (chunk ^ (row >> 2)) & 3;
-}
-template <int ROWS, int WAVES, int DEPTH, bool DIRECT>
+// LDS holds kStages depths of k, kDepth bytes of each row: one is multiplied, the next is there,
+// the others are on their way.  (Two depths of 128 bytes, the next begun as one ends: 8192^3
+// 435 us; a load takes about 1.2 us from its begin, a depth of 128 bytes is multiplied in 0.9.)
+constexpr int kDepth = 64, kStages = 4;
+
+// One side's rows of a tile on their way to LDS.  Chunk c of row r goes to slot (c ^ r / 4) & 3
+// of the row's four, so that 16 lanes that read one chunk of 16 rows take all 64 banks once.
+// The lanes of a wave bring slot after slot of row after row: LDS is then filled in the lanes'
+// order, which is what a load straight to LDS does.
+__device__ __forceinline__ int slot_of(int row, int chunk) { return (chunk ^ (row >> 2)) & 3; }
+template <int ROWS, int WAVES, bool DIRECT>
 struct Side {
-  static constexpr int kChunks = DEPTH / kChunk16, kStep = 64 / kChunks * WAVES;   // rows of one load of all waves
-  static constexpr int kLoads = ROWS / kStep;
-  static_assert(ROWS % kStep == 0 && kStep % 16 == 0, "the lane's chunk is the same in all its rows");
+  static constexpr int kStep = 16 * WAVES, kLoads = ROWS / kStep;   // rows of one load of all waves
+  static_assert(ROWS % kStep == 0, "the lane's chunk is the same in all its rows");
   const int8_t* base;
   uint32_t at[kLoads];       // DIRECT: bytes from base to the lane's rows
   int64_t stride;
@@ -72,32 +75,24 @@ struct Side {
   __device__ __forceinline__ void aim(const int8_t* p, int64_t st, int64_t r0, int rows) {
     stride = st;
     base = p + r0 * st;
-    row0 = threadIdx.x / kChunks;
+    row0 = threadIdx.x / 4;
     last = static_cast<int>(rows - r0 < ROWS ? rows - r0 : ROWS) - 1;
-    chunk = slot_of<DEPTH>(row0, threadIdx.x % kChunks);
+    chunk = slot_of(row0, threadIdx.x % 4);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) at[i] = static_cast<uint32_t>(row(i) * st + chunk * kChunk16);
   }
   // rows past the end repeat the last one: their sums are not written
   __device__ __forceinline__ int row(int i) const { return row0 + kStep * i < last ? row0 + kStep * i : last; }
 
-  // DIRECT: load i of bytes k .. k + DEPTH of the rows.  Where only `left` are there (all of
-  // which are whole chunks), the chunks past them bring the row's first one of these instead.
-  __device__ __forceinline__ void one(uint32_t to, int k, int left, int i) const {
-    const uint32_t back = chunk * kChunk16 < left ? 0 : chunk * kChunk16;
-    bring(to + i * kStep * DEPTH, reinterpret_cast<uintptr_t>(base + k), at[i] - back);
+  // DIRECT: load i of the next kDepth bytes of the rows, all there.
+  __device__ __forceinline__ void one(uint32_t to, int i) const {
+    bring(to + i * kStep * kDepth, reinterpret_cast<uintptr_t>(base), at[i]);
   }
-  // Zeros in their place.
-  __device__ __forceinline__ void clear(int8_t* lds, int left) const {
-    if (chunk * kChunk16 < left) return;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) *reinterpret_cast<i32x4*>(lds + i * kStep * DEPTH + threadIdx.x * kChunk16) = i32x4{};
-  }
-  // The bytes by way of registers, from any address, zeros past `left`.
-  __device__ __forceinline__ void hold(int k, int left) {
+  // The same by way of registers, from any address, zeros past the `left` bytes that are there.
+  __device__ __forceinline__ void hold(int left) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int8_t* from = base + row(i) * stride + k + chunk * kChunk16;
+      const int8_t* from = base + row(i) * stride + chunk * kChunk16;
       const int n = left - chunk * kChunk16;
       if (n >= kChunk16) {
         held[i] = *reinterpret_cast<const i32x4_any*>(from);
@@ -111,7 +106,7 @@ struct Side {
   __device__ __forceinline__ void put(int8_t* lds) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<i32x4*>(lds + i * kStep * DEPTH + threadIdx.x * kChunk16) = held[i];
+      *reinterpret_cast<i32x4*>(lds + i * kStep * kDepth + threadIdx.x * kChunk16) = held[i];
   }
 };
 
@@ -125,23 +120,26 @@ __device__ __forceinline__ void stage_out(bf16_t* p, f32x4 v) {
 }
 
 // Workgroups take tiles of BM x BN sums one after another; their WM x WN waves have a part of
-// MI x NI blocks of 16 x 16 each.  LDS holds two depths of k: while one is multiplied the next
-// is on its way, and the next tile's first ones while a tile's outputs leave.  The
-// instruction's rows are n and its columns m, so that a lane ends with neighbouring outputs.
-template <typename Tout, int BM, int BN, int WM, int WN, int DEPTH, int GROUPS, bool DIRECT>
+// MI x NI blocks of 16 x 16 each.  The loads go on from tile to tile, also while a tile's outputs
+// leave.  The instruction's rows are n and its columns m, so that a lane ends with neighbouring
+// outputs.  GROUPS workgroups share a compute unit.
+template <typename Tout, int BM, int BN, int WM, int WN, int GROUPS, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_kernel(MatmulParams p, int ntm, int ntn) {
   constexpr int kWaves = WM * WN, kLanes = 64 * kWaves, kRows = BM / WM, kCols = BN / WN, MI = kRows / 16, NI = kCols / 16;
-  typedef Side<BM, kWaves, DEPTH, DIRECT> A;
-  typedef Side<BN, kWaves, DEPTH, DIRECT> B;
-  constexpr int kLoads = A::kLoads + B::kLoads, kA = BM * DEPTH, kStage = (BM + BN) * DEPTH;
+  typedef Side<BM, kWaves, DIRECT> A;
+  typedef Side<BN, kWaves, DIRECT> B;
+  constexpr int kLoads = A::kLoads + B::kLoads, kA = BM * kDepth, kStage = (BM + BN) * kDepth;
+  static_assert((kStage & (kStage - 1)) == 0, "stages follow one another by a mask");
   constexpr bool kPart = std::is_same<Tout, int32_t>::value;       // sums of a part of k, as they are
   constexpr int kPer = 16 / sizeof(Tout), kSpan = 4 * kPer, kPitch = kSpan + kPer;   // outputs of a row that leave at a time
-  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage];
-  __shared__ __attribute__((aligned(16))) float scale[3][2 * BN + BM];   // of three tiles: b's scales, biases, a's
+  // of three tiles: b's scales, biases, a's scales, filled up to whole loads of all waves
+  constexpr int kScaleLoads = (2 * BN + BM + kLanes - 1) / kLanes, kScales = kScaleLoads * kLanes;
+  __shared__ __attribute__((aligned(16))) int8_t lds[kStages * kStage];
+  __shared__ __attribute__((aligned(16))) float scale[3][kScales];
   __shared__ __attribute__((aligned(16))) Tout room[kWaves][32 * kPitch];
   const int tiles = ntm * ntn;
-  if (gridDim.y > 1) {      // this row of the grid sums its part of k, in whole depths
-    const int each = ((p.k + DEPTH - 1) / DEPTH + gridDim.y - 1) / gridDim.y * DEPTH, from = blockIdx.y * each;
+  if (gridDim.y > 1) {      // this row of the grid sums its part of k
+    const int each = ((p.k + 127) / 128 + gridDim.y - 1) / gridDim.y * 128, from = blockIdx.y * each;
     p.a += from;
     p.b += from;
     p.k = p.k - from < each ? p.k - from : each;
@@ -159,43 +157,42 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     n0 = static_cast<int64_t>(in / high) * BN;
   };
 
-  // A depth is S slots, each a block of a's rows times all of b's: the order within a slot, and
+  // A depth is MI slots, each a block of a's rows times all of b's: the order within a slot, and
   // of slots, is fixed (left to itself the compiler reads blocks when they are needed, and the
   // matrix unit waits for them).  A slot reads a's block for kAhead slots later, the last kAhead
-  // slots of a step also b's blocks of the next step.
-  constexpr int KS = DEPTH / 64, S = KS * MI, kAhead = MI > 3 ? 3 : MI - 1, kRing = kAhead + 1;
-  static_assert(S % kRing == 0 && KS % 2 == 0 && MI % 2 == 0, "places of blocks are constants");
+  // slots of a depth also b's blocks of the next.
+  constexpr int kAhead = MI > 3 ? 3 : MI - 1, kRing = kAhead + 1;
+  static_assert(MI % kRing == 0 && MI % 2 == 0, "places of blocks are constants");
   i32x4 acc[MI][NI] = {}, fa[kRing], fb[2][NI];
-  // a block's chunk 4 ks + l / 16 of row l % 16
-  const int r = lane & 15, h = lane >> 4;
-  const auto fetch_a = [&](const int8_t* from, int s) {
-    fa[s % kRing] = *reinterpret_cast<const i32x4*>(from + (wm * kRows + s % MI * 16 + r) * DEPTH + slot_of<DEPTH>(r, s / MI * 4 + h) * kChunk16);
+  // a block's chunk l / 16 of row l % 16
+  const int r = lane & 15, h = lane >> 4, mine_at = r * kDepth + slot_of(r, h) * kChunk16;
+  const auto fetch_a = [&](const int8_t* from, int i) {
+    fa[i % kRing] = *reinterpret_cast<const i32x4*>(from + (wm * kRows + i * 16) * kDepth + mine_at);
   };
-  const auto fetch_b = [&](const int8_t* from, int ks, int i) {
-    fb[ks & 1][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * kCols + i * 16 + r) * DEPTH + slot_of<DEPTH>(r, ks * 4 + h) * kChunk16);
+  const auto fetch_b = [&](const int8_t* from, int half, int i) {
+    fb[half][i] = *reinterpret_cast<const i32x4*>(from + kA + (wn * kCols + i * 16) * kDepth + mine_at);
   };
-  const auto slot = [&](const int8_t* now, const int8_t* next, int s, auto&& begin) {
-    const int ks = s / MI, late = s % MI - (MI - kAhead);   // 0 .. kAhead - 1 in the last slots of a step
-    if (s + kAhead < S) fetch_a(now, s + kAhead);
-    else fetch_a(next, s + kAhead - S);
+  const auto slot = [&](const int8_t* now, const int8_t* next, int half, int i, auto&& begin) {
+    const int late = i - (MI - kAhead);             // 0 .. kAhead - 1 in the last slots
+    if (late < 0) fetch_a(now, i + kAhead);
+    else fetch_a(next, i + kAhead - MI);
     if (late >= 0) {
 #pragma unroll
-      for (int i = late * NI / kAhead; i < (late + 1) * NI / kAhead; ++i) fetch_b(ks + 1 < KS ? now : next, (ks + 1) % KS, i);
-      if (ks + 1 == KS) {
+      for (int j = late * NI / kAhead; j < (late + 1) * NI / kAhead; ++j) fetch_b(next, half ^ 1, j);
+    } else {
 #pragma unroll
-        for (int i = late * kLoads / kAhead; i < (late + 1) * kLoads / kAhead; ++i) begin(i);
-      }
+      for (int l = i * kLoads / (MI - kAhead); l < (i + 1) * kLoads / (MI - kAhead); ++l) begin(l);
     }
 #pragma unroll
     for (int j = 0; j < NI; ++j)
-      acc[s % MI][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[ks & 1][j], fa[s % kRing], acc[s % MI][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[half][j], fa[i % kRing], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
   const auto nothing = [](int) {};
 
-  // The depths of k: what k has beyond whole depths comes first, filled up with zeros.  The
+  // The depths of k go in pairs, the last one filled up with zeros (DIRECT: all are whole).  The
   // workgroup loads depth after depth, tile after tile; (lv, lt) is the next to load.
-  const int rest = p.k % DEPTH ? p.k % DEPTH : DEPTH, depths = (p.k + DEPTH - 1) / DEPTH;
+  const int depths = (p.k + 2 * kDepth - 1) / (2 * kDepth) * 2;
   A sa;
   B sb;
   int lv = blockIdx.x, lt = 0;
@@ -205,15 +202,14 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     sa.aim(p.a, p.sa, m0, p.m);
     sb.aim(p.b, p.sb, n0, p.n);
   };
-  const auto k_of = [&]() { return lt == 0 ? 0 : rest + (lt - 1) * DEPTH; };
-  const auto left_of = [&]() { return lt == 0 ? rest : DEPTH; };
-  const auto begin = [&](uint32_t ta, uint32_t tb, int k, int left, int i) {
-    if (i < A::kLoads) sa.one(ta, k, left, i);
-    else sb.one(tb, k, left, i - A::kLoads);
+  const auto begin = [&](uint32_t to, int l) {
+    if (l < A::kLoads) sa.one(to, l);
+    else sb.one(to + kA, l - A::kLoads);
   };
   const auto hold = [&]() {
-    sa.hold(k_of(), left_of());
-    sb.hold(k_of(), left_of());
+    const int left = p.k - lt * kDepth;
+    sa.hold(left);
+    sb.hold(left);
   };
   const auto put = [&](int8_t* to) {
     sa.put(to);
@@ -221,56 +217,47 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   };
   // (Past the workgroup's last depth its loads repeat that one, and nothing reads them.)
   const auto advance = [&]() {
-    if (++lt < depths) return;
-    if (lv + static_cast<int>(gridDim.x) >= tiles) {
-      lt = depths - 1;
-      return;
-    }
-    lt = 0;
-    lv += gridDim.x;
-    aim();
-  };
-  if (depths > 0) {
-    aim();
-    if (DIRECT) {
-      for (int d = 0; d < 2; ++d) {
-        const uint32_t ta = place_of<1024>(lds + d * kStage), tb = place_of<1024>(lds + d * kStage + kA);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) begin(ta, tb, k_of(), left_of(), i);
-        advance();
-      }
+    if (++lt < depths) {
+      sa.base += kDepth;
+      sb.base += kDepth;
+    } else if (lv + static_cast<int>(gridDim.x) < tiles) {
+      lt = 0;
+      lv += gridDim.x;
+      aim();
     } else {
-      hold();
-      put(lds);
-      advance();
+      lt = depths - 1;
     }
-  }
-  // A tile's scales go to LDS in the last depth of the tile before, in three places in turn: a
-  // wave that is still with the outputs of the tile before that keeps its own.
-  float sc[(2 * BN + BM + kLanes - 1) / kLanes];
-  const auto get_scales = [&](int v) {
+  };
+  // A tile's scales, straight to one of three places in turn: a wave that is still with the
+  // outputs of two tiles before keeps its own.
+  const auto get_scales = [&](int v, int turn) {
     int64_t m0, n0;
     place(v, m0, n0);
 #pragma unroll
-    for (int i = 0; i * kLanes < 2 * BN + BM; ++i) {
-      const int at = i * kLanes + threadIdx.x;
-      const int64_t n = n0 + at % BN < p.n ? n0 + at % BN : p.n - 1, m = m0 + at - 2 * BN < p.m ? m0 + at - 2 * BN : p.m - 1;
-      sc[i] = at < BN ? p.bs[n] : at < 2 * BN ? (p.bias ? p.bias[n] : 0.f) : at < 2 * BN + BM ? p.as[m] : 0.f;
+    for (int l = 0; l < kScaleLoads; ++l) {
+      const int c = l * kLanes + threadIdx.x;
+      const int64_t n = n0 + c % BN < p.n ? n0 + c % BN : p.n - 1, m = m0 + (c - 2 * BN) < p.m ? m0 + (c - 2 * BN) : p.m - 1;
+      const float* from = c < BN ? p.bs + n : c < 2 * BN ? (p.bias ? p.bias : p.bs) + n : c < 2 * BN + BM ? p.as + m : p.as;
+      bring_word(place_of<256>(reinterpret_cast<int8_t*>(scale[turn] + l * kLanes)), from);
     }
   };
-  const auto put_scales = [&](int turn) {
+  get_scales(blockIdx.x, 0);
+  if (depths > 0) {
+    aim();
 #pragma unroll
-    for (int i = 0; i * kLanes < 2 * BN + BM; ++i)
-      if (i * kLanes + static_cast<int>(threadIdx.x) < 2 * BN + BM) scale[turn][i * kLanes + threadIdx.x] = sc[i];
-  };
-  get_scales(blockIdx.x);
-  put_scales(0);
-  all_here<0>();
-  if (DIRECT && rest < DEPTH && depths > 0) {
-    sa.clear(lds, rest);
-    if (depths == 1) sa.clear(lds + kStage, rest);
-    all_here<0>();
+    for (int d = 0; d < (DIRECT ? 3 : 2); ++d) {
+      if (DIRECT) {
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) begin(place_of<1024>(lds + d * kStage), l);
+      } else {
+        hold();
+        put(lds + d * kStage);
+      }
+      advance();
+    }
+    if (!DIRECT) hold();
   }
+  all_here<0>();
   if (depths > 0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch_a(lds, i);
@@ -278,58 +265,43 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     for (int i = 0; i < NI; ++i) fetch_b(lds, 0, i);
   }
 
-  // Stores of a whole tile's outputs that may be under way at its next barrier: what that waits
-  // for was begun before them.
-  constexpr int kStores = MI / 2 * (kCols / kSpan) * 2;
-  bool storing = false;
   int stage = 0, turn = 0;
   for (int v = blockIdx.x; v < tiles; v += gridDim.x) {
     int64_t m0, n0;
     place(v, m0, n0);
     const int then = turn == 2 ? 0 : turn + 1;
-    const bool another = v + static_cast<int>(gridDim.x) < tiles;
     // Blocks are read ahead across depths and tiles too: the barrier comes before the last kAhead
-    // slots of a depth, when all of its blocks are in registers.  (The workgroup's last depth
-    // reads what is not there, and does not use it.)
-    for (int t = 0; t < depths; ++t, stage ^= 1) {
-      int8_t* now = lds + stage * kStage;
-      int8_t* next = lds + (stage ^ 1) * kStage;
-      const bool scales = t == depths - 1 && another;
-      if (scales) get_scales(v + gridDim.x);
-      const bool held = !DIRECT && (t + 1 < depths || another);
-      if (held) {
-        hold();
-        advance();
-      }
+    // slots of a depth, when all of its blocks are in registers and the loads of all but the
+    // two newest depths have arrived.  (The workgroup's last depth reads what is not there, and
+    // does not use it.)  Every instruction here that is none of the matrix units' counts, since
+    // a SIMD's two waves stand at the barrier together.
+    for (int t = 0; t < depths; t += 2) {
 #pragma unroll
-      for (int i = 0; i < S - kAhead; ++i) slot(now, next, i, nothing);
-      if (held) put(next);
-      if (scales) put_scales(then);
-      if (!DIRECT) {
-        all_here<0>();
-      } else {      // all but the stores
-        if (t == 0 && storing) all_here<kStores>();
-        else all_here<0>();
-        if (rest < DEPTH && t == depths - 1) {
-          sa.clear(next, rest);
-          all_here<0>();
+      for (int half = 0; half < 2; ++half) {
+        int8_t* now = lds + stage;
+        stage = (stage + kStage) & (kStages * kStage - 1);
+        int8_t* next = lds + stage;
+        if (!DIRECT) {      // what was read a depth ago is for the depth after the next
+          put(lds + ((stage + kStage) & (kStages * kStage - 1)));
+          advance();
+          hold();
         }
-      }
-      const uint32_t ta = place_of<1024>(now), tb = place_of<1024>(now + kA);
-      const int k = k_of(), left = left_of();
+        const uint32_t to = place_of<1024>(lds + ((stage + 2 * kStage) & (kStages * kStage - 1)));
 #pragma unroll
-      for (int i = S - kAhead; i < S; ++i)
-        slot(now, next, i, [&](int l) {
-          if (DIRECT) begin(ta, tb, k, left, l);
-        });
-      if (DIRECT) advance();
+        for (int i = 0; i < MI - kAhead; ++i)
+          slot(now, next, half, i, [&](int l) {
+            if (DIRECT) begin(to, l);
+          });
+        if (DIRECT) advance();
+        all_here<DIRECT ? 2 * kLoads : 63>();
+#pragma unroll
+        for (int i = MI - kAhead; i < MI; ++i) slot(now, next, half, i, nothing);
+      }
     }
-
-    if (depths == 0 && another) {
-      get_scales(v + gridDim.x);
-      put_scales(then);
-      all_here<0>();
-    }
+    // The tile's scales have arrived: its second barrier waits for all but the loads begun since its
+    // start.
+    if (depths == 0) all_here<0>();
+    get_scales(v + static_cast<int>(gridDim.x) < tiles ? v + static_cast<int>(gridDim.x) : v, then);
 
     // Outputs: 32 rows of 64 bytes at a time through LDS of the wave's own, so that they leave in
     // 16-byte words, four to a row.
@@ -347,7 +319,9 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
 #pragma unroll
           for (int g = 0; g < kSpan / 16; ++g) {
             const int c = j * kSpan + g * 16 + h * 4;
-            const f32x4 vb = *reinterpret_cast<const f32x4*>(bs + c), bias = *reinterpret_cast<const f32x4*>(bs + BN + c);
+            const f32x4 vb = *reinterpret_cast<const f32x4*>(bs + c);
+            f32x4 bias = {};
+            if (p.bias) bias = *reinterpret_cast<const f32x4*>(bs + BN + c);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               f32x4 out;
@@ -381,7 +355,6 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
         }
       }
     };
-    storing = m0 + BM <= p.m && n0 + BN <= p.n && depths > 1;
     if (m0 + BM <= p.m && n0 + BN <= p.n) outputs(std::true_type{});
     else outputs(std::false_type{});
 #pragma unroll
@@ -390,7 +363,7 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
       for (int j = 0; j < NI; ++j) acc[i][j] = i32x4{};
     turn = then;
   }
-  if (DIRECT) all_here<0>();   // no load to LDS outlives the workgroup
+  all_here<0>();   // no load to LDS outlives the workgroup
 }
 
 // Outputs from the sums of the parts of k.
@@ -472,19 +445,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void i8_few_kernel(MatmulParams p) 
 
 namespace {
 
-// Rows that loads straight to LDS can take: whole 16-byte chunks, and a tile's rows within 32 bits.
+// Rows that loads straight to LDS can take: whole pairs of depths, at multiples of 16 bytes, and a
+// tile's rows within 32 bits of offsets.
 bool direct(const MatmulParams& p) {
   const auto fine = [&](const int8_t* q, int64_t stride, int rows) {
     return reinterpret_cast<uintptr_t>(q) % 16 == 0 && (rows == 1 || (stride % 16 == 0 && stride < (1 << 23)));
   };
-  return p.k % 16 == 0 && fine(p.a, p.sa, p.m) && fine(p.b, p.sb, p.n);
+  return p.k % (2 * kDepth) == 0 && fine(p.a, p.sa, p.m) && fine(p.b, p.sb, p.n);
 }
 
 template <typename Tout, int BM, int BN, int WM, int WN, int GROUPS, bool DIRECT>
 void tiles(const MatmulParams& p, int parts, hipStream_t s) {
   const int ntm = (p.m - 1) / BM + 1, ntn = (p.n - 1) / BN + 1;
   const int64_t n = static_cast<int64_t>(ntm) * ntn, most = kUnits * GROUPS;
-  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, 128, GROUPS, DIRECT>), dim3(static_cast<unsigned>(n < most ? n : most), parts),
+  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, GROUPS, DIRECT>), dim3(static_cast<unsigned>(n < most ? n : most), parts),
                      dim3(64 * WM * WN), 0, s, p, ntm, ntn);
 }
 
@@ -492,14 +466,12 @@ template <typename Tout>
 void by_tiles(const MatmulParams& p, int parts, hipStream_t s) {
   const int64_t big = static_cast<int64_t>((p.m - 1) / 256 + 1) * ((p.n - 1) / 256 + 1);
   const int64_t mid = static_cast<int64_t>((p.m - 1) / 128 + 1) * ((p.n - 1) / 128 + 1);
-  if (!direct(p)) return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 2, false>(p, parts, s) : tiles<Tout, 64, 64, 2, 2, 2, false>(p, parts, s);
+  if (!direct(p)) return big >= 256 ? tiles<Tout, 256, 256, 2, 4, 1, false>(p, parts, s) : mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 2, false>(p, parts, s) : tiles<Tout, 64, 64, 2, 2, 2, false>(p, parts, s);
   const char* e = getenv("MM_V");
   const int v = e ? atoi(e) : 0;
   if (v == 2) return tiles<Tout, 256, 256, 2, 4, 1, true>(p, parts, s);
   if (v == 4) return tiles<Tout, 128, 128, 2, 2, 2, true>(p, parts, s);
   if (v == 6) return tiles<Tout, 64, 64, 2, 2, 3, true>(p, parts, s);
-  if (v == 7) return tiles<Tout, 256, 128, 4, 2, 1, true>(p, parts, s);
-  if (v == 8) return tiles<Tout, 128, 64, 2, 2, 2, true>(p, parts, s);
   if (big >= 256) return tiles<Tout, 256, 256, 2, 4, 1, true>(p, parts, s);
   return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 2, true>(p, parts, s) : tiles<Tout, 64, 64, 2, 2, 3, true>(p, parts, s);
 }
