@@ -597,10 +597,6 @@ sscan_status sscan_i8_quant(int64_t rows, int64_t dim, int dtype, const void* x,
 /* Products of a row that sscan_i8_matmul sums: any codes (-128 included) stay inside 32 bits. */
 #define SSCAN_I8_MAX_K 131071
 
-/* Workspace bytes of sscan_i8_matmul (0: none needed).  With less, or none, it runs without
- * splitting the sums over workgroups: the same result, slower. */
-size_t sscan_i8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
-
 /*
  * Product of rows in 8-bit integers, with the scales of both sides:
  *
@@ -613,14 +609,12 @@ size_t sscan_i8_matmul_workspace_size(int64_t m, int64_t n, int64_t k);
  *   b, b_scales : [n, k] (int8), row stride b_stride; [n] (float32)
  *   bias        : [n] (float32), NULL: zero
  *   out         : [m, n] (dtype), row stride out_stride
- *   workspace   : sscan_i8_matmul_workspace_size, 256-byte aligned, NULL: none
- * Any strides and alignment work; rows at multiples of 16 bytes are read fastest.  k is at
- * most SSCAN_I8_MAX_K, m and n at most 2^31 - 1.  With k == 0 the sums are zero.
+ * Any strides and alignment work; rows at multiples of 16 bytes with k a multiple of 128 are
+ * read fastest.  k is at most SSCAN_I8_MAX_K, m and n at most 2^31 - 1.  With k == 0 the sums are zero.
  */
 sscan_status sscan_i8_matmul(int64_t m, int64_t n, int64_t k, const int8_t* a, int64_t a_stride,
                              const float* a_scales, const int8_t* b, int64_t b_stride, const float* b_scales,
-                             const float* bias, int dtype, void* out, int64_t out_stride, void* workspace,
-                             size_t workspace_bytes, void* stream);
+                             const float* bias, int dtype, void* out, int64_t out_stride, void* stream);
 
 /*
  * Depthwise causal convolution over time, the prologue of sscan_fwd_conv as an operator of

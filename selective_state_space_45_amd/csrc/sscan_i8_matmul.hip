@@ -9,7 +9,6 @@
 // Large products are bound by power: the matrix units alone, on random codes, reach 4100
 // TOP/s with this instruction and 3450 with v_mfma_i32_32x32x32_i8, on zeros 4850 and 4970.
 #include "sscan_layer.h"
-#include <cstdlib>
 
 namespace sscan {
 
@@ -111,7 +110,6 @@ struct Side {
 };
 
 // Four neighbouring outputs of a row in Tout.
-__device__ __forceinline__ void stage_out(int32_t* p, f32x4 v) { *reinterpret_cast<i32x4*>(p) = __builtin_bit_cast(i32x4, v); }
 __device__ __forceinline__ void stage_out(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void stage_out(bf16_t* p, f32x4 v) {
   typedef __bf16 b4 __attribute__((ext_vector_type(4)));
@@ -130,7 +128,6 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   typedef Side<BN, kWaves, DIRECT> B;
   constexpr int kLoads = A::kLoads + B::kLoads, kA = BM * kDepth, kStage = (BM + BN) * kDepth;
   static_assert((kStage & (kStage - 1)) == 0, "stages follow one another by a mask");
-  constexpr bool kPart = std::is_same<Tout, int32_t>::value;       // sums of a part of k, as they are
   constexpr int kPer = 16 / sizeof(Tout), kSpan = 4 * kPer, kPitch = kSpan + kPer;   // outputs of a row that leave at a time
   // of three tiles: b's scales, biases, a's scales, filled up to whole loads of all waves
   constexpr int kScaleLoads = (2 * BN + BM + kLanes - 1) / kLanes, kScales = kScaleLoads * kLanes;
@@ -138,13 +135,6 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   __shared__ __attribute__((aligned(16))) float scale[3][kScales];
   __shared__ __attribute__((aligned(16))) Tout room[kWaves][32 * kPitch];
   const int tiles = ntm * ntn;
-  if (gridDim.y > 1) {      // this row of the grid sums its part of k
-    const int each = ((p.k + 127) / 128 + gridDim.y - 1) / gridDim.y * 128, from = blockIdx.y * each;
-    p.a += from;
-    p.b += from;
-    p.k = p.k - from < each ? p.k - from : each;
-    p.out = static_cast<Tout*>(p.out) + static_cast<int64_t>(blockIdx.y) * p.m * p.n;
-  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   // Where the workgroup's tile of turn v begins.  Tiles go down 4 rows of tiles, then along n:
@@ -326,10 +316,8 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
             for (int u = 0; u < 2; ++u) {
               f32x4 out;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int32_t sum = acc[2 * i + u][j * kSpan / 16 + g][e];
-                out[e] = kPart ? __int_as_float(sum) : fmaf(static_cast<float>(sum), as[u] * vb[e], bias[e]);
-              }
+              for (int e = 0; e < 4; ++e)
+                out[e] = fmaf(static_cast<float>(acc[2 * i + u][j * kSpan / 16 + g][e]), as[u] * vb[e], bias[e]);
               stage_out(mine + (u * 16 + r) * kPitch + g * 16 + h * 4, out);
             }
           }
@@ -366,47 +354,20 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   all_here<0>();   // no load to LDS outlives the workgroup
 }
 
-// Outputs from the sums of the parts of k.
+// Up to 16 rows of a: b is read once, from memory into registers, and the launch and one latency of
+// memory are most of the time.  A workgroup has 16 rows of b; its waves split k, in steps of 64
+// bytes, and their sums are joined in LDS.  Any alignment: a lane's 16 bytes of a row are loaded
+// as they lie, the last ones of k byte by byte.  1 x 5120 x 2560: 8.5 us a call, 9.6 by tiles;
+// 16 rows about the same either way, and from 32 on the tiles are ahead.
+constexpr int kFewWaves = 8, kFewRows = 16;
 template <typename Tout>
-__global__ __launch_bounds__(256) void i8_join_kernel(MatmulParams p, int parts, int64_t words) {
-  const int64_t id = static_cast<int64_t>(workgroup<256>()) * 256 + threadIdx.x;
-  if (id >= words) return;
-  const int nw = (p.n + 3) / 4;
-  const int64_t m = id / nw;
-  const int n = static_cast<int>(id - m * nw) * 4, have = p.n - n < 4 ? p.n - n : 4;
-  const int64_t all = static_cast<int64_t>(p.m) * p.n;
-  const int32_t* from = p.partial + m * p.n + n;
-  i32x4 sum = {};
-  for (int s = 0; s < parts; ++s, from += all) {
-    if (have == 4) {
-      sum += *reinterpret_cast<const i32x4_any*>(from);
-    } else {
-      for (int e = 0; e < have; ++e) sum[e] += from[e];
-    }
-  }
-  const float as = p.as[m];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < have)
-      store_val(static_cast<Tout*>(p.out) + m * p.so + n + e,
-                fmaf(static_cast<float>(sum[e]), as * p.bs[n + e], p.bias ? p.bias[n + e] : 0.f));
-}
-
-// Few rows of a (at most 16 MI): b is read once, from memory into registers, and the launch and one
-// latency of memory are most of the time.  A workgroup has 16 rows of b; its waves split k, in
-// steps of 64 bytes, and their sums are joined in LDS.  Any alignment: a lane's 16 bytes of a
-// row are loaded as they lie, the last ones of k byte by byte.
-constexpr int kFewWaves = 8;
-template <typename Tout, int MI>
 __global__ __launch_bounds__(64 * kFewWaves) void i8_few_kernel(MatmulParams p) {
-  __shared__ i32x4 sums[kFewWaves][MI][64];
+  __shared__ i32x4 sums[kFewWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, h = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(workgroup<64 * kFewWaves>()) * 16;
   if (n0 >= p.n) return;
+  const int8_t* a = p.a + static_cast<int64_t>(r < p.m ? r : p.m - 1) * p.sa;
   const int8_t* b = p.b + (n0 + r < p.n ? n0 + r : p.n - 1) * p.sb;
-  const int8_t* a[MI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i) a[i] = p.a + static_cast<int64_t>(i * 16 + r < p.m ? i * 16 + r : p.m - 1) * p.sa;
   const auto get = [&](const int8_t* row, int k) {
     if (k + kChunk16 <= p.k) return i32x4(*reinterpret_cast<const i32x4_any*>(row + k));
     uint32_t w[4] = {};
@@ -415,31 +376,24 @@ __global__ __launch_bounds__(64 * kFewWaves) void i8_few_kernel(MatmulParams p) 
   };
   const int steps = (p.k + 63) / 64, each = (steps + kFewWaves - 1) / kFewWaves;
   const int begin = wave * each, end = begin + each < steps ? begin + each : steps;
-  i32x4 acc[MI] = {};
+  i32x4 acc = {};
 #pragma unroll 4
   for (int s = begin; s < end; ++s) {
     const int k = s * 64 + h * kChunk16;
-    const i32x4 fb = get(b, k);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb, get(a[i], k), acc[i], 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(get(b, k), get(a, k), acc, 0, 0, 0);
   }
-#pragma unroll
-  for (int i = 0; i < MI; ++i) sums[wave][i][lane] = acc[i];
+  sums[wave][lane] = acc;
   __syncthreads();
-  for (int i = wave; i < MI; i += kFewWaves) {
-    i32x4 sum = sums[0][i][lane];
+  if (wave != 0 || r >= p.m) return;
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) sum += sums[w][i][lane];
-    const int m = i * 16 + r;
-    if (m >= p.m) continue;
-    const float as = p.as[m];
+  for (int w = 1; w < kFewWaves; ++w) acc += sums[w][lane];
+  const float as = p.as[r];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t n = n0 + h * 4 + e;
-      if (n < p.n)
-        store_val(static_cast<Tout*>(p.out) + m * p.so + n,
-                  fmaf(static_cast<float>(sum[e]), as * p.bs[n], p.bias ? p.bias[n] : 0.f));
-    }
+  for (int e = 0; e < 4; ++e) {
+    const int64_t n = n0 + h * 4 + e;
+    if (n < p.n)
+      store_val(static_cast<Tout*>(p.out) + r * p.so + n,
+                fmaf(static_cast<float>(acc[e]), as * p.bs[n], p.bias ? p.bias[n] : 0.f));
   }
 }
 
@@ -454,75 +408,43 @@ bool direct(const MatmulParams& p) {
   return p.k % (2 * kDepth) == 0 && fine(p.a, p.sa, p.m) && fine(p.b, p.sb, p.n);
 }
 
-template <typename Tout, int BM, int BN, int WM, int WN, int GROUPS, bool DIRECT>
-void tiles(const MatmulParams& p, int parts, hipStream_t s) {
+template <typename Tout, int BM, int BN, int WM, int WN, int GROUPS>
+void tiles(const MatmulParams& p, hipStream_t s) {
   const int ntm = (p.m - 1) / BM + 1, ntn = (p.n - 1) / BN + 1;
   const int64_t n = static_cast<int64_t>(ntm) * ntn, most = kUnits * GROUPS;
-  hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, GROUPS, DIRECT>), dim3(static_cast<unsigned>(n < most ? n : most), parts),
-                     dim3(64 * WM * WN), 0, s, p, ntm, ntn);
+  const dim3 grid(static_cast<unsigned>(n < most ? n : most)), block(64 * WM * WN);
+  if (direct(p)) hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, GROUPS, true>), grid, block, 0, s, p, ntm, ntn);
+  else hipLaunchKernelGGL((i8_tile_kernel<Tout, BM, BN, WM, WN, GROUPS, false>), grid, block, 0, s, p, ntm, ntn);
 }
 
+int64_t tiles_of(const MatmulParams& p, int side) {
+  return static_cast<int64_t>((p.m - 1) / side + 1) * ((p.n - 1) / side + 1);
+}
+
+// The tile's side.  Small tiles while the compute units hold them all at once, two each: what a
+// depth of k takes then is latency, which grows with the tile (256 x 2560 x 5120, in 160 tiles
+// of 64 x 64 15 us, in 40 of 128 x 128 28, in 10 of 256 x 256 55; 2048 x 4096 x 2048, 512 tiles of
+// 128 x 128 24 us, 128 of 256 x 256 28).  Otherwise the largest, which reads least (4096 x 2560 x
+// 2560: 160 of 256 x 256 33 us, 640 of 128 x 128 40; 16411 x 1280 x 2560 float32, 325 tiles in two
+// rounds: 71 us, the 70 tiles of the second round as 270 small ones after the first: 75).
 template <typename Tout>
-void by_tiles(const MatmulParams& p, int parts, hipStream_t s) {
-  const int64_t big = static_cast<int64_t>((p.m - 1) / 256 + 1) * ((p.n - 1) / 256 + 1);
-  const int64_t mid = static_cast<int64_t>((p.m - 1) / 128 + 1) * ((p.n - 1) / 128 + 1);
-  if (!direct(p)) return big >= 256 ? tiles<Tout, 256, 256, 2, 4, 1, false>(p, parts, s) : mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 2, false>(p, parts, s) : tiles<Tout, 64, 64, 2, 2, 2, false>(p, parts, s);
-  const char* e = getenv("MM_V");
-  const int v = e ? atoi(e) : 0;
-  if (v == 2) return tiles<Tout, 256, 256, 2, 4, 1, true>(p, parts, s);
-  if (v == 4) return tiles<Tout, 128, 128, 2, 2, 2, true>(p, parts, s);
-  if (v == 6) return tiles<Tout, 64, 64, 2, 2, 3, true>(p, parts, s);
-  if (big >= 256) return tiles<Tout, 256, 256, 2, 4, 1, true>(p, parts, s);
-  return mid >= 256 ? tiles<Tout, 128, 128, 2, 2, 2, true>(p, parts, s) : tiles<Tout, 64, 64, 2, 2, 3, true>(p, parts, s);
-}
-
-template <typename Tout>
-void few(const MatmulParams& p, hipStream_t s) {
-  const dim3 grid = grid_of<64 * kFewWaves>((static_cast<int64_t>(p.n) + 15) / 16), block(64 * kFewWaves);
-  if (p.m <= 16) hipLaunchKernelGGL((i8_few_kernel<Tout, 1>), grid, block, 0, s, p);
-  else if (p.m <= 32) hipLaunchKernelGGL((i8_few_kernel<Tout, 2>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((i8_few_kernel<Tout, 4>), grid, block, 0, s, p);
-}
-
-int parts_of(int64_t m, int64_t n, int64_t k) {
-  const char* e = getenv("MM_S");
-  if (m <= 64 && !getenv("MM_V")) return 1;
-  int parts = e ? atoi(e) : 1;
-  const int depths = static_cast<int>((k + 127) / 128);
-  if (parts > depths) parts = depths > 0 ? depths : 1;
-  const int each = (depths + parts - 1) / parts;
-  return each > 0 ? (depths + each - 1) / each : 1;       // none of them empty
-}
-
-template <typename Tout>
-hipError_t product(const MatmulParams& p, hipStream_t s) {
-  if (p.m <= 64 && !getenv("MM_V")) {
-    few<Tout>(p, s);
-    return hipGetLastError();
+void product(const MatmulParams& p, hipStream_t s) {
+  const dim3 few_grid = grid_of<64 * kFewWaves>((static_cast<int64_t>(p.n) + 15) / 16);
+  if (p.m <= kFewRows) {
+    hipLaunchKernelGGL((i8_few_kernel<Tout>), few_grid, dim3(64 * kFewWaves), 0, s, p);
+    return;
   }
-  const int parts = p.partial ? parts_of(p.m, p.n, p.k) : 1;
-  if (parts == 1) {
-    by_tiles<Tout>(p, 1, s);
-    return hipGetLastError();
-  }
-  MatmulParams q = p;
-  q.out = p.partial;
-  q.so = p.n;
-  by_tiles<int32_t>(q, parts, s);
-  const int64_t words = static_cast<int64_t>(p.m) * ((p.n + 3) / 4);
-  hipLaunchKernelGGL((i8_join_kernel<Tout>), grid_of<256>((words + 255) / 256), dim3(256), 0, s, p, parts, words);
-  return hipGetLastError();
+  if (tiles_of(p, 64) <= 2 * kUnits) return tiles<Tout, 64, 64, 2, 2, 3>(p, s);
+  if (tiles_of(p, 128) <= 2 * kUnits) return tiles<Tout, 128, 128, 2, 2, 2>(p, s);
+  tiles<Tout, 256, 256, 2, 4, 1>(p, s);
 }
 
 }  // namespace
 
-size_t i8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  const int parts = parts_of(m, n, k);
-  return parts > 1 ? static_cast<size_t>(parts) * m * n * 4 : 0;
-}
-
-hipError_t launch_i8_matmul(const MatmulParams& p, size_t, bool bf16, hipStream_t s) {
-  return bf16 ? product<bf16_t>(p, s) : product<float>(p, s);
+hipError_t launch_i8_matmul(const MatmulParams& p, bool bf16, hipStream_t s) {
+  if (bf16) product<bf16_t>(p, s);
+  else product<float>(p, s);
+  return hipGetLastError();
 }
 
 }  // namespace sscan

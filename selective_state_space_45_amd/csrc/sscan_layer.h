@@ -46,7 +46,6 @@ struct MatmulParams {
   const float* bias;      // nullable
   void* out;
   int64_t so;
-  int32_t* partial;       // nullable: sums of the parts of k
   int m, n, k;
 };
 
@@ -88,12 +87,11 @@ struct ConvStepParams {
 hipError_t launch_rms_fwd(const RmsFwdParams& p, bool bf16, bool kept_bf16, hipStream_t s);
 hipError_t launch_rms_bwd(const RmsBwdParams& p, bool bf16, bool kept_bf16, hipStream_t s);
 hipError_t launch_i8_quant(const RmsFwdParams& p, bool bf16, hipStream_t s);
-hipError_t launch_i8_matmul(const MatmulParams& p, size_t partial_bytes, bool bf16, hipStream_t s);
+hipError_t launch_i8_matmul(const MatmulParams& p, bool bf16, hipStream_t s);
 hipError_t launch_dwconv_fwd(const ConvParams& p, int taps, bool bf16, hipStream_t s);
 hipError_t launch_dwconv_bwd(const ConvParams& p, int taps, bool bf16, hipStream_t s);
 hipError_t launch_dwconv_step(const ConvStepParams& p, int taps, bool bf16, hipStream_t s);
 size_t rms_bwd_workspace_bytes(int64_t rows, int64_t dim);
-size_t i8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 size_t dwconv_bwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim, int taps);
 
 // 8-bit rows.  The scale is the float32 number nearest to top / 127 (a correctly rounded

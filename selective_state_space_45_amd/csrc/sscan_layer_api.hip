@@ -152,7 +152,7 @@ int check_mnk(int64_t m, int64_t n, int64_t k) {
 
 int i8_matmul(int64_t m, int64_t n, int64_t k, const int8_t* a, int64_t a_stride, const float* a_scales,
               const int8_t* b, int64_t b_stride, const float* b_scales, const float* bias, int dtype, void* out,
-              int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
+              int64_t out_stride, void* stream) {
   if (dtype != SSCAN_F32 && dtype != SSCAN_BF16) return fail(SSCAN_ERR_UNSUPPORTED, "unknown dtype %d", dtype);
   SSCAN_TRY(check_mnk(m, n, k));
   if (m == 0 || n == 0) return ok();
@@ -166,19 +166,16 @@ int i8_matmul(int64_t m, int64_t n, int64_t k, const int8_t* a, int64_t a_stride
   SSCAN_TRY(check_f32("a_scales", a_scales));
   SSCAN_TRY(check_f32("b_scales", b_scales));
   SSCAN_TRY(check_f32("bias", bias));
-  if (workspace && !aligned(workspace, 256)) return fail(SSCAN_ERR_INVALID_ARG, "workspace not 256-byte aligned");
-  const size_t need = i8_matmul_workspace_bytes(m, n, k);
-  const bool split = workspace && workspace_bytes >= need && need > 0;
   const size_t cols = static_cast<size_t>(n) * 4;
-  const Buf outs[] = {extent(to, m, n, es), {split ? workspace : nullptr, split ? need : 0}};
+  const Buf outs[] = {extent(to, m, n, es)};
   const Buf ins[] = {extent(ta, m, k, 1), extent(tb, n, k, 1), {a_scales, static_cast<size_t>(m) * 4}, {b_scales, cols},
                      {bias, cols}};
   SSCAN_TRY(check_apart(outs, ins));
   MatmulParams p{};
   p.a = a; p.b = b; p.sa = ta.stride; p.sb = tb.stride; p.as = a_scales; p.bs = b_scales; p.bias = bias;
-  p.out = out; p.so = to.stride; p.partial = split ? static_cast<int32_t*>(workspace) : nullptr;
+  p.out = out; p.so = to.stride;
   p.m = static_cast<int>(m); p.n = static_cast<int>(n); p.k = static_cast<int>(k);
-  const hipError_t e = launch_i8_matmul(p, split ? need : 0, dtype == SSCAN_BF16, static_cast<hipStream_t>(stream));
+  const hipError_t e = launch_i8_matmul(p, dtype == SSCAN_BF16, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "8-bit product launch");
 }
 
@@ -330,17 +327,11 @@ sscan_status sscan_i8_quant(int64_t rows, int64_t dim, int dtype, const void* x,
   return static_cast<sscan_status>(i8_quant(rows, dim, dtype, x, x_stride, codes, codes_stride, scales, stream));
 }
 
-size_t sscan_i8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
-  if (m <= 0 || n <= 0 || k <= 0 || k > SSCAN_I8_MAX_K || m > INT32_MAX || n > INT32_MAX) return 0;
-  return i8_matmul_workspace_bytes(m, n, k);
-}
-
 sscan_status sscan_i8_matmul(int64_t m, int64_t n, int64_t k, const int8_t* a, int64_t a_stride,
                              const float* a_scales, const int8_t* b, int64_t b_stride, const float* b_scales,
-                             const float* bias, int dtype, void* out, int64_t out_stride, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+                             const float* bias, int dtype, void* out, int64_t out_stride, void* stream) {
   return static_cast<sscan_status>(i8_matmul(m, n, k, a, a_stride, a_scales, b, b_stride, b_scales, bias, dtype, out,
-                                             out_stride, workspace, workspace_bytes, stream));
+                                             out_stride, stream));
 }
 
 sscan_status sscan_dwconv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t dconv, int dtype, int silu,

@@ -11,8 +11,8 @@ import torch
 
 from . import _DTYPES, _at, _check, _dense_like, _lib, _nseq, _rows, _scratch, _stream_at
 
-__all__ = ["rms_bwd_workspace_size", "sscan_rms_fwd", "sscan_rms_bwd", "sscan_i8_quant", "i8_matmul_workspace_size",
-           "sscan_i8_matmul", "dwconv_bwd_workspace_size", "sscan_dwconv_fwd", "sscan_dwconv_bwd", "sscan_dwconv_step"]
+__all__ = ["rms_bwd_workspace_size", "sscan_rms_fwd", "sscan_rms_bwd", "sscan_i8_quant", "sscan_i8_matmul",
+           "dwconv_bwd_workspace_size", "sscan_dwconv_fwd", "sscan_dwconv_bwd", "sscan_dwconv_step"]
 
 _P, _I64, _SZ, _F, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
 for _name, _args, _res in (
@@ -20,8 +20,7 @@ for _name, _args, _res in (
         ("sscan_rms_bwd_workspace_size", [_I64] * 2, _SZ),
         ("sscan_rms_bwd", [_I64] * 2 + [_I] * 2 + [_P, _I64, _P, _F, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P], _I),
         ("sscan_i8_quant", [_I64] * 2 + [_I, _P, _I64, _P, _I64, _P, _P], _I),
-        ("sscan_i8_matmul_workspace_size", [_I64] * 3, _SZ),
-        ("sscan_i8_matmul", [_I64] * 3 + [_P, _I64, _P, _P, _I64, _P, _P, _I, _P, _I64, _P, _SZ, _P], _I),
+        ("sscan_i8_matmul", [_I64] * 3 + [_P, _I64, _P, _P, _I64, _P, _P, _I, _P, _I64, _P], _I),
         ("sscan_dwconv_fwd", [_I64] * 4 + [_I] * 2 + [_P, _I64] + [_P] * 4 + [_I64] + [_P] * 3, _I),
         ("sscan_dwconv_bwd_workspace_size", [_I64] * 4, _SZ),
         ("sscan_dwconv_bwd", [_I64] * 4 + [_I] * 2 + [_P, _I64] + [_P] * 4 + [_I64] + [_P] * 3 + [_I64] + [_P] * 4
@@ -191,13 +190,9 @@ def sscan_i8_quant(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales
     return codes, scales
 
 
-def i8_matmul_workspace_size(m: int, n: int, k: int) -> int:
-    return int(_lib.sscan_i8_matmul_workspace_size(m, n, k))
-
-
 def sscan_i8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
                     bias: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
-                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """a b^T of rows in 8-bit integers with the scales of both sides: out[..., j] = a_scale
     b_scale[j] (a . b[j]) + bias[j].  a: [rows, k] or [batch, seqlen, k] int8 with a_scales of
     its shape without k; b: [n, k] int8 with b_scales [n]; bias [n] float32.  Returns [..., n]
@@ -216,13 +211,9 @@ def sscan_i8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=a.device)
     po, so = _rows(out, "out", dtype, shape)
-    need = _lib.sscan_i8_matmul_workspace_size(m, n, k)
-    pws, nws = None, 0
-    if need:
-        workspace, pws, nws = _scratch(workspace, need, a.device)
-    _together(a, a_scales, b, b_scales, bias, out, workspace)
+    _together(a, a_scales, b, b_scales, bias, out)
     _run(a, _lib.sscan_i8_matmul, m, n, k, pa, sa, _at(a_scales, "a_scales", _F32, a.shape[:-1]), pb, sb,
-         _at(b_scales, "b_scales", _F32, (n,)), _at(bias, "bias", _F32, (n,)), _DTYPES[dtype], po, so, pws, nws)
+         _at(b_scales, "b_scales", _F32, (n,)), _at(bias, "bias", _F32, (n,)), _DTYPES[dtype], po, so)
     return out
 
 

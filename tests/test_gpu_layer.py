@@ -246,7 +246,7 @@ def product(ss, m, n, k, dtype, bias=True, layout=(0, 0), seed=6, low=-127, **kw
 
 PRODUCTS = [(1, 1, 1), (1, 16, 64), (1, 5120, 2560), (2, 17, 63), (3, 100, 65), (15, 33, 128), (16, 16, 127), (17, 40, 129), (31, 64, 300),
             (33, 65, 96), (63, 250, 257), (64, 64, 64), (65, 129, 191), (100, 1, 700), (128, 128, 128), (129, 255, 1000), (255, 257, 384),
-            (256, 256, 256), (257, 300, 513), (300, 1000, 1535), (512, 512, 640), (700, 260, 4096), (1000, 777, 129)]
+            (256, 256, 256), (257, 300, 513), (300, 1000, 1535), (512, 512, 640), (1100, 2200, 256), (1100, 2200, 272), (700, 260, 4096), (1000, 777, 129)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -300,20 +300,18 @@ def test_products_into_columns(ss, m, n, k, dtype):
         assert bool((wide == 3.0).all())
 
 
-def test_products_with_and_without_workspace(ss):
-    """A split of the sums changes nothing: they are whole numbers."""
-    lib = ss.library()
-    for m, n, k in ((256, 2560, 5120), (100, 256, 20000), (5, 64, 100000), (256, 256, 8192)):
-        a, sa = code_rows(1, m, k)
-        b, sb = code_rows(2, n, k)
-        want = ss.sscan_i8_matmul(a, sa, b, sb, dtype=F32)
-        got = torch.empty_like(want)
-        rc = lib.sscan_i8_matmul(m, n, k, a.data_ptr(), 0, sa.data_ptr(), b.data_ptr(), 0, sb.data_ptr(), None, 0,
-                                 got.data_ptr(), 0, None, 0, torch.cuda.current_stream().cuda_stream)
-        assert rc == 0
-        same(got, want, (m, n, k))
-        close(got, layer.i8_matmul(a.cpu().numpy(), host(sa), b.cpu().numpy(), host(sb)),
-              layer.i8_matmul_error(a.cpu().numpy(), host(sa), b.cpu().numpy(), host(sb)), (m, n, k))
+@pytest.mark.parametrize("m,n,k", [(16411, 80, 128), (16411, 1280, 256), (4109, 4100, 128), (8192, 2600, 384), (20000, 300, 144)])
+def test_products_of_many_tiles(ss, m, n, k):
+    """Workgroups that take several tiles, rows that go in smaller ones, against float64 on the GPU."""
+    a, sa = code_rows(1, m, k)
+    b, sb = code_rows(2, n, k)
+    bias = normal(3, n)
+    for dtype in (F32, BF16):
+        got = ss.sscan_i8_matmul(a, sa, b, sb, bias=bias, dtype=dtype).double()
+        out = (a.double() @ b.double().t()) * (sa.double()[:, None] * sb.double())
+        want = out + bias.double()
+        err = layer.U * (3.01 * out.abs() + want.abs())
+        assert ((got - want).abs() <= err + HALF[dtype] * (want.abs() + err)).all()
 
 
 def test_products_in_three_dimensions(ss):
