@@ -1,40 +1,94 @@
 // Depthwise causal convolution over time, dense or packed: forward, backward, one token.
+//
+// A few operations an element: bound by memory.  A wave runs along a block of tokens of one
+// batch row with neighbouring channels in its lanes, 8 bytes of a row each, the inputs of the
+// last taps in registers and the next rows already on their way, so that each row is read
+// once but for the few that two blocks share.  Rows need no alignment beyond their elements'.
+// Where a sequence begins and ends is the same for the whole wave: it is looked up once per
+// block and then followed in scalar registers.
 #include "sscan_layer.h"
 
 namespace sscan {
 
-constexpr int kConvTile = 64;   // tokens of a workgroup
+constexpr int kConvWaves = 4;   // waves of a workgroup, one block of tokens after another
 
-// The sequence that token t is in: tokens [lo, hi) of the row, index s among all sequences;
-// hi <= t for padding.  Whatever offsets holds, 0 <= lo <= t, hi <= L and s is in range.
-struct Sequence {
-  int64_t s, lo, hi;
+// V neighbouring channels of a row, at any address its elements may have.
+template <typename Tin, int V>
+struct Word {
+  typedef Tin vec __attribute__((ext_vector_type(V)));
+  typedef vec any __attribute__((aligned(sizeof(Tin))));
+  static __device__ __forceinline__ vec load(const Tin* row, uint32_t at) {
+    uintptr_t r = reinterpret_cast<uintptr_t>(row);   // the row's address stays in scalar registers
+    asm("" : "+s"(r));
+    return *reinterpret_cast<__attribute__((address_space(1))) const any*>(r + at);
+  }
+  static __device__ __forceinline__ void store(Tin* row, uint32_t at, const float* v) {
+    uintptr_t r = reinterpret_cast<uintptr_t>(row);
+    asm("" : "+s"(r));
+    vec out;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      Tin e;
+      store_val(&e, v[j]);
+      out[j] = e;
+    }
+    *reinterpret_cast<__attribute__((address_space(1))) any*>(r + at) = out;
+  }
 };
-__device__ __forceinline__ Sequence sequence_of(const ConvParams& p, int64_t b, int64_t t) {
-  if (!p.offsets) return {b, 0, p.L};
-  int64_t lo = 0, hi = p.num_seqs;                   // the last s with offsets[s] <= t, or 0
+
+// The sequence that the wave's token is in: tokens [lo, hi) of the batch row, index s among
+// all sequences; padding has hi = kNone.  Whatever offsets holds, indexes stay in range.
+constexpr int kNone = INT32_MAX;
+struct Sequence {
+  int64_t s;
+  int lo, hi;
+};
+__device__ __forceinline__ void bounds(const int32_t* offsets, int nseq, int L, int t, Sequence& q) {
+  const int from = offsets[q.s], to = offsets[q.s + 1];
+  q.lo = from < 0 ? 0 : (from > t ? t : from);
+  q.hi = to > L ? L : to;
+  if (q.hi <= t) q.hi = kNone, q.lo = kNone;
+}
+__device__ __forceinline__ Sequence sequence_of(const int32_t* offsets, int nseq, int L, int64_t b, int t) {
+  if (!offsets) return {b, 0, L};
+  int lo = 0, hi = nseq;                             // the last s with offsets[s] <= t, or 0
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (p.offsets[mid] <= t) lo = mid;
+    const int mid = lo + (hi - lo) / 2;
+    if (offsets[mid] <= t) lo = mid;
     else hi = mid;
   }
-  const int64_t from = p.offsets[lo], to = p.offsets[lo + 1];
-  return {lo, from < 0 ? 0 : (from > t ? t : from), to > p.L ? p.L : to};
+  Sequence q{lo, 0, 0};
+  bounds(offsets, nseq, L, t, q);
+  return q;
+}
+// The sequence that begins at t, where one ended.
+__device__ __forceinline__ void follow(const int32_t* offsets, int nseq, int L, int t, Sequence& q) {
+  if (!offsets) {
+    q.lo = q.hi = kNone;
+    return;
+  }
+  while (q.s + 1 < nseq && offsets[q.s + 1] <= t) ++q.s;
+  bounds(offsets, nseq, L, t, q);
 }
 
-// The input at token t, which may lie up to K - 1 before its sequence.
-template <typename Tin, int K>
-__device__ __forceinline__ float input_at(const ConvParams& p, const Sequence& q, int64_t row0, int64_t t, int64_t c) {
-  if (t >= q.lo) return to_f32(static_cast<const Tin*>(p.x)[(row0 + t) * p.sx + c]);
-  if (K == 1 || !p.h0) return 0.f;
-  return p.h0[(q.s * p.dim + c) * (K - 1) + (K - 1) + (t - q.lo)];
-}
-
-template <int K>
-__device__ __forceinline__ void load_taps(const ConvParams& p, int64_t c, float* w, float& b) {
+// Taps, bias and states of V channels.
+template <int K, int V>
+struct Taps {
+  float w[K][V], b[V];
+  __device__ __forceinline__ Taps(const ConvParams& p, int64_t c) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) w[k] = p.w[c * K + k];
-  b = p.b ? p.b[c] : 0.f;
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[k][v] = p.w[(c + v) * K + k];
+      b[v] = p.b ? p.b[c + v] : 0.f;
+    }
+  }
+};
+// Element i of the state [sequences][dim][K - 1] of V channels (zeros without one).
+template <int K, int V>
+__device__ __forceinline__ void state_at(const float* state, int64_t s, int64_t dim, int64_t c, int i, float* out) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) out[v] = state ? state[(s * dim + c + v) * (K - 1) + i] : 0.f;
 }
 
 __device__ __forceinline__ float silu_slope(float v) {
@@ -42,128 +96,322 @@ __device__ __forceinline__ float silu_slope(float v) {
   return g * (1.f + v * (1.f - g));
 }
 
-// dv at token t of sequence q (zero past its end), and its K inputs.
-template <typename Tin, int K>
-__device__ __forceinline__ float dv_at(const ConvParams& p, const Sequence& q, int64_t row0, int64_t t, int64_t c,
-                                       const float* w, float b, float* in) {
-#pragma unroll
-  for (int k = 0; k < K; ++k) in[k] = 0.f;
-  if (t >= q.hi) return 0.f;
-  float v = b;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    in[k] = input_at<Tin, K>(p, q, row0, t - (K - 1) + k, c);
-    v = fmaf(w[k], in[k], v);
+// The work of a wave: its batch row, tokens t0 .. t1 - 1, and channels of a lane, of which
+// those past the last whole word repeat it (and write the same values).
+struct Part {
+  int64_t b, c;
+  int t0, t1;
+  __device__ __forceinline__ Part(const ConvParams& p, uint32_t block, int tokens, int nblk, int nct, int V) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t set = block / nct;
+    b = set / nblk;
+    const int64_t t = (set - b * nblk) * (static_cast<int64_t>(kConvWaves) * tokens) + static_cast<int64_t>(wave) * tokens;
+    t0 = static_cast<int>(t < p.L ? t : p.L);
+    t1 = static_cast<int>(t + tokens < p.L ? t + tokens : p.L);
+    c = (static_cast<int64_t>(block % nct) * 64 + (threadIdx.x & 63)) * V;
+    if (c > p.dim - V) c = p.dim - V;
   }
-  const float dy = to_f32(static_cast<const Tin*>(p.dy)[(row0 + t) * p.dim + c]);
-  return p.silu ? dy * silu_slope(v) : dy;
-}
+};
 
-// One channel a lane, kConvTile tokens of one batch row.
-template <typename Tin, int K>
-__global__ __launch_bounds__(64) void dwconv_fwd_kernel(ConvParams p, int64_t nblk, int64_t nct) {
-  const int64_t id = workgroup<64>();
-  const int64_t c = id % nct * 64 + threadIdx.x, b = id / nct / nblk, t0 = id / nct % nblk * kConvTile;
-  if (b >= p.batch || c >= p.dim) return;
-  const int64_t row0 = b * p.L, t1 = t0 + kConvTile < p.L ? t0 + kConvTile : p.L;
-  float w[K], bias;
-  load_taps<K>(p, c, w, bias);
-  for (int64_t t = t0; t < t1; ++t) {
-    const Sequence q = sequence_of(p, b, t);
-    float y = 0.f;
-    if (t < q.hi) {
-      float v = bias;
+// Inputs before token t of a sequence: of the row, or of the state before it.
+template <typename Tin, int K, int V>
+__device__ __forceinline__ void history(const ConvParams& p, const Sequence& q, const Tin* x, uint32_t at, int64_t c, int t,
+                                        float (&in)[K][V]) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) v = fmaf(w[k], input_at<Tin, K>(p, q, row0, t - (K - 1) + k, c), v);
-      y = p.silu ? silu(v) : v;
+  for (int j = 1; j < K; ++j) {
+    float* to = in[K - 1 - j];
+    if (q.hi == kNone) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) to[v] = 0.f;
+    } else if (t - j >= q.lo) {
+      const typename Word<Tin, V>::vec r = Word<Tin, V>::load(x + (t - j) * p.sx, at);
+#pragma unroll
+      for (int v = 0; v < V; ++v) to[v] = to_f32(r[v]);
+    } else {
+      state_at<K, V>(p.h0, q.s, p.dim, c, K - 1 + (t - j - q.lo), to);
     }
-    store_val(static_cast<Tin*>(p.y) + (row0 + t) * p.dim + c, y);
   }
 }
 
-// The sequence of index s: its place among the rows' tokens.
-__device__ __forceinline__ Sequence sequence(const ConvParams& p, int64_t s, int64_t& row0) {
-  row0 = 0;
-  if (!p.offsets) {
+// One lane for each sequence and channel: the state after it.
+template <typename Tin, int K>
+__device__ __forceinline__ void last_state(const ConvParams& p, int64_t id) {
+  if (!p.h_last || id >= p.num_seqs * p.dim) return;   // a grid that is filled up has more lanes
+  const int64_t s = id / p.dim, c = id - s * p.dim;
+  int64_t row0 = 0, lo = 0, hi = p.L;
+  if (p.offsets) {
+    lo = p.offsets[s] < 0 ? 0 : (p.offsets[s] > p.L ? p.L : p.offsets[s]);
+    hi = p.offsets[s + 1] < lo ? lo : (p.offsets[s + 1] > p.L ? p.L : p.offsets[s + 1]);
+  } else {
     row0 = s * p.L;
-    return {s, 0, p.L};
   }
-  const int64_t from = p.offsets[s], to = p.offsets[s + 1];
-  const int64_t lo = from < 0 ? 0 : (from > p.L ? p.L : from);
-  return {s, lo, to < lo ? lo : (to > p.L ? p.L : to)};
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) {
+    const int64_t t = hi - (K - 1) + j;
+    p.h_last[id * (K - 1) + j] = t >= lo ? to_f32(static_cast<const Tin*>(p.x)[(row0 + t) * p.sx + c])
+                                         : (p.h0 ? p.h0[id * (K - 1) + (K - 1) + (t - lo)] : 0.f);
+  }
 }
 
-template <typename Tin, int K>
-__global__ __launch_bounds__(256) void dwconv_last_kernel(ConvParams p) {
-  const int64_t id = static_cast<int64_t>(workgroup<256>()) * 256 + threadIdx.x;
-  if (id >= p.num_seqs * p.dim) return;
-  const int64_t c = id % p.dim;
-  int64_t row0;
-  const Sequence q = sequence(p, id / p.dim, row0);
+// Blocks of `tokens` tokens (a multiple of kRows).  Workgroups from `main` on write last states.
+template <typename Tin, int K, int V>
+__global__ __launch_bounds__(64 * kConvWaves) void dwconv_fwd_kernel(ConvParams p, const int32_t* __restrict__ offsets, int tokens,
+                                                                     int nblk, int nct, uint32_t main) {
+  constexpr int kRows = 8;      // rows on their way at a time
+  typedef Word<Tin, V> W;
+  const uint32_t block = workgroup<64 * kConvWaves>();
+  if (block >= main) return last_state<Tin, K>(p, static_cast<int64_t>(block - main) * (64 * kConvWaves) + threadIdx.x);
+  const Part at(p, block, tokens, nblk, nct, V);
+  if (at.t0 >= at.t1) return;
+  const int L = static_cast<int>(p.L), nseq = static_cast<int>(p.num_seqs);
+  const Tin* x = static_cast<const Tin*>(p.x) + at.b * p.L * p.sx;
+  Tin* y = static_cast<Tin*>(p.y) + at.b * p.L * p.dim;
+  const uint32_t lane = static_cast<uint32_t>(at.c * sizeof(Tin));
+  typename W::vec next[kRows];
+  const auto load = [&](int t) {      // rows past the block's end repeat its last one
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) p.h_last[id * (K - 1) + j] = input_at<Tin, K>(p, q, row0, q.hi - (K - 1) + j, c);
-}
-
-template <typename Tin, int K>
-__global__ __launch_bounds__(64) void dwconv_bwd_kernel(ConvParams p, int64_t nblk, int64_t nct) {
-  const int64_t id = workgroup<64>();
-  const int64_t c = id % nct * 64 + threadIdx.x, blk = id / nct, b = blk / nblk, t0 = blk % nblk * kConvTile;
-  if (b >= p.batch || c >= p.dim) return;
-  const int64_t row0 = b * p.L, t1 = t0 + kConvTile < p.L ? t0 + kConvTile : p.L;
-  float w[K], bias, dw[K] = {}, db = 0.f;
-  load_taps<K>(p, c, w, bias);
-  for (int64_t t = t0; t < t1; ++t) {
-    const Sequence q = sequence_of(p, b, t);
-    float dx = 0.f;
-    if (t < q.hi) {
-      float in[K];
+    for (int k = 0; k < kRows; ++k) next[k] = W::load(x + (t + k < at.t1 ? t + k : at.t1 - 1) * p.sx, lane);
+  };
+  load(at.t0);
+  const Taps<K, V> taps(p, at.c);
+  Sequence q = sequence_of(offsets, nseq, L, at.b, at.t0);
+  float in[K][V];
+  history<Tin, K, V>(p, q, x, lane, at.c, at.t0, in);
+  const auto run = [&](auto with_silu) {
+    for (int t = at.t0; t < at.t1; t += kRows) {
+      typename W::vec now[kRows];
 #pragma unroll
-      for (int j = K - 1; j >= 0; --j) dx = fmaf(w[K - 1 - j], dv_at<Tin, K>(p, q, row0, t + j, c, w, bias, in), dx);
-      const float dv = dv_at<Tin, K>(p, q, row0, t, c, w, bias, in);
+      for (int k = 0; k < kRows; ++k) now[k] = next[k];
+      if (t + kRows < at.t1) load(t + kRows);
 #pragma unroll
-      for (int k = 0; k < K; ++k) dw[k] = fmaf(dv, in[k], dw[k]);
-      db += dv;
-      const int64_t j = t - (q.hi - (K - 1));
-      if (K > 1 && p.dlast && j >= 0) dx += p.dlast[(q.s * p.dim + c) * (K - 1) + j];
+      for (int k = 0; k < kRows; ++k) {
+        if (t + k >= at.t1) break;
+        if (t + k == q.hi) {
+          follow(offsets, nseq, L, t + k, q);
+          history<Tin, K, V>(p, q, x, lane, at.c, t + k, in);
+        }
+        float out[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          in[K - 1][v] = to_f32(now[k][v]);
+          float sum = taps.b[v];
+#pragma unroll
+          for (int i = 0; i < K; ++i) sum = fmaf(taps.w[i][v], in[i][v], sum);
+          out[v] = decltype(with_silu)::value ? silu(sum) : sum;
+          if (q.hi == kNone) out[v] = 0.f;
+#pragma unroll
+          for (int i = 0; i < K - 1; ++i) in[i][v] = in[i + 1][v];
+        }
+        W::store(y + (t + k) * p.dim, lane, out);
+      }
     }
-    store_val(static_cast<Tin*>(p.dx) + (row0 + t) * p.sdx + c, dx);
-  }
-#pragma unroll
-  for (int k = 0; k < K; ++k) p.partial[(blk * p.dim + c) * (K + 1) + k] = dw[k];
-  p.partial[(blk * p.dim + c) * (K + 1) + K] = db;
+  };
+  if (p.silu) run(std::true_type{});
+  else run(std::false_type{});
 }
 
+// One lane for each sequence and channel: the gradient of the state before it, from the
+// sequence's first tokens.
 template <typename Tin, int K>
-__global__ __launch_bounds__(256) void dwconv_dinitial_kernel(ConvParams p) {
-  const int64_t id = static_cast<int64_t>(workgroup<256>()) * 256 + threadIdx.x;
-  if (id >= p.num_seqs * p.dim) return;
-  const int64_t c = id % p.dim;
-  int64_t row0;
-  const Sequence q = sequence(p, id / p.dim, row0);
-  float w[K], bias, in[K];
-  load_taps<K>(p, c, w, bias);
+__device__ __forceinline__ void dinitial_state(const ConvParams& p, int64_t id) {
+  if (!p.dh0 || id >= p.num_seqs * p.dim) return;   // a grid that is filled up has more lanes
+  const int64_t s = id / p.dim, c = id - s * p.dim;
+  int64_t row0 = 0, lo = 0, hi = p.L;
+  if (p.offsets) {
+    lo = p.offsets[s] < 0 ? 0 : (p.offsets[s] > p.L ? p.L : p.offsets[s]);
+    hi = p.offsets[s + 1] < lo ? lo : (p.offsets[s + 1] > p.L ? p.L : p.offsets[s + 1]);
+  } else {
+    row0 = s * p.L;
+  }
+  const Taps<K, 1> taps(p, c);
+  float in[2 * K] = {}, dv[K] = {};                   // inputs from K - 1 tokens before on, gradients of the first K - 1
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) in[j] = p.h0 ? p.h0[id * (K - 1) + j] : 0.f;
+#pragma unroll
+  for (int m = 0; m < K - 1; ++m) {
+    if (lo + m >= hi) continue;
+    in[K - 1 + m] = to_f32(static_cast<const Tin*>(p.x)[(row0 + lo + m) * p.sx + c]);
+    float v = taps.b[0];
+#pragma unroll
+    for (int k = 0; k < K; ++k) v = fmaf(taps.w[k][0], in[m + k], v);
+    const float dy = to_f32(static_cast<const Tin*>(p.dy)[(row0 + lo + m) * p.dim + c]);
+    dv[m] = p.silu ? dy * silu_slope(v) : dy;
+  }
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) {
     float d = 0.f;
 #pragma unroll
-    for (int m = 0; m <= i; ++m) d = fmaf(w[i - m], dv_at<Tin, K>(p, q, row0, q.lo + m, c, w, bias, in), d);
-    const int64_t j = i - (q.hi - q.lo);
+    for (int m = 0; m <= i; ++m) d = fmaf(taps.w[i - m][0], dv[m], d);
+    const int64_t j = i - (hi - lo);
     if (p.dlast && j >= 0) d += p.dlast[id * (K - 1) + j];
     p.dh0[id * (K - 1) + i] = d;
   }
 }
 
+// Along a block and the K - 1 tokens after it that its last tokens reach: token t's gradient dv
+// completes dx of token t - (K - 1); where a sequence ends, the last K - 1 of its dx are
+// completed without later ones, and with the last state's gradient.  The workgroup's sums of
+// the parameters' gradients go to its row of `partial`, [K + 1][dim], the bias's last.
+template <typename Tin, int K, int V>
+__global__ __launch_bounds__(64 * kConvWaves) void dwconv_bwd_kernel(ConvParams p, const int32_t* __restrict__ offsets, int tokens,
+                                                                     int nblk, int nct, uint32_t main) {
+  constexpr int kRows = 4;      // rows of each side on their way at a time
+  typedef Word<Tin, V> W;
+  __shared__ float sums[kConvWaves - 1][K + 1][V][64];
+  const uint32_t block = workgroup<64 * kConvWaves>();
+  if (block >= main) return dinitial_state<Tin, K>(p, static_cast<int64_t>(block - main) * (64 * kConvWaves) + threadIdx.x);
+  const Part at(p, block, tokens, nblk, nct, V);
+  const int L = static_cast<int>(p.L), nseq = static_cast<int>(p.num_seqs);
+  const uint32_t lane = static_cast<uint32_t>(at.c * sizeof(Tin));
+  float dw[K + 1][V] = {};
+  if (at.t0 < at.t1) {
+    const Tin* x = static_cast<const Tin*>(p.x) + at.b * p.L * p.sx;
+    const Tin* dy = static_cast<const Tin*>(p.dy) + at.b * p.L * p.dim;
+    Tin* dx = static_cast<Tin*>(p.dx) + at.b * p.L * p.sdx;
+    const int end = at.t1 + K - 1 < L ? at.t1 + K - 1 : L;
+    typename W::vec nx[kRows], ng[kRows];
+    const auto load = [&](int t) {      // rows past the end repeat the last one
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int64_t r = t + k < end ? t + k : end - 1;
+        nx[k] = W::load(x + r * p.sx, lane);
+        ng[k] = W::load(dy + r * p.dim, lane);
+      }
+    };
+    load(at.t0);
+    const Taps<K, V> taps(p, at.c);
+    Sequence q = sequence_of(offsets, nseq, L, at.b, at.t0);
+    float in[K][V], dv[K][V] = {};      // of the tokens up to now, the newest last
+    history<Tin, K, V>(p, q, x, lane, at.c, at.t0, in);
+    // dx of token u, `from` tokens before the newest: later gradients than that are not there
+    const auto complete = [&](int u, int from, const float* more) {
+      float out[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        out[v] = more ? more[v] : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (j <= from) out[v] = fmaf(taps.w[K - 1 - j][v], dv[K - 1 - from + j][v], out[v]);
+      }
+      W::store(dx + u * p.sdx, lane, out);
+    };
+    // the last tokens of the sequence, which ends at t; the newest gradient is of token t - 1
+    const auto finish = [&](int t) {
+#pragma unroll
+      for (int j = K - 2; j >= 0; --j) {
+        const int u = t - 1 - j;
+        if (u < q.lo || u < at.t0 || u >= at.t1) continue;
+        float more[V];
+        state_at<K, V>(p.dlast, q.s, p.dim, at.c, K - 2 - j, more);
+        complete(u, j, more);
+      }
+    };
+    const auto run = [&](auto with_silu) {
+      for (int t = at.t0; t < end; t += kRows) {
+        typename W::vec rx[kRows], rg[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) rx[k] = nx[k], rg[k] = ng[k];
+        if (t + kRows < end) load(t + kRows);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const int now = t + k;
+          if (now >= end) break;
+          if (now == q.hi) {
+            finish(now);
+            follow(offsets, nseq, L, now, q);
+            history<Tin, K, V>(p, q, x, lane, at.c, now, in);
+          }
+          if (q.hi == kNone) {          // padding
+            const float zero[V] = {};
+            if (now < at.t1) W::store(dx + now * p.sdx, lane, zero);
+            continue;
+          }
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            in[K - 1][v] = to_f32(rx[k][v]);
+            float d = to_f32(rg[k][v]);
+            if (decltype(with_silu)::value) {
+              float sum = taps.b[v];
+#pragma unroll
+              for (int i = 0; i < K; ++i) sum = fmaf(taps.w[i][v], in[i][v], sum);
+              d *= silu_slope(sum);
+            }
+#pragma unroll
+            for (int i = 0; i < K - 1; ++i) dv[i][v] = dv[i + 1][v];
+            dv[K - 1][v] = d;
+          }
+          if (now < at.t1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+              for (int i = 0; i < K; ++i) dw[i][v] = fmaf(dv[K - 1][v], in[i][v], dw[i][v]);
+              dw[K][v] += dv[K - 1][v];
+            }
+          }
+          if (now - (K - 1) >= q.lo && now - (K - 1) >= at.t0) complete(now - (K - 1), K - 1, nullptr);
+#pragma unroll
+          for (int i = 0; i < K - 1; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) in[i][v] = in[i + 1][v];
+        }
+      }
+    };
+    if (p.silu) run(std::true_type{});
+    else run(std::false_type{});
+    if (end == q.hi) finish(end);
+  }
+  // the waves' sums, added in their order
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i <= K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) sums[wave - 1][i][v][l] = dw[i][v];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  const int64_t set = block / nct;
+#pragma unroll
+  for (int i = 0; i <= K; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float sum = dw[i][v];
+#pragma unroll
+      for (int w = 0; w < kConvWaves - 1; ++w) sum += sums[w][i][v][l];
+      p.partial[(set * (K + 1) + i) * p.dim + at.c + v] = sum;
+    }
+}
+
+// The parameters' gradients from the workgroups' sums: 64 channels of one parameter a workgroup,
+// its 16 waves a 16th of the sums each, eight loads in flight.
+constexpr int kParamWaves = 16;
 template <int K>
-__global__ __launch_bounds__(256) void dwconv_param_kernel(ConvParams p, int64_t blocks) {
-  const int64_t c = blockIdx.x * int64_t(256) + threadIdx.x;
-  if (c >= p.dim) return;
-  float sum[K + 1] = {};
-  for (int64_t b = 0; b < blocks; ++b)
+__global__ __launch_bounds__(64 * kParamWaves) void dwconv_param_kernel(ConvParams p, int64_t sets) {
+  __shared__ float lds[kParamWaves][64];
+  const uint32_t block = workgroup<64 * kParamWaves>();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = block % (K + 1);
+  const int64_t c = static_cast<int64_t>(block / (K + 1)) * 64 + lane;
+  float sum = 0.f;
+  if (c < p.dim) {
+    const float* from = p.partial + i * p.dim + c;
+    const int64_t row = (K + 1) * p.dim;
+    int64_t g = wave;
+    for (; g + 7 * kParamWaves < sets; g += 8 * kParamWaves) {
+      float v[8];
 #pragma unroll
-    for (int k = 0; k <= K; ++k) sum[k] += p.partial[(b * p.dim + c) * (K + 1) + k];
+      for (int k = 0; k < 8; ++k) v[k] = from[(g + k * kParamWaves) * row];
 #pragma unroll
-  for (int k = 0; k < K; ++k) p.dw[c * K + k] = sum[k];
-  if (p.db) p.db[c] = sum[K];
+      for (int k = 0; k < 8; ++k) sum += v[k];
+    }
+    for (; g < sets; g += kParamWaves) sum += from[g * row];
+  }
+  lds[wave][lane] = sum;
+  __syncthreads();
+  if (wave != 0 || c >= p.dim) return;
+#pragma unroll
+  for (int k = 1; k < kParamWaves; ++k) sum += lds[k][lane];
+  if (i < K) p.dw[c * K + i] = sum;
+  else if (p.db) p.db[c] = sum;
 }
 
 template <typename Tin, int K>
@@ -191,52 +439,97 @@ __global__ __launch_bounds__(64) void dwconv_step_kernel(ConvStepParams p, int64
 
 namespace {
 
-int64_t blocks_of(int64_t L) { return (L + kConvTile - 1) / kConvTile; }
+// Tokens of a wave's block, workgroups along the tokens and channels, workgroups in all.
+struct ConvPlan {
+  int tokens, nblk, nct;
+  int64_t main;
+};
 
-template <typename Tin, int K>
-hipError_t fwd(const ConvParams& p, hipStream_t s) {
-  const int64_t nblk = blocks_of(p.L), nct = (p.dim + 63) / 64;
-  if (p.batch * nblk > 0)
-    hipLaunchKernelGGL((dwconv_fwd_kernel<Tin, K>), grid_of<64>(p.batch * nblk * nct), dim3(64), 0, s, p, nblk, nct);
-  if (K > 1 && p.h_last)
-    hipLaunchKernelGGL((dwconv_last_kernel<Tin, K>), grid_of<256>((p.num_seqs * p.dim + 255) / 256), dim3(256), 0, s, p);
-  return hipGetLastError();
+// Blocks as long as 64 tokens, shorter ones while the waves are too few to keep memory busy.
+ConvPlan plan_of(int64_t batch, int64_t L, int64_t dim, int V) {
+  ConvPlan q;
+  q.nct = static_cast<int>((dim + 64 * V - 1) / (64 * V));
+  for (q.tokens = 64; q.tokens > 16; q.tokens /= 2)
+    if (batch * ((L + q.tokens - 1) / q.tokens) * q.nct >= 4096) break;
+  q.nblk = static_cast<int>((L + kConvWaves * q.tokens - 1) / (kConvWaves * q.tokens));
+  q.main = batch * q.nblk * q.nct;
+  return q;
+}
+
+// Channels of a lane: 8 bytes of a row, or one where the row has fewer.
+int lane_channels(int64_t dim, size_t elem) { return dim >= static_cast<int64_t>(8 / elem) ? static_cast<int>(8 / elem) : 1; }
+
+int64_t lanes_of(int64_t n) { return (n + 64 * kConvWaves - 1) / (64 * kConvWaves); }
+
+template <typename Tin, int K, int V>
+void fwd(const ConvParams& p, hipStream_t s) {
+  const ConvPlan q = plan_of(p.batch, p.L, p.dim, V);
+  const int64_t more = K > 1 && p.h_last ? lanes_of(p.num_seqs * p.dim) : 0;
+  if (q.main + more > 0)
+    hipLaunchKernelGGL((dwconv_fwd_kernel<Tin, K, V>), grid_of<64 * kConvWaves>(q.main + more), dim3(64 * kConvWaves), 0, s, p, p.offsets,
+                       q.tokens, q.nblk, q.nct, static_cast<uint32_t>(q.main));
+}
+
+template <typename Tin, int K, int V>
+void bwd(const ConvParams& p, hipStream_t s) {
+  const ConvPlan q = plan_of(p.batch, p.L, p.dim, V);
+  const int64_t more = K > 1 && p.dh0 ? lanes_of(p.num_seqs * p.dim) : 0;
+  if (q.main + more > 0)
+    hipLaunchKernelGGL((dwconv_bwd_kernel<Tin, K, V>), grid_of<64 * kConvWaves>(q.main + more), dim3(64 * kConvWaves), 0, s, p, p.offsets,
+                       q.tokens, q.nblk, q.nct, static_cast<uint32_t>(q.main));
+  hipLaunchKernelGGL((dwconv_param_kernel<K>), grid_of<64 * kParamWaves>((p.dim + 63) / 64 * (K + 1)), dim3(64 * kParamWaves), 0, s, p,
+                     p.batch * q.nblk);
 }
 
 template <typename Tin, int K>
-hipError_t bwd(const ConvParams& p, hipStream_t s) {
-  const int64_t nblk = blocks_of(p.L), nct = (p.dim + 63) / 64;
-  if (p.batch * nblk > 0)
-    hipLaunchKernelGGL((dwconv_bwd_kernel<Tin, K>), grid_of<64>(p.batch * nblk * nct), dim3(64), 0, s, p, nblk, nct);
-  if (K > 1 && p.dh0 && p.num_seqs > 0)
-    hipLaunchKernelGGL((dwconv_dinitial_kernel<Tin, K>), grid_of<256>((p.num_seqs * p.dim + 255) / 256), dim3(256), 0, s, p);
-  hipLaunchKernelGGL((dwconv_param_kernel<K>), dim3((p.dim + 255) / 256), dim3(256), 0, s, p, p.batch * nblk);
-  return hipGetLastError();
-}
-
-template <typename Tin, int K>
-hipError_t step(const ConvStepParams& p, hipStream_t s) {
+void step(const ConvStepParams& p, hipStream_t s) {
   const int64_t nct = (p.dim + 63) / 64;
   hipLaunchKernelGGL((dwconv_step_kernel<Tin, K>), grid_of<64>(p.batch * nct), dim3(64), 0, s, p, nct);
+}
+
+// f(element, taps) with both as types.
+template <typename F>
+hipError_t by_type(int taps, bool bf16, F&& f) {
+  const auto of = [&](auto elem) {
+    switch (taps) {
+      case 1: return f(elem, std::integral_constant<int, 1>{});
+      case 2: return f(elem, std::integral_constant<int, 2>{});
+      case 3: return f(elem, std::integral_constant<int, 3>{});
+      default: return f(elem, std::integral_constant<int, 4>{});
+    }
+  };
+  if (bf16) of(bf16_t{});
+  else of(float{});
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t dwconv_bwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim, int taps) {
-  return static_cast<size_t>(batch) * blocks_of(L) * dim * (taps + 1) * 4;
+  if (batch <= 0 || L <= 0 || dim <= 0) return 0;
+  // of the type with the more workgroups along the tokens
+  const int64_t a = plan_of(batch, L, dim, lane_channels(dim, 2)).nblk, b = plan_of(batch, L, dim, lane_channels(dim, 4)).nblk;
+  return static_cast<size_t>(batch) * (a > b ? a : b) * dim * (taps + 1) * 4;
 }
 
-#define SSCAN_BY_TAPS(call)                                          \
-  switch (taps) {                                                    \
-    case 1: return bf16 ? call<bf16_t, 1>(p, s) : call<float, 1>(p, s); \
-    case 2: return bf16 ? call<bf16_t, 2>(p, s) : call<float, 2>(p, s); \
-    case 3: return bf16 ? call<bf16_t, 3>(p, s) : call<float, 3>(p, s); \
-    default: return bf16 ? call<bf16_t, 4>(p, s) : call<float, 4>(p, s); \
-  }
+hipError_t launch_dwconv_fwd(const ConvParams& p, int taps, bool bf16, hipStream_t s) {
+  return by_type(taps, bf16, [&](auto elem, auto k) {
+    typedef decltype(elem) Tin;
+    if (lane_channels(p.dim, sizeof(Tin)) > 1) fwd<Tin, decltype(k)::value, 8 / sizeof(Tin)>(p, s);
+    else fwd<Tin, decltype(k)::value, 1>(p, s);
+  });
+}
 
-hipError_t launch_dwconv_fwd(const ConvParams& p, int taps, bool bf16, hipStream_t s) { SSCAN_BY_TAPS(fwd) }
-hipError_t launch_dwconv_bwd(const ConvParams& p, int taps, bool bf16, hipStream_t s) { SSCAN_BY_TAPS(bwd) }
-hipError_t launch_dwconv_step(const ConvStepParams& p, int taps, bool bf16, hipStream_t s) { SSCAN_BY_TAPS(step) }
+hipError_t launch_dwconv_bwd(const ConvParams& p, int taps, bool bf16, hipStream_t s) {
+  return by_type(taps, bf16, [&](auto elem, auto k) {
+    typedef decltype(elem) Tin;
+    if (lane_channels(p.dim, sizeof(Tin)) > 1) bwd<Tin, decltype(k)::value, 8 / sizeof(Tin)>(p, s);
+    else bwd<Tin, decltype(k)::value, 1>(p, s);
+  });
+}
+
+hipError_t launch_dwconv_step(const ConvStepParams& p, int taps, bool bf16, hipStream_t s) {
+  return by_type(taps, bf16, [&](auto elem, auto k) { step<decltype(elem), decltype(k)::value>(p, s); });
+}
 
 }  // namespace sscan
