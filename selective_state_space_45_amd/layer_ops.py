@@ -65,12 +65,34 @@ def _float(t: torch.Tensor, name: str) -> int:
     return _DTYPES[t.dtype]
 
 
-def _code_rows(shape, device) -> torch.Tensor:
-    """Codes whose rows start at multiples of 16 bytes (which sscan_i8_matmul reads fastest)."""
-    dim = shape[-1]
+def _new(x: torch.Tensor, dtype, given: Optional[torch.Tensor], name: str):
+    """(dense tensor of x's shape, its address): the given one, checked, or a new one."""
+    if given is not None:
+        return given, _at(given, name, dtype, x.shape)
+    t = torch.empty_like(x, dtype=dtype) if x.is_contiguous() else torch.empty(x.shape, dtype=dtype, device=x.device)
+    return t, t.data_ptr()
+
+
+def _codes(x: torch.Tensor, given: Optional[torch.Tensor]):
+    """(codes for x, address, row stride), new ones with rows that start at multiples of 16
+    bytes (which sscan_i8_matmul reads fastest)."""
+    dim = x.shape[-1]
+    if given is not None:
+        return (given, *_rows(given, "codes", _I8, x.shape))
     if dim % 16 == 0:
-        return torch.empty(shape, dtype=_I8, device=device)
-    return torch.empty((*shape[:-1], (dim + 15) // 16 * 16), dtype=_I8, device=device)[..., :dim]
+        return (*_new(x, _I8, None, "codes"), dim)
+    wide = (dim + 15) // 16 * 16
+    t = torch.empty((*x.shape[:-1], wide), dtype=_I8, device=x.device)
+    return t[..., :dim], t.data_ptr(), wide
+
+
+def _scales(x: torch.Tensor, given: Optional[torch.Tensor]):
+    """(a scale for each row of x, address)."""
+    shape = x.shape[:-1]
+    if given is not None:
+        return given, _at(given, "scales", _F32, shape)
+    t = torch.empty(shape, dtype=_F32, device=x.device)
+    return t, t.data_ptr()
 
 
 def rms_bwd_workspace_size(rows: int, dim: int) -> int:
@@ -91,7 +113,7 @@ def sscan_rms_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residu
     tensors by name; out["residual"] may be residual itself."""
     rows, dim = _tokens(x, "x")
     dt = _float(x, "x")
-    shape, dtype, dev = x.shape, x.dtype, x.device
+    shape, dtype = x.shape, x.dtype
     if residual is not None:
         if residual_dtype not in (None, residual.dtype):
             raise ValueError(f"residual must be {residual_dtype}, got {residual.dtype}")
@@ -105,26 +127,21 @@ def sscan_rms_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residu
     px, sx = _rows(x, "x", dtype, shape)
     pres, pw = _at(residual, "residual", residual_dtype, shape), _at(weight, "weight", _F32, (dim,))
     out = dict(out) if out else {}
-    y = kept = codes = scales = None
+    get = out.get
+    y = py = kept = pk = codes = pc = scales = psc = None
+    sc = dim
     if want_y:
-        y = out.get("y")
-        if y is None:
-            y = out["y"] = _dense_like(x)
+        y, py = _new(x, dtype, get("y"), "y")
+        out["y"] = y
     if want_residual:
-        kept = out.get("residual")
-        if kept is None:
-            kept = out["residual"] = torch.empty(shape, dtype=residual_dtype, device=dev)
-    pc, sc = None, dim
+        kept, pk = _new(x, residual_dtype, get("residual"), "residual")
+        out["residual"] = kept
     if want_codes:
-        codes, scales = out.get("codes"), out.get("scales")
-        if codes is None:
-            codes = out["codes"] = _code_rows(shape, dev)
-        if scales is None:
-            scales = out["scales"] = torch.empty(shape[:-1], dtype=_F32, device=dev)
-        pc, sc = _rows(codes, "codes", _I8, shape)
+        codes, pc, sc = _codes(x, get("codes"))
+        scales, psc = _scales(x, get("scales"))
+        out["codes"], out["scales"] = codes, scales
     _together(x, residual, weight, y, kept, codes, scales)
-    _run(x, _lib.sscan_rms_fwd, rows, dim, dt, _DTYPES[residual_dtype], px, sx, pres, pw, eps, _at(y, "y", dtype, shape),
-         _at(kept, "residual", residual_dtype, shape), pc, sc, _at(scales, "scales", _F32, shape[:-1]))
+    _run(x, _lib.sscan_rms_fwd, rows, dim, dt, _DTYPES[residual_dtype], px, sx, pres, pw, eps, py, pk, pc, sc, psc)
     return out
 
 
@@ -178,15 +195,11 @@ def sscan_i8_quant(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales
     without its last dimension)."""
     rows, dim = _tokens(x, "x")
     dt = _float(x, "x")
-    shape = x.shape
-    px, sx = _rows(x, "x", x.dtype, shape)
-    if codes is None:
-        codes = _code_rows(shape, x.device)
-    if scales is None:
-        scales = torch.empty(shape[:-1], dtype=_F32, device=x.device)
-    pc, sc = _rows(codes, "codes", _I8, shape)
+    px, sx = _rows(x, "x", x.dtype, x.shape)
+    codes, pc, sc = _codes(x, codes)
+    scales, ps = _scales(x, scales)
     _together(x, codes, scales)
-    _run(x, _lib.sscan_i8_quant, rows, dim, dt, px, sx, pc, sc, _at(scales, "scales", _F32, shape[:-1]))
+    _run(x, _lib.sscan_i8_quant, rows, dim, dt, px, sx, pc, sc, ps)
     return codes, scales
 
 
@@ -205,14 +218,16 @@ def sscan_i8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_
         dtype = out.dtype
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
+    lead = a.shape[:-1]
     pa, sa = _rows(a, "a", _I8, a.shape)
     pb, sb = _rows(b, "b", _I8, (n, k))
-    shape = (*a.shape[:-1], n)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=a.device)
-    po, so = _rows(out, "out", dtype, shape)
+        out = torch.empty((*lead, n), dtype=dtype, device=a.device)
+        po, so = out.data_ptr(), n
+    else:
+        po, so = _rows(out, "out", dtype, (*lead, n))
     _together(a, a_scales, b, b_scales, bias, out)
-    _run(a, _lib.sscan_i8_matmul, m, n, k, pa, sa, _at(a_scales, "a_scales", _F32, a.shape[:-1]), pb, sb,
+    _run(a, _lib.sscan_i8_matmul, m, n, k, pa, sa, _at(a_scales, "a_scales", _F32, lead), pb, sb,
          _at(b_scales, "b_scales", _F32, (n,)), _at(bias, "bias", _F32, (n,)), _DTYPES[dtype], po, so)
     return out
 
