@@ -1,7 +1,7 @@
 // Products of rows in 8-bit integers with the scales of both sides.
 //
 // out[m, n] = (sum_k a[m, k] b[n, k]) (as[m] bs[n]) + bias[n].  Both sides have k along their
-// rows, so both go through LDS the same way: 128 bytes of each row at a time, in 16-byte
+// rows, so both go through LDS the same way: 64 bytes of each row at a time, in 16-byte
 // chunks, which are what a lane of a matrix instruction takes (v_mfma_i32_16x16x64_i8: lane l
 // holds row l % 16, bytes 16 (l / 16) .. + 15 of 64).  The order of k is the same on both
 // sides and otherwise free, since the sums are whole numbers.
@@ -288,9 +288,11 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
         for (int i = MI - kAhead; i < MI; ++i) slot(now, next, half, i, nothing);
       }
     }
-    // The tile's scales have arrived: its second barrier waits for all but the loads begun since its
-    // start.
-    if (depths == 0) all_here<0>();
+    // The tile's scales have arrived: DIRECT, its second barrier waits for all but the loads begun
+    // since its start; by way of registers, a depth waits for what was read a depth ago, but near
+    // the end of k, and with no tile to follow, nothing is read: at least its first depth reads the
+    // fourth, if that is not among the last two.
+    if (depths == 0 || (!DIRECT && depths <= 4)) all_here<0>();
     get_scales(v + static_cast<int>(gridDim.x) < tiles ? v + static_cast<int>(gridDim.x) : v, then);
 
     // Outputs: 32 rows of 64 bytes at a time through LDS of the wave's own, so that they leave in

@@ -314,6 +314,21 @@ def test_products_of_many_tiles(ss, m, n, k):
         assert ((got - want).abs() <= err + HALF[dtype] * (want.abs() + err)).all()
 
 
+@pytest.mark.parametrize("k", [1, 16, 48, 64, 70, 130, 150, 192, 250, 300, 400])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_products_of_many_tiles_with_few_depths(ss, k, pad):
+    """Scales that change from tile to tile, while there is little of k to wait for."""
+    m, n = 16411, 1300
+    a, sa = code_rows(1, m, k, pad=pad)
+    b, sb = code_rows(2, n, k, pad=pad)
+    sums = a.double() @ b.double().t()
+    for seed in range(3):
+        sa, sb = normal(seed, m).abs() + 0.1, normal(seed + 9, n).abs() + 0.1
+        out = sums * (sa.double()[:, None] * sb.double())
+        got = ss.sscan_i8_matmul(a, sa, b, sb, dtype=F32).double()
+        assert ((got - out).abs() <= layer.U * 3.01 * out.abs() + HALF[F32] * out.abs() * (1 + layer.U * 4) + TINY).all()
+
+
 def test_products_in_three_dimensions(ss):
     a, sa = code_rows(1, 6, 48)
     b, sb = code_rows(2, 10, 48)
