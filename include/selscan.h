@@ -545,7 +545,8 @@ sscan_status sscan_glr_step(int64_t batch, int64_t dim, int dtype, float* state,
  *   codes, scales: y in 8 bits as sscan_i8_quant gives it (from y before its rounding to
  *                  dtype), both or neither; codes has the row stride codes_stride
  * residual_dtype is SSCAN_F32, or dtype.  eps is at least 0 and finite.  Sums are float32:
- * a row whose sum of squares passes float32's range has r = 0.
+ * a row whose sum of squares passes float32's range has r = 0, and one whose mean(s^2) + eps
+ * is below its normal numbers (2^-126; never with eps of that size) has r infinite.
  */
 sscan_status sscan_rms_fwd(int64_t rows, int64_t dim, int dtype, int residual_dtype, const void* x, int64_t x_stride,
                            const void* residual, const float* weight, float eps, void* y, void* residual_out,
