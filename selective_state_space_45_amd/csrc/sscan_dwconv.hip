@@ -157,7 +157,7 @@ __device__ __forceinline__ void last_state(const ConvParams& p, int64_t id) {
 template <typename Tin, int K, int V>
 __global__ __launch_bounds__(64 * kConvWaves) void dwconv_fwd_kernel(ConvParams p, const int32_t* __restrict__ offsets, int tokens,
                                                                      int nblk, int nct, uint32_t main) {
-  constexpr int kRows = 8;      // rows on their way at a time
+  constexpr int kRows = 4;      // rows on their way at a time
   typedef Word<Tin, V> W;
   const uint32_t block = workgroup<64 * kConvWaves>();
   if (block >= main) return last_state<Tin, K>(p, static_cast<int64_t>(block - main) * (64 * kConvWaves) + threadIdx.x);
@@ -177,32 +177,45 @@ __global__ __launch_bounds__(64 * kConvWaves) void dwconv_fwd_kernel(ConvParams 
   Sequence q = sequence_of(offsets, nseq, L, at.b, at.t0);
   float in[K][V];
   history<Tin, K, V>(p, q, x, lane, at.c, at.t0, in);
+  const auto token = [&](int now, typename W::vec vx, auto with_silu) {
+    float out[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      in[K - 1][v] = to_f32(vx[v]);
+      float sum = taps.b[v];
+#pragma unroll
+      for (int i = 0; i < K; ++i) sum = fmaf(taps.w[i][v], in[i][v], sum);
+      out[v] = decltype(with_silu)::value ? silu(sum) : sum;
+#pragma unroll
+      for (int i = 0; i < K - 1; ++i) in[i][v] = in[i + 1][v];
+    }
+    W::store(y + now * p.dim, lane, out);
+  };
   const auto run = [&](auto with_silu) {
     for (int t = at.t0; t < at.t1; t += kRows) {
-      typename W::vec now[kRows];
+      typename W::vec rows[kRows];
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) now[k] = next[k];
+      for (int k = 0; k < kRows; ++k) rows[k] = next[k];
       if (t + kRows < at.t1) load(t + kRows);
+      if (t + kRows <= at.t1 && t + kRows <= q.hi && q.hi != kNone) {      // all of one sequence
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        if (t + k >= at.t1) break;
+        for (int k = 0; k < kRows; ++k) token(t + k, rows[k], with_silu);
+        continue;
+      }
+#pragma unroll 1
+      for (int k = 0; k < kRows && t + k < at.t1; ++k) {
         if (t + k == q.hi) {
           follow(offsets, nseq, L, t + k, q);
           history<Tin, K, V>(p, q, x, lane, at.c, t + k, in);
         }
-        float out[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          in[K - 1][v] = to_f32(now[k][v]);
-          float sum = taps.b[v];
-#pragma unroll
-          for (int i = 0; i < K; ++i) sum = fmaf(taps.w[i][v], in[i][v], sum);
-          out[v] = decltype(with_silu)::value ? silu(sum) : sum;
-          if (q.hi == kNone) out[v] = 0.f;
-#pragma unroll
-          for (int i = 0; i < K - 1; ++i) in[i][v] = in[i + 1][v];
+        if (q.hi == kNone) {          // padding
+          const float zero[V] = {};
+          W::store(y + (t + k) * p.dim, lane, zero);
+        } else {
+          token(t + k, rows[0], with_silu);
         }
-        W::store(y + (t + k) * p.dim, lane, out);
+#pragma unroll
+        for (int j = 0; j < kRows - 1; ++j) rows[j] = rows[j + 1];
       }
     }
   };
@@ -306,13 +319,50 @@ __global__ __launch_bounds__(64 * kConvWaves) void dwconv_bwd_kernel(ConvParams 
         complete(u, j, more);
       }
     };
+    // Token `now`; `inner`: it is one of the block's, and so is the token whose dx it completes, of
+    // the same sequence.
+    const auto token = [&](int now, typename W::vec vx, typename W::vec vg, auto with_silu, auto inner) {
+      constexpr bool kInner = decltype(inner)::value;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        in[K - 1][v] = to_f32(vx[v]);
+        float d = to_f32(vg[v]);
+        if (decltype(with_silu)::value) {
+          float sum = taps.b[v];
+#pragma unroll
+          for (int i = 0; i < K; ++i) sum = fmaf(taps.w[i][v], in[i][v], sum);
+          d *= silu_slope(sum);
+        }
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) dv[i][v] = dv[i + 1][v];
+        dv[K - 1][v] = d;
+      }
+      if (kInner || now < at.t1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+          for (int i = 0; i < K; ++i) dw[i][v] = fmaf(dv[K - 1][v], in[i][v], dw[i][v]);
+          dw[K][v] += dv[K - 1][v];
+        }
+      }
+      if (kInner || (now - (K - 1) >= q.lo && now - (K - 1) >= at.t0)) complete(now - (K - 1), K - 1, nullptr);
+#pragma unroll
+      for (int i = 0; i < K - 1; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) in[i][v] = in[i + 1][v];
+    };
     const auto run = [&](auto with_silu) {
       for (int t = at.t0; t < end; t += kRows) {
         typename W::vec rx[kRows], rg[kRows];
 #pragma unroll
         for (int k = 0; k < kRows; ++k) rx[k] = nx[k], rg[k] = ng[k];
         if (t + kRows < end) load(t + kRows);
+        if (t - (K - 1) >= at.t0 && t - (K - 1) >= q.lo && t + kRows <= at.t1 && t + kRows <= q.hi && q.hi != kNone) {
 #pragma unroll
+          for (int k = 0; k < kRows; ++k) token(t + k, rx[k], rg[k], with_silu, std::true_type{});
+          continue;
+        }
+#pragma unroll 1
         for (int k = 0; k < kRows; ++k) {
           const int now = t + k;
           if (now >= end) break;
@@ -324,35 +374,11 @@ __global__ __launch_bounds__(64 * kConvWaves) void dwconv_bwd_kernel(ConvParams 
           if (q.hi == kNone) {          // padding
             const float zero[V] = {};
             if (now < at.t1) W::store(dx + now * p.sdx, lane, zero);
-            continue;
+          } else {
+            token(now, rx[0], rg[0], with_silu, std::false_type{});
           }
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            in[K - 1][v] = to_f32(rx[k][v]);
-            float d = to_f32(rg[k][v]);
-            if (decltype(with_silu)::value) {
-              float sum = taps.b[v];
-#pragma unroll
-              for (int i = 0; i < K; ++i) sum = fmaf(taps.w[i][v], in[i][v], sum);
-              d *= silu_slope(sum);
-            }
-#pragma unroll
-            for (int i = 0; i < K - 1; ++i) dv[i][v] = dv[i + 1][v];
-            dv[K - 1][v] = d;
-          }
-          if (now < at.t1) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-#pragma unroll
-              for (int i = 0; i < K; ++i) dw[i][v] = fmaf(dv[K - 1][v], in[i][v], dw[i][v]);
-              dw[K][v] += dv[K - 1][v];
-            }
-          }
-          if (now - (K - 1) >= q.lo && now - (K - 1) >= at.t0) complete(now - (K - 1), K - 1, nullptr);
-#pragma unroll
-          for (int i = 0; i < K - 1; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) in[i][v] = in[i + 1][v];
+          for (int j = 0; j < kRows - 1; ++j) rx[j] = rx[j + 1], rg[j] = rg[j + 1];
         }
       }
     };
