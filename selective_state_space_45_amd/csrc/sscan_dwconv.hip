@@ -1,11 +1,15 @@
 // Depthwise causal convolution over time, dense or packed: forward, backward, one token.
 //
-// A few operations an element: bound by memory.  A wave runs along a block of tokens of one
-// batch row with neighbouring channels in its lanes, 8 bytes of a row each, the inputs of the
-// last taps in registers and the next rows already on their way, so that each row is read
-// once but for the few that two blocks share.  Rows need no alignment beyond their elements'.
-// Where a sequence begins and ends is the same for the whole wave: it is looked up once per
-// block and then followed in scalar registers.
+// Bound by memory, and the backward nearly as much by its arithmetic.  A wave runs along a block of
+// tokens of one batch row with neighbouring channels in its lanes, 8 bytes of a row each, the
+// inputs of the last taps in registers and the next rows already on their way, so that each row is
+// read once but for the few that two blocks share.  Rows need no alignment beyond their elements'.
+// Where a sequence begins and ends is the same for the whole wave: it is looked up once per block
+// and then followed in scalar registers.  Tokens go in groups of as many as are on their way:
+// a group inside one sequence without a test or a move, any other by a loop over its tokens (with
+// the tests in every token the forward of 8 x 4096 x 2048 bf16 took 66 us, now 51; the backward
+// 132, now 108).  At 5 TB/s their reads and writes take 54 and 81 us; the backward issues about
+// 130 vector instructions for each 4 channels of a token and wave, some 60 us of them.
 #include "sscan_layer.h"
 
 namespace sscan {
@@ -471,13 +475,15 @@ struct ConvPlan {
   int64_t main;
 };
 
-// Blocks of 16 tokens, longer ones where the waves are many (backward of 8 x 4096 x 2048 bf16 in
-// blocks of 16, 32, 64: 142, 132, 142 us; forward of 16411 x 2560: 44, 47, 50).
+// Blocks of 64 tokens, of which the first and the last few take the slower way; shorter ones while
+// the waves are too few to keep memory busy (in blocks of 16, 32, 64: backward of 8 x 4096 x 2048
+// bf16, 4096 waves in blocks of 64, 139, 119, 108 us; of 4094 x 1535 float32, 768 waves, 20.6,
+// 22.6, 24.7 us; forward of 16411 x 2560 bf16, 2570 waves, 38, 39, 39).
 ConvPlan plan_of(int64_t batch, int64_t L, int64_t dim, int V) {
   ConvPlan q;
   q.nct = static_cast<int>((dim + 64 * V - 1) / (64 * V));
-  for (q.tokens = 32; q.tokens > 16; q.tokens /= 2)
-    if (batch * ((L + q.tokens - 1) / q.tokens) * q.nct >= 8192) break;
+  for (q.tokens = 64; q.tokens > 16; q.tokens /= 2)
+    if (batch * ((L + q.tokens - 1) / q.tokens) * q.nct >= 4096) break;
   q.nblk = static_cast<int>((L + kConvWaves * q.tokens - 1) / (kConvWaves * q.tokens));
   q.main = batch * q.nblk * q.nct;
   return q;

@@ -425,7 +425,8 @@ int64_t tiles_of(const MatmulParams& p, int side) {
 
 // The tile's side.  Small tiles while the compute units hold them all at once, two each: what a
 // depth of k takes then is latency, which grows with the tile (256 x 2560 x 5120, in 160 tiles
-// of 64 x 64 15 us, in 40 of 128 x 128 28, in 10 of 256 x 256 55; 2048 x 4096 x 2048, 512 tiles of
+// of 64 x 64 15 us, in 40 of 128 x 128 28, in 10 of 256 x 256 55; but 256 x 10240 x 2560, in 640 of
+// 64 x 64 21 us, in 160 of 128 x 128 17; 2048 x 4096 x 2048, 512 tiles of
 // 128 x 128 24 us, 128 of 256 x 256 28).  Otherwise the largest, which reads least (4096 x 2560 x
 // 2560: 160 of 256 x 256 33 us, 640 of 128 x 128 40; 16411 x 1280 x 2560 float32, 325 tiles in two
 // rounds: 71 us, the 70 tiles of the second round as 270 small ones after the first: 75).
