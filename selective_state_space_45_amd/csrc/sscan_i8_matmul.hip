@@ -50,9 +50,11 @@ __device__ __forceinline__ uint32_t place_of(int8_t* p) {
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) int8_t*)p) + (threadIdx.x >> 6) * BYTES));
 }
 
-// LDS holds kStages depths of k, kDepth bytes of each row: one is multiplied, the next is there,
-// the others are on their way.  (Two depths of 128 bytes, the next begun as one ends: 8192^3
-// 435 us; a load takes about 1.2 us from its begin, a depth of 128 bytes is multiplied in 0.9.)
+// LDS holds kStages depths of k, kDepth bytes of each row: a pair of depths is multiplied while the
+// next is on its way.  Both depths of a pair are begun together, so that they meet in the
+// 128-byte lines that memory is read in (begun one by one, three depths ahead, every line passed
+// from L2 to a compute unit twice: 8192^3 463 us, now 433; a compute unit then got about 43 bytes a
+// nanosecond, whatever the tile).
 constexpr int kDepth = 64, kStages = 4;
 
 // One side's rows of a tile on their way to LDS.  Chunk c of row r goes to slot (c ^ r / 4) & 3
@@ -83,9 +85,11 @@ struct Side {
   // rows past the end repeat the last one: their sums are not written
   __device__ __forceinline__ int row(int i) const { return row0 + kStep * i < last ? row0 + kStep * i : last; }
 
-  // DIRECT: load i of the next kDepth bytes of the rows, all there.
-  __device__ __forceinline__ void one(uint32_t to, int i) const {
+  // DIRECT: load i of the next two depths of the rows, all there: the second finds its half of the
+  // lines on their way.
+  __device__ __forceinline__ void two(uint32_t to, uint32_t then, int i) const {
     bring(to + i * kStep * kDepth, reinterpret_cast<uintptr_t>(base), at[i]);
+    bring(then + i * kStep * kDepth, reinterpret_cast<uintptr_t>(base) + kDepth, at[i]);
   }
   // The same by way of registers, from any address, zeros past the `left` bytes that are there.
   __device__ __forceinline__ void hold(int left) {
@@ -150,9 +154,13 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   // A depth is MI slots, each a block of a's rows times all of b's: the order within a slot, and
   // of slots, is fixed (left to itself the compiler reads blocks when they are needed, and the
   // matrix unit waits for them).  A slot reads a's block for kAhead slots later, the last kAhead
-  // slots of a depth also b's blocks of the next.
+  // slots of a depth also b's blocks of the next.  The loads of a pair begin in the last kAhead
+  // slots of the pair before and go on over kBegin slots: as evenly as leaves them the time
+  // to arrive, which in large tiles is long (8192^3 in 4, 8, 11, 13 slots: 457, 437, 433, 447 us;
+  // in tiles of 128 x 128 4 slots: 256 x 10240 x 2560 16.8 us, in 7 18.2).
   constexpr int kAhead = MI > 3 ? 3 : MI - 1, kRing = kAhead + 1;
   static_assert(MI % kRing == 0 && MI % 2 == 0, "places of blocks are constants");
+  constexpr int kBegin = MI > 4 ? MI + kAhead : MI;
   i32x4 acc[MI][NI] = {}, fa[kRing], fb[2][NI];
   // a block's chunk l / 16 of row l % 16
   const int r = lane & 15, h = lane >> 4, mine_at = r * kDepth + slot_of(r, h) * kChunk16;
@@ -169,19 +177,20 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     if (late >= 0) {
 #pragma unroll
       for (int j = late * NI / kAhead; j < (late + 1) * NI / kAhead; ++j) fetch_b(next, half ^ 1, j);
-    } else {
-#pragma unroll
-      for (int l = i * kLoads / (MI - kAhead); l < (i + 1) * kLoads / (MI - kAhead); ++l) begin(l);
     }
+    const int step = half == 1 ? late : i + kAhead;       // 0 .. in the slots that begin loads
+#pragma unroll
+    for (int l = step * kLoads / kBegin; l < (step + 1) * kLoads / kBegin; ++l)
+      if (l < kLoads) begin(l);
 #pragma unroll
     for (int j = 0; j < NI; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[half][j], fa[i % kRing], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  const auto nothing = [](int) {};
 
   // The depths of k go in pairs, the last one filled up with zeros (DIRECT: all are whole).  The
   // workgroup loads depth after depth, tile after tile; (lv, lt) is the next to load.
+  constexpr int kTurn = DIRECT ? 2 : 1;      // depths that are loaded at a time
   const int depths = (p.k + 2 * kDepth - 1) / (2 * kDepth) * 2;
   A sa;
   B sb;
@@ -192,9 +201,9 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     sa.aim(p.a, p.sa, m0, p.m);
     sb.aim(p.b, p.sb, n0, p.n);
   };
-  const auto begin = [&](uint32_t to, int l) {
-    if (l < A::kLoads) sa.one(to, l);
-    else sb.one(to + kA, l - A::kLoads);
+  const auto begin = [&](uint32_t to, uint32_t then, int l) {
+    if (l < A::kLoads) sa.two(to, then, l);
+    else sb.two(to + kA, then + kA, l - A::kLoads);
   };
   const auto hold = [&]() {
     const int left = p.k - lt * kDepth;
@@ -207,15 +216,16 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   };
   // (Past the workgroup's last depth its loads repeat that one, and nothing reads them.)
   const auto advance = [&]() {
-    if (++lt < depths) {
-      sa.base += kDepth;
-      sb.base += kDepth;
+    lt += kTurn;
+    if (lt < depths) {
+      sa.base += kTurn * kDepth;
+      sb.base += kTurn * kDepth;
     } else if (lv + static_cast<int>(gridDim.x) < tiles) {
       lt = 0;
       lv += gridDim.x;
       aim();
     } else {
-      lt = depths - 1;
+      lt = depths - kTurn;
     }
   };
   // A tile's scales, straight to one of three places in turn: a wave that is still with the
@@ -235,10 +245,10 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   if (depths > 0) {
     aim();
 #pragma unroll
-    for (int d = 0; d < (DIRECT ? 3 : 2); ++d) {
+    for (int d = 0; d < 2; d += kTurn) {
       if (DIRECT) {
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l) begin(place_of<1024>(lds + d * kStage), l);
+        for (int l = 0; l < kLoads; ++l) begin(place_of<1024>(lds), place_of<1024>(lds + kStage), l);
       } else {
         hold();
         put(lds + d * kStage);
@@ -249,6 +259,11 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   }
   all_here<0>();
   if (depths > 0) {
+    if (DIRECT) {
+#pragma unroll
+      for (int l = 0; l < (kAhead < kBegin ? kAhead : kBegin) * kLoads / kBegin; ++l)
+        begin(place_of<1024>(lds + 2 * kStage), place_of<1024>(lds + 3 * kStage), l);
+    }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch_a(lds, i);
 #pragma unroll
@@ -261,9 +276,8 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     place(v, m0, n0);
     const int then = turn == 2 ? 0 : turn + 1;
     // Blocks are read ahead across depths and tiles too: the barrier comes before the last kAhead
-    // slots of a depth, when all of its blocks are in registers and the loads of all but the
-    // two newest depths have arrived.  (The workgroup's last depth reads what is not there, and
-    // does not use it.)  Every instruction here that is none of the matrix units' counts, since
+    // slots of a depth, when all of its blocks are in registers and, at the end of a pair, the next
+    // pair has arrived.  (The workgroup's last depth reads what is not there, and does not use it.)  Every instruction here that is none of the matrix units' counts, since
     // a SIMD's two waves stand at the barrier together.
     for (int t = 0; t < depths; t += 2) {
 #pragma unroll
@@ -276,22 +290,26 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
           advance();
           hold();
         }
-        const uint32_t to = place_of<1024>(lds + ((stage + 2 * kStage) & (kStages * kStage - 1)));
+        const uint32_t to = place_of<1024>(lds + ((stage + (half == 0 ? 1 : 2) * kStage) & (kStages * kStage - 1)));
+        const uint32_t then = place_of<1024>(lds + ((stage + (half == 0 ? 2 : 3) * kStage) & (kStages * kStage - 1)));
 #pragma unroll
         for (int i = 0; i < MI - kAhead; ++i)
           slot(now, next, half, i, [&](int l) {
-            if (DIRECT) begin(to, l);
+            if (DIRECT && half == 0) begin(to, then, l);
           });
-        if (DIRECT) advance();
-        all_here<DIRECT ? 2 * kLoads : 63>();
+        if (!DIRECT || half == 0) all_here<63>();
+        else all_here<0>();
 #pragma unroll
-        for (int i = MI - kAhead; i < MI; ++i) slot(now, next, half, i, nothing);
+        for (int i = MI - kAhead; i < MI; ++i)
+          slot(now, next, half, i, [&](int l) {
+            if (DIRECT) begin(to, then, l);
+          });
+        if (DIRECT && half == 0) advance();
       }
     }
-    // The tile's scales have arrived: DIRECT, its second barrier waits for all but the loads begun
-    // since its start; by way of registers, a depth waits for what was read a depth ago, but near
-    // the end of k, and with no tile to follow, nothing is read: at least its first depth reads the
-    // fourth, if that is not among the last two.
+    // The tile's scales have arrived: DIRECT, with the next pair of depths; by way of registers, a
+    // depth waits for what was read a depth ago, but near the end of k, and with no tile to follow,
+    // nothing is read: at least its first depth reads the fourth, if that is not among the last two.
     if (depths == 0 || (!DIRECT && depths <= 4)) all_here<0>();
     get_scales(v + static_cast<int>(gridDim.x) < tiles ? v + static_cast<int>(gridDim.x) : v, then);
 
@@ -426,9 +444,9 @@ int64_t tiles_of(const MatmulParams& p, int side) {
 // The tile's side.  Small tiles while the compute units hold them all at once, two each: what a
 // depth of k takes then is latency, which grows with the tile (256 x 2560 x 5120, in 160 tiles
 // of 64 x 64 15 us, in 40 of 128 x 128 28, in 10 of 256 x 256 55; but 256 x 10240 x 2560, in 640 of
-// 64 x 64 21 us, in 160 of 128 x 128 17; 2048 x 4096 x 2048, 512 tiles of
-// 128 x 128 24 us, 128 of 256 x 256 28).  Otherwise the largest, which reads least (4096 x 2560 x
-// 2560: 160 of 256 x 256 33 us, 640 of 128 x 128 40; 16411 x 1280 x 2560 float32, 325 tiles in two
+// 64 x 64 21 us, in 160 of 128 x 128 17; 2048 x 4096 x 2048, 512 tiles of 128 x 128 22 us, 128 of
+// 256 x 256 28).  Otherwise the largest, which reads least (4096 x 2560 x
+// 2560: 160 of 256 x 256 36 us, 640 of 128 x 128 40; 16411 x 1280 x 2560 float32, 325 tiles in two
 // rounds: 71 us, the 70 tiles of the second round as 270 small ones after the first: 75).
 template <typename Tout>
 void product(const MatmulParams& p, hipStream_t s) {
