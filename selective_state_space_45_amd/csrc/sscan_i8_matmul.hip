@@ -155,12 +155,14 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   // of slots, is fixed (left to itself the compiler reads blocks when they are needed, and the
   // matrix unit waits for them).  A slot reads a's block for kAhead slots later, the last kAhead
   // slots of a depth also b's blocks of the next.  The loads of a pair begin in the last kAhead
-  // slots of the pair before and go on over kBegin slots: as evenly as leaves them the time
-  // to arrive, which in large tiles is long (8192^3 in 4, 8, 11, 13 slots: 457, 437, 433, 447 us;
-  // in tiles of 128 x 128 4 slots: 256 x 10240 x 2560 16.8 us, in 7 18.2).
+  // slots of the pair before.  In large tiles they go on over kBegin slots, as evenly as leaves them
+  // the time to arrive (8192^3 in 4, 8, 11, 13 slots: 457, 437, 433, 447 us); in small ones that
+  // time is what a pair takes, and they all begin there (256 x 2560 x 5120 15.0 us, now 14.6).  Room
+  // for 8 depths in LDS does not help: a pair of 128 x 128 already fills the 32 KB that the lines
+  // pass through (256 x 10240 x 2560 16.7 us, with 8 depths 21.3).
   constexpr int kAhead = MI > 3 ? 3 : MI - 1, kRing = kAhead + 1;
   static_assert(MI % kRing == 0 && MI % 2 == 0, "places of blocks are constants");
-  constexpr int kBegin = MI > 4 ? MI + kAhead : MI;
+  constexpr int kBegin = MI > 4 ? MI + kAhead : kAhead;
   i32x4 acc[MI][NI] = {}, fa[kRing], fb[2][NI];
   // a block's chunk l / 16 of row l % 16
   const int r = lane & 15, h = lane >> 4, mine_at = r * kDepth + slot_of(r, h) * kChunk16;
