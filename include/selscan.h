@@ -528,7 +528,10 @@ sscan_status sscan_glr_step(int64_t batch, int64_t dim, int dtype, float* state,
  * a decode batch), and a row stride is in elements, 0 for dense.
  */
 
-/* Channels of a row that sscan_rms_fwd, sscan_rms_bwd and sscan_i8_quant accept. */
+/* From here on a tensor with a row stride extends from its first byte to its last: outputs and
+ * inputs that are different columns of one tensor count as overlapping.
+ *
+ * Channels of a row that sscan_rms_fwd, sscan_rms_bwd and sscan_i8_quant accept. */
 #define SSCAN_RMS_MAX_DIM 32768
 
 /*

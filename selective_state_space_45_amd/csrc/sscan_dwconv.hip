@@ -444,6 +444,8 @@ __global__ __launch_bounds__(64 * kParamWaves) void dwconv_param_kernel(ConvPara
   else if (p.db) p.db[c] = sum;
 }
 
+// One token: a lane a channel, whose state is read and written once, 12 bytes of it next to the
+// neighbour's.  256 x 5120 bf16: 8.9 us, its bytes at 5 TB/s 7.3.
 template <typename Tin, int K>
 __global__ __launch_bounds__(64) void dwconv_step_kernel(ConvStepParams p, int64_t nct) {
   const int64_t id = workgroup<64>();
