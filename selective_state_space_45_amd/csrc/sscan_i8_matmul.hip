@@ -57,11 +57,15 @@ __device__ __forceinline__ uint32_t place_of(int8_t* p) {
 // nanosecond, whatever the tile).
 constexpr int kDepth = 64, kStages = 4;
 
-// One side's rows of a tile on their way to LDS.  Chunk c of row r goes to slot (c ^ r / 4) & 3
-// of the row's four, so that 16 lanes that read one chunk of 16 rows take all 64 banks once.
-// The lanes of a wave bring slot after slot of row after row: LDS is then filled in the lanes'
-// order, which is what a load straight to LDS does.
-__device__ __forceinline__ int slot_of(int row, int chunk) { return (chunk ^ (row >> 2)) & 3; }
+// Where a row of 64 bytes in LDS has its 16-byte chunk c: at slot (c ^ -(row / 4)) & 3.  A reading of
+// 16 bytes a lane goes in four parts, of lanes 0-3, 12-15, 20-27 and 4-11, 16-19, 28-31, and the same
+// of the upper half (found by pairs of lanes that read one bank): with a matrix instruction's
+// rows in the lanes, each part then takes all 64 banks once (with c ^ row / 4, which does so for 16
+// lanes in a row, a reading took 8 cycles, not 4).
+__device__ __forceinline__ int slot_of(int row, int chunk) { return (chunk ^ -(row >> 2)) & 3; }
+
+// One side's rows of a tile on their way to LDS.  The lanes of a wave bring slot after slot of row
+// after row: LDS is then filled in the lanes' order, which is what a load straight to LDS does.
 template <int ROWS, int WAVES, bool DIRECT>
 struct Side {
   static constexpr int kStep = 16 * WAVES, kLoads = ROWS / kStep;   // rows of one load of all waves
@@ -132,12 +136,12 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
   typedef Side<BN, kWaves, DIRECT> B;
   constexpr int kLoads = A::kLoads + B::kLoads, kA = BM * kDepth, kStage = (BM + BN) * kDepth;
   static_assert((kStage & (kStage - 1)) == 0, "stages follow one another by a mask");
-  constexpr int kPer = 16 / sizeof(Tout), kSpan = 4 * kPer, kPitch = kSpan + kPer;   // outputs of a row that leave at a time
+  constexpr int kPer = 16 / sizeof(Tout), kSpan = 4 * kPer;   // outputs of a word, and of a row that leave at a time
   // of three tiles: b's scales, biases, a's scales, filled up to whole loads of all waves
   constexpr int kScaleLoads = (2 * BN + BM + kLanes - 1) / kLanes, kScales = kScaleLoads * kLanes;
   __shared__ __attribute__((aligned(16))) int8_t lds[kStages * kStage];
   __shared__ __attribute__((aligned(16))) float scale[3][kScales];
-  __shared__ __attribute__((aligned(16))) Tout room[kWaves][32 * kPitch];
+  __shared__ __attribute__((aligned(16))) Tout room[kWaves][32 * kSpan];
   const int tiles = ntm * ntn;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -340,7 +344,8 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 out[e] = fmaf(static_cast<float>(acc[2 * i + u][j * kSpan / 16 + g][e]), as[u] * vb[e], bias[e]);
-              stage_out(mine + (u * 16 + r) * kPitch + g * 16 + h * 4, out);
+              const int col = g * 16 + h * 4;
+              stage_out(mine + (u * 16 + r) * kSpan + slot_of(r, col / kPer) * kPer + col % kPer, out);
             }
           }
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -351,7 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
             const int n = static_cast<int>(n0) + wn * kCols + j * kSpan + c;
             typedef Tout word __attribute__((ext_vector_type(kPer)));
             typedef word word_any __attribute__((aligned(sizeof(Tout))));
-            const word w = *reinterpret_cast<const word*>(mine + row * kPitch + c);
+            const word w = *reinterpret_cast<const word*>(mine + row * kSpan + slot_of(row, lane % 4) * kPer);
             Tout* to = static_cast<Tout*>(p.out) + m * p.so + n;
             if (decltype(whole)::value || (m < p.m && n + kPer <= p.n)) {
               *reinterpret_cast<word_any*>(to) = w;
