@@ -323,6 +323,7 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     // 16-byte words, four to a row.
     const float* bs = scale[turn] + wn * kCols;
     Tout* mine = room[wave];
+    const int64_t wide = p.n - n0;       // columns from the tile's first on
     const auto outputs = [&](auto whole) {
 #pragma unroll
       for (int i = 0; i < MI / 2; ++i) {
@@ -353,17 +354,17 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
           for (int q = 0; q < 2; ++q) {
             const int row = q * 16 + lane / 4, c = lane % 4 * kPer;
             const int64_t m = mi + row;
-            const int n = static_cast<int>(n0) + wn * kCols + j * kSpan + c;
+            const int n = wn * kCols + j * kSpan + c;
             typedef Tout word __attribute__((ext_vector_type(kPer)));
             typedef word word_any __attribute__((aligned(sizeof(Tout))));
             const word w = *reinterpret_cast<const word*>(mine + row * kSpan + slot_of(row, lane % 4) * kPer);
-            Tout* to = static_cast<Tout*>(p.out) + m * p.so + n;
-            if (decltype(whole)::value || (m < p.m && n + kPer <= p.n)) {
+            Tout* to = static_cast<Tout*>(p.out) + m * p.so + n0 + n;
+            if (decltype(whole)::value || (m < p.m && n + kPer <= wide)) {
               *reinterpret_cast<word_any*>(to) = w;
             } else if (m < p.m) {
 #pragma unroll
               for (int e = 0; e < kPer; ++e)
-                if (n + e < p.n) to[e] = w[e];
+                if (n + e < wide) to[e] = w[e];
             }
           }
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -320,6 +320,31 @@ def test_products_past_32_bits(ss):  # noqa: F811
     check(a[:7], ones(7, 5), codes(130, 256), ones(130, 6), [0, 6])
 
 
+def test_products_of_the_most_rows(ss):  # noqa: F811
+    """2^31 - 1 rows of either side: the last tile would reach past what 31 bits count."""
+    most, k = 2 ** 31 - 1, 16
+    g = torch.Generator("cuda").manual_seed(4)
+    codes = lambda n: torch.randint(-127, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    many, scales = torch.zeros(most, k, dtype=torch.int8, device="cuda"), torch.ones(most, device="cuda")
+    few, fs = codes(17), normal(1, 17).abs() + 0.1
+    for at in (0, 2 ** 30, most - 300):
+        many[at:at + 300] = codes(300)
+        scales[at:at + 300] = normal(2, 300).abs() + 0.1
+    for turn, n in ((0, 17), (1, 17), (0, 1)):
+        a, sa, b, sb = (few[:n], fs[:n], many, scales) if turn == 0 else (many, scales, few[:n], fs[:n])
+        out = ss.sscan_i8_matmul(a, sa, b, sb)
+        for at in (0, 2 ** 30, most - 300):
+            part = slice(at, at + 300)
+            if turn == 0:
+                args, got = (host(a), host(sa), host(b[part]), host(sb[part])), out[:, part]
+            else:
+                args, got = (host(a[part]), host(sa[part]), host(b), host(sb)), out[part]
+            close(got, layer.i8_matmul(*args), layer.i8_matmul_error(*args), f"rows from {at}")
+        rest = out[:, 300:2 ** 30] if turn == 0 else out[300:2 ** 30]
+        assert not bool(rest[..., :4096].any()) and not bool((rest[:, -4096:] if turn == 0 else rest[-4096:]).any())
+        del out, rest
+
+
 def test_convolution_past_32_bits(ss):  # noqa: F811
     L, D = (1 << 20) + 5, 2304                     # 2.4e9 elements in one row
     x, dy = filled(L, D, seed=1)[None], filled(L, D, seed=2)[None]
