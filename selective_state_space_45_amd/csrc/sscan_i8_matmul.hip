@@ -220,7 +220,8 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     sa.put(to);
     sb.put(to + kA);
   };
-  // (Past the workgroup's last depth its loads repeat that one, and nothing reads them.)
+  // (Past the workgroup's last depth its loads repeat that one, and nothing reads them: a test in
+  // each slot costs more, 8192^3 443 us for 432.)
   const auto advance = [&]() {
     lt += kTurn;
     if (lt < depths) {
@@ -323,11 +324,16 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
     // 16-byte words, four to a row.
     const float* bs = scale[turn] + wn * kCols;
     Tout* mine = room[wave];
-    const int64_t wide = p.n - n0;       // columns from the tile's first on
+    // the tile's first output, and the rows and columns of it that there are
+    Tout* first = static_cast<Tout*>(p.out) + m0 * p.so + n0;
+    const int tall = static_cast<int>(p.m - m0 < BM ? p.m - m0 : BM), wide = static_cast<int>(p.n - n0 < BN ? p.n - n0 : BN);
     const auto outputs = [&](auto whole) {
+      int l = lane;      // anew in each tile: what follows from it is not kept over the depths
+      asm volatile("" : "+v"(l));
+      const int r = l & 15, h = l >> 4;
 #pragma unroll
       for (int i = 0; i < MI / 2; ++i) {
-        const int64_t mi = m0 + wm * kRows + i * 32;
+        const int mi = wm * kRows + i * 32;
         float as[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) as[u] = scale[turn][2 * BN + wm * kRows + i * 32 + u * 16 + r];
@@ -352,16 +358,16 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const int row = q * 16 + lane / 4, c = lane % 4 * kPer;
-            const int64_t m = mi + row;
+            const int row = q * 16 + l / 4, c = l % 4 * kPer;
+            const int m = mi + row;
             const int n = wn * kCols + j * kSpan + c;
             typedef Tout word __attribute__((ext_vector_type(kPer)));
             typedef word word_any __attribute__((aligned(sizeof(Tout))));
-            const word w = *reinterpret_cast<const word*>(mine + row * kSpan + slot_of(row, lane % 4) * kPer);
-            Tout* to = static_cast<Tout*>(p.out) + m * p.so + n0 + n;
-            if (decltype(whole)::value || (m < p.m && n + kPer <= wide)) {
+            const word w = *reinterpret_cast<const word*>(mine + row * kSpan + slot_of(row, l % 4) * kPer);
+            Tout* to = first + m * p.so + n;
+            if (decltype(whole)::value || (m < tall && n + kPer <= wide)) {
               *reinterpret_cast<word_any*>(to) = w;
-            } else if (m < p.m) {
+            } else if (m < tall) {
 #pragma unroll
               for (int e = 0; e < kPer; ++e)
                 if (n + e < wide) to[e] = w[e];
@@ -371,7 +377,7 @@ __global__ __launch_bounds__(64 * WM * WN, GROUPS * WM * WN / 4) void i8_tile_ke
         }
       }
     };
-    if (m0 + BM <= p.m && n0 + BN <= p.n) outputs(std::true_type{});
+    if (tall == BM && wide == BN) outputs(std::true_type{});
     else outputs(std::false_type{});
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -454,8 +460,10 @@ int64_t tiles_of(const MatmulParams& p, int side) {
 // of 64 x 64 15 us, in 40 of 128 x 128 28, in 10 of 256 x 256 55; but 256 x 10240 x 2560, in 640 of
 // 64 x 64 21 us, in 160 of 128 x 128 17; 2048 x 4096 x 2048, 512 tiles of 128 x 128 22 us, 128 of
 // 256 x 256 28).  Otherwise the largest, which reads least (4096 x 2560 x
-// 2560: 160 of 256 x 256 36 us, 640 of 128 x 128 40; 16411 x 1280 x 2560 float32, 325 tiles in two
-// rounds: 71 us, the 70 tiles of the second round as 270 small ones after the first: 75).
+// 2560: 160 of 256 x 256 36 us, 640 of 128 x 128 40).  Where they go in rounds of which the last is
+// partly filled, the rows beyond the whole rounds go by the smaller tiles, if those fit at once (float32:
+// 16411 x 1280 x 2560, 325 tiles, 72 us in one launch, 67 with the last 3355 rows in 270 small
+// tiles; 4200 x 4096 x 4096 96 and 78; 9000 x 2048 x 2048 57 and 49; 6000 x 2560 x 5120 71 and 70).
 template <typename Tout>
 void product(const MatmulParams& p, hipStream_t s) {
   const dim3 few_grid = grid_of<64 * kFewWaves>((static_cast<int64_t>(p.n) + 15) / 16);
@@ -465,6 +473,21 @@ void product(const MatmulParams& p, hipStream_t s) {
   }
   if (tiles_of(p, 64) <= 2 * kUnits) return tiles<Tout, 64, 64, 2, 2, 3>(p, s);
   if (tiles_of(p, 128) <= 2 * kUnits) return tiles<Tout, 128, 128, 2, 2, 2>(p, s);
+  const int64_t all = tiles_of(p, 256), across = (p.n - 1) / 256 + 1;
+  const int64_t high = all / kUnits * kUnits / across * 256;       // rows in whole rounds
+  if (high > 0 && high < p.m) {
+    MatmulParams rest = p;
+    rest.m = static_cast<int>(p.m - high);
+    rest.a += high * p.sa;
+    rest.as += high;
+    rest.out = static_cast<Tout*>(p.out) + high * p.so;
+    if (tiles_of(rest, 128) <= 2 * kUnits) {
+      MatmulParams most = p;
+      most.m = static_cast<int>(high);
+      tiles<Tout, 256, 256, 2, 4, 1>(most, s);
+      return product<Tout>(rest, s);
+    }
+  }
   tiles<Tout, 256, 256, 2, 4, 1>(p, s);
 }
 
