@@ -247,7 +247,7 @@ __global__ __launch_bounds__(block_of(LANES)) void rms_fwd_kernel(RmsFwdParams p
   constexpr int kRows = block_of(LANES) / LANES;
   __shared__ float lds[4 * RowLanes<LANES>::kWaves];
   RowLanes<LANES> join(lds);
-  const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  const int lane = kRows == 1 ? threadIdx.x : threadIdx.x % LANES, sub = kRows == 1 ? 0 : threadIdx.x / LANES;
   const Weights<LANES, WORDS> weights(p.weight, lane, p.dim);
   const float per = 1.f / static_cast<float>(p.dim);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < p.rows; row += static_cast<int64_t>(gridDim.x) * kRows) {
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(block_of(LANES)) void rms_bwd_kernel(RmsBwdParams p
   __shared__ float lds[4 * RowLanes<LANES>::kWaves];
   __shared__ float sums[kRows > 1 ? kRows * LANES * kWord : 1];
   RowLanes<LANES> join(lds);
-  const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  const int lane = kRows == 1 ? threadIdx.x : threadIdx.x % LANES, sub = kRows == 1 ? 0 : threadIdx.x / LANES;
   const Weights<LANES, WORDS> weights(p.weight, lane, p.dim);
   float dw[WORDS][kWord] = {};
   const float per = 1.f / static_cast<float>(p.dim);
@@ -409,7 +409,9 @@ namespace {
 
 // Lanes and words of a row.  Forward: few words a lane, which keeps many rows in flight
 // (16411 x 2560 bf16 to 8 bits: 57 us with 256 lanes of 2 words, 62 with 128 of 3, of which
-// fewer idle; 32768 x 2048: the same within 3 %), and rows below 256 lanes on fewer of them.
+// fewer idle; 32768 x 2048: the same within 3 %; one word on each of 320 to 448 lanes: 57, and 3500
+// channels to 8 bits 111 for 98), and rows of fewer words on fewer lanes (16411 x 1400 on 192 of them
+// 34 us, on 256 37; rows alone to 8 bits 21 and 23.5).
 // Backward: one wave a row while it holds it, which joins a row's sums without a barrier and
 // four rows' part of dweight in LDS (4094 x 1535 float32: 30 us, 33 with 256 lanes; 32768 x
 // 2048 bf16 the same within 2 %); fewer than 1024 rows leave compute units idle that way.
@@ -419,7 +421,7 @@ struct RowPlan {
 
 RowPlan forward_plan(int64_t dim) {
   const int words = static_cast<int>((dim + kWord - 1) / kWord);
-  const int lanes = words > 256 * 4 ? 1024 : words > 128 ? 256 : words > 64 ? 128 : 64;
+  const int lanes = words > 256 * 4 ? 1024 : words > 192 ? 256 : words > 64 ? (words + 63) / 64 * 64 : 64;
   return {lanes, (words + lanes - 1) / lanes};
 }
 
@@ -469,6 +471,7 @@ hipError_t fwd(const RmsFwdParams& p, hipStream_t s) {
   };
   if (q.lanes == 64) launch(Int<64>{}, Int<1>{});
   else if (q.lanes == 128) launch(Int<128>{}, Int<1>{});
+  else if (q.lanes == 192) launch(Int<192>{}, Int<1>{});
   else if (q.lanes == 256) with_words(Int<256>{}, q.words, launch);
   else with_many(q.words, launch);
   return hipGetLastError();

@@ -49,7 +49,7 @@ def same(got, want, name):
 # ---------------------------------------------------------------------------------------
 
 TYPES = [(F32, F32), (BF16, BF16), (BF16, F32)]
-ROWS = [(1, 1), (1, 7), (3, 64), (5, 65), (2, 512), (70, 513), (9, 1535), (33, 2048), (4, 2560), (3, 4097), (2, 8192), (3, 20001),
+ROWS = [(1, 1), (1, 7), (3, 64), (5, 65), (2, 512), (70, 513), (6, 1025), (40, 1400), (9, 1535), (33, 2048), (4, 2560), (3, 4097), (2, 8192), (3, 20001),
         (1, 32768)]
 
 

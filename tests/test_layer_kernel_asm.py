@@ -10,7 +10,7 @@ from test_kernel_asm import _compile_asm, _hipcc
 # kernels of the source, and for name patterns the scratch they may use: the norm's backward
 # over rows of 16385 to 32768 channels holds 32 of two inputs in each of 1024 lanes
 SOURCES = {
-    "sscan_rms.hip": (79, {r"rms_bwd_kernel\w*Li1024ELi4E": 64}),
+    "sscan_rms.hip": (84, {r"rms_bwd_kernel\w*Li1024ELi4E": 64}),
     "sscan_i8_matmul.hip": (14, {}),
     "sscan_dwconv.hip": (44, {}),
 }
