@@ -91,7 +91,7 @@ def _scales(x: torch.Tensor, given: Optional[torch.Tensor]):
     shape = x.shape[:-1]
     if given is not None:
         return given, _at(given, "scales", _F32, shape)
-    t = torch.empty(shape, dtype=_F32, device=x.device)
+    t = x.new_empty(shape[0] if len(shape) == 1 else shape, dtype=_F32)      # an int is the cheaper argument
     return t, t.data_ptr()
 
 
@@ -222,7 +222,7 @@ def sscan_i8_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_
     pa, sa = _rows(a, "a", _I8, a.shape)
     pb, sb = _rows(b, "b", _I8, (n, k))
     if out is None:
-        out = torch.empty((*lead, n), dtype=dtype, device=a.device)
+        out = a.new_empty((m, n) if len(lead) == 1 else (*lead, n), dtype=dtype)
         po, so = out.data_ptr(), n
     else:
         po, so = _rows(out, "out", dtype, (*lead, n))
