@@ -314,6 +314,25 @@ def test_products_of_many_tiles(ss, m, n, k):
         assert ((got - want).abs() <= err + HALF[dtype] * (want.abs() + err)).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(1024, 2048, 128), (1025, 2048, 192), (2048, 4096, 128), (2049, 4096, 64), (4096, 4096, 128), (4097, 4096, 100),
+                                   (4101, 4096, 128), (4112, 4096, 384), (4113, 4096, 130), (5000, 4100, 256), (6145, 2560, 128)])
+def test_products_where_the_tiles_change(ss, m, n, k):
+    """Sizes at which the tiles' side changes, or the last rows go by other tiles, from columns of a
+    wider tensor into columns of one."""
+    a, sa = code_rows(1, m, k, pad=32, shift=16)
+    b, sb = code_rows(2, n, k)
+    bias = normal(3, n)
+    out = (a.double() @ b.double().t()) * (sa.double()[:, None] * sb.double())
+    want = out + bias.double()
+    err = layer.U * (3.01 * out.abs() + want.abs())
+    for dtype, start in ((F32, 3), (BF16, 8)):
+        wide = torch.full((m, n + 11), 3.0, dtype=dtype, device="cuda")
+        got = ss.sscan_i8_matmul(a, sa, b, sb, bias=bias, out=wide[:, start:start + n]).double()
+        assert ((got - want).abs() <= err + HALF[dtype] * (want.abs() + err)).all()
+        wide[:, start:start + n] = 3.0
+        assert bool((wide == 3.0).all())
+
+
 @pytest.mark.parametrize("k", [1, 16, 48, 64, 70, 130, 150, 192, 250, 300, 400])
 @pytest.mark.parametrize("pad", [0, 1])
 def test_products_of_many_tiles_with_few_depths(ss, k, pad):
