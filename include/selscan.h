@@ -544,7 +544,8 @@ sscan_status sscan_glr_step(int64_t batch, int64_t dim, int dtype, float* state,
  *   residual     : [rows, dim] (residual_dtype), NULL: s = x rounded to residual_dtype
  *   weight       : [dim] (float32), NULL: ones
  *   y            : [rows, dim] (dtype), NULL: not written
- *   residual_out : [rows, dim] (residual_dtype), s, NULL: not written; may be residual
+ *   residual_out : [rows, dim] (residual_dtype), s, NULL: not written; may be residual (and
+ *                  x too, if x is that tensor, dense and of its type); apart from all else
  *   codes, scales: y in 8 bits as sscan_i8_quant gives it (from y before its rounding to
  *                  dtype), both or neither; codes has the row stride codes_stride
  * residual_dtype is SSCAN_F32, or dtype.  eps is at least 0 and finite.  Sums are float32:
@@ -571,7 +572,8 @@ size_t sscan_rms_bwd_workspace_size(int64_t rows, int64_t dim);
  *   dy            : [rows, dim] (dtype)
  *   dresidual_out : [rows, dim] (residual_dtype), NULL: zero
  *   dx            : [rows, dim] (dtype), row stride dx_stride, NULL: not written
- *   dresidual     : [rows, dim] (residual_dtype), NULL: not written; may be dresidual_out
+ *   dresidual     : [rows, dim] (residual_dtype), NULL: not written; may be dresidual_out (and
+ *                   s or dy too, if dense and of its type); apart from all else
  *   dweight       : [dim] (float32), NULL: not written
  *   workspace     : sscan_rms_bwd_workspace_size, 256-byte aligned (needed for dweight)
  * Results are bitwise reproducible.

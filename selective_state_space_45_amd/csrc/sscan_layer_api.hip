@@ -15,18 +15,25 @@ using namespace sscan;
 size_t size_of(int dtype) { return dtype == SSCAN_BF16 ? 2 : 4; }
 int64_t stride_or(int64_t stride, int64_t dense) { return stride == 0 ? dense : stride; }
 
-// Outputs share bytes with nothing else of the call, except for the pair (may, with), which
-// may be one and the same buffer.
+// Outputs share bytes with nothing else of the call.
 template <size_t NO, size_t NI>
-int check_apart(const Buf (&outs)[NO], const Buf (&ins)[NI], const void* may = nullptr, const void* with = nullptr) {
+int check_apart(const Buf (&outs)[NO], const Buf (&ins)[NI]) {
   for (const Buf& o : outs) {
     for (const Buf& i : ins)
-      if (overlaps(o.p, o.n, i.p, i.n) && !(o.p == may && i.p == with && may == with))
-        return fail(SSCAN_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+      if (overlaps(o.p, o.n, i.p, i.n)) return fail(SSCAN_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
     for (const Buf& q : outs)
       if (&q < &o && overlaps(o.p, o.n, q.p, q.n)) return fail(SSCAN_ERR_INVALID_ARG, "two outputs overlap");
   }
   return SSCAN_OK;
+}
+
+// The bytes of an input that outputs keep apart from.  A dense output with elements of `size` bytes
+// may be `stream`, in which case an input that is the same tensor, element for element, is not counted:
+// each element is read before it is written, by the same lane.  (Other outputs keep apart from it as
+// they do from the output.)
+Buf apart_from(const Tok& in, int64_t rows, int64_t dim, size_t es, const void* out, const void* stream, size_t size) {
+  if (out && out == stream && in.p == out && (rows == 1 || in.stride == dim) && es == size) return {nullptr, 0};
+  return extent(in, rows, dim, es);
 }
 
 // Sizes of an operator on rows.  Workgroups are counted in 31 bits, at least one a row.
@@ -74,8 +81,9 @@ int rms_fwd(int64_t rows, int64_t dim, int dtype, int residual_dtype, const void
   SSCAN_TRY(check_f32("scales", scales));
   const Buf outs[] = {extent(ty, rows, dim, es), extent(tk, rows, dim, er), extent(tc, rows, dim, 1),
                       {scales, static_cast<size_t>(rows) * 4}};
-  const Buf ins[] = {extent(tx, rows, dim, es), extent(tr, rows, dim, er), {weight, static_cast<size_t>(dim) * 4}};
-  SSCAN_TRY(check_apart(outs, ins, residual_out, residual));
+  const auto apart = [&](const Tok& t, size_t e) { return apart_from(t, rows, dim, e, residual_out, residual, er); };
+  const Buf ins[] = {apart(tx, es), apart(tr, er), {weight, static_cast<size_t>(dim) * 4}};
+  SSCAN_TRY(check_apart(outs, ins));
   RmsFwdParams p{};
   p.x = x; p.sx = tx.stride; p.residual = residual; p.weight = weight; p.eps = eps;
   p.y = y; p.kept = residual_out; p.codes = codes; p.sc = tc.stride; p.scales = scales;
@@ -108,8 +116,9 @@ int rms_bwd(int64_t rows, int64_t dim, int dtype, int residual_dtype, const void
   SSCAN_TRY(check_buffer("workspace", workspace, workspace_bytes, need, 256));
   const size_t par = static_cast<size_t>(dim) * 4;
   const Buf outs[] = {extent(tdx, rows, dim, es), extent(tdr, rows, dim, er), {dweight, par}, {workspace, need}};
-  const Buf ins[] = {extent(ts, rows, dim, er), extent(tdy, rows, dim, es), extent(tdk, rows, dim, er), {weight, par}};
-  SSCAN_TRY(check_apart(outs, ins, dresidual, dresidual_out));
+  const auto apart = [&](const Tok& t, size_t e) { return apart_from(t, rows, dim, e, dresidual, dresidual_out, er); };
+  const Buf ins[] = {apart(ts, er), apart(tdy, es), apart(tdk, er), {weight, par}};
+  SSCAN_TRY(check_apart(outs, ins));
   RmsBwdParams p{};
   p.s = s; p.ss = ts.stride; p.weight = weight; p.eps = eps; p.dy = dy; p.dkept = dresidual_out;
   p.dx = dx; p.sdx = tdx.stride; p.dresidual = dresidual; p.dweight = dweight;

@@ -551,3 +551,26 @@ def test_convolution_is_the_scans_prologue(ss):
     fused = ss.sscan_fwd(x, dt, A, Bm, C, conv_w=w, conv_b=b)
     y = ss.sscan_fwd(ss.sscan_dwconv_fwd(x, w, conv_b=b), dt, A, Bm, C)
     assert ((y - fused).abs() <= 1e-4 * (1 + fused.abs())).all()
+
+
+@pytest.mark.parametrize("dtype,rtype", TYPES)
+def test_norm_in_place_of_the_stream_itself(ss, dtype, rtype):
+    """The stream that is updated is also another input, where that is of its type."""
+    res, w = normal(1, 70, 300, dtype=rtype), normal(2, 300)
+    if dtype is rtype:
+        want = ss.sscan_rms_fwd(res, w, residual=res)
+        stream = res.clone()
+        got = ss.sscan_rms_fwd(stream, w, residual=stream, out=dict(residual=stream))
+        same(got["y"], want["y"], "y")
+        same(stream, want["residual"], "residual")
+        want = ss.sscan_rms_bwd(res, w, stream, dresidual=stream, want_dresidual=True)
+        grad = stream.clone()
+        got = ss.sscan_rms_bwd(res, w, grad, dresidual=grad, want_dresidual=True, out=dict(dresidual=grad))
+        for k in want:
+            same(got[k], want[k], k + " from dy")
+    dy = normal(3, 70, 300, dtype=dtype)
+    want = ss.sscan_rms_bwd(res, w, dy, dresidual=res, want_dresidual=True)
+    grad = res.clone()
+    got = ss.sscan_rms_bwd(grad, w, dy, dresidual=grad, want_dresidual=True, out=dict(dresidual=grad))
+    for k in want:
+        same(got[k], want[k], k + " from s")

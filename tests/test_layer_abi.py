@@ -191,3 +191,22 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
                     (lambda: ss.sscan_dwconv_fwd(x, w), "batch, seqlen, dim"), (lambda: ss.sscan_dwconv_step(x, x[None], w), "batch, dim")):
         with pytest.raises(ValueError, match=word):
             f()
+
+
+# The stream that is updated in place is at 1 (the norm) or 4 (its backward), 4 rows of 8 float32.
+STREAM, GRADIENT = at(1), at(4)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=STREAM, sx=16, dtype=0),                  # x at the stream's address, its rows further apart
+    dict(x=STREAM, dtype=1),                         # in other elements
+    dict(x=P(2 * MB + 32), dtype=0),                 # a row further on
+    dict(w=STREAM), dict(w=P(2 * MB + 32))])
+def test_norm_in_place_keeps_apart_from_other_inputs(lib, kw):
+    refused(lib, rms_fwd, dict(kept=STREAM, **kw), INVALID, b"overlap")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(s=GRADIENT, ss=16), dict(s=P(5 * MB + 32)), dict(dy=GRADIENT, dtype=1), dict(dy=P(5 * MB + 32), dtype=0), dict(w=GRADIENT)])
+def test_norm_backward_in_place_keeps_apart_from_other_inputs(lib, kw):
+    refused(lib, rms_bwd, dict(dres=GRADIENT, **kw), INVALID, b"overlap")
