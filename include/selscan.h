@@ -548,6 +548,7 @@ sscan_status sscan_glr_step(int64_t batch, int64_t dim, int dtype, float* state,
  *                  x too, if x is that tensor, dense and of its type); apart from all else
  *   codes, scales: y in 8 bits as sscan_i8_quant gives it (from y before its rounding to
  *                  dtype), both or neither; codes has the row stride codes_stride
+ *                  (with dim == 0 nothing is written: sscan_i8_quant has those rows' scales)
  * residual_dtype is SSCAN_F32, or dtype.  eps is at least 0 and finite.  Sums are float32:
  * a row whose sum of squares passes float32's range has r = 0, and one whose mean(s^2) + eps
  * is below its normal numbers (2^-126; never with eps of that size) has r infinite.
@@ -590,6 +591,7 @@ sscan_status sscan_rms_bwd(int64_t rows, int64_t dim, int dtype, int residual_dt
  *
  * (the quotient of the real numbers, ties to even; at most 127 in magnitude).  A row with
  * an infinity or NaN has the scale NaN and codes 0, so it comes out of a product as NaN.
+ * A row without channels (dim == 0; x and codes may be NULL) has the scale 2^-126.
  * Weights are brought into this form once, each output's row by itself; activations at each
  * call, or by sscan_rms_fwd.
  *

@@ -284,7 +284,7 @@ __global__ __launch_bounds__(block_of(LANES)) void rms_fwd_kernel(RmsFwdParams p
         if (p.y) store_word(static_cast<Tin*>(p.y) + row * p.dim, (i * LANES + lane) * kWord, p.dim, v[i]);
       }
     }
-    if (p.codes) {
+    if (p.scales) {      // also of rows without channels, which have no codes
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < WORDS; ++i)

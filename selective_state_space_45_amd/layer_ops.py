@@ -142,6 +142,8 @@ def sscan_rms_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residu
         out["codes"], out["scales"] = codes, scales
     _together(x, residual, weight, y, kept, codes, scales)
     _run(x, _lib.sscan_rms_fwd, rows, dim, dt, _DTYPES[residual_dtype], px, sx, pres, pw, eps, py, pk, pc, sc, psc)
+    if want_codes and dim == 0:       # rows without channels have scales all the same
+        _run(x, _lib.sscan_i8_quant, rows, 0, dt, None, 0, None, 0, psc)
     return out
 
 

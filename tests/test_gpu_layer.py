@@ -574,3 +574,19 @@ def test_norm_in_place_of_the_stream_itself(ss, dtype, rtype):
     got = ss.sscan_rms_bwd(grad, w, dy, dresidual=grad, want_dresidual=True, out=dict(dresidual=grad))
     for k in want:
         same(got[k], want[k], k + " from s")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lead", [(1,), (300,), (2, 5)])
+def test_rows_without_channels_have_scales(ss, dtype, lead):
+    """2^-126, as rows of zeros have, from the quantisation and from the norm; a product of such rows
+    is its bias."""
+    x = torch.empty(*lead, 0, dtype=dtype, device="cuda")
+    bias = normal(1, 9)
+    w, ws = ss.sscan_i8_quant(torch.empty(9, 0, device="cuda"), scales=torch.full((9,), float("nan"), device="cuda"))
+    nan = lambda: torch.full(lead, float("nan"), device="cuda")
+    normed = ss.sscan_rms_fwd(x, want_codes=True, out=dict(scales=nan()))
+    for codes, scales in (ss.sscan_i8_quant(x, scales=nan()), (normed["codes"], normed["scales"])):
+        assert codes.shape == x.shape and bool((scales == 2.0 ** -126).all())
+        same(ss.sscan_i8_matmul(codes, scales, w, ws, bias=bias, dtype=F32), bias.expand(*lead, 9), "product")
+    assert bool((ws == 2.0 ** -126).all())
