@@ -109,8 +109,9 @@ def sscan_rms_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residu
     tensor); residual: x's shape, dense, float32 or x's type; weight [dim] float32 (default
     ones).  Returns a dict with y (want_y), codes and scales (want_codes: y in 8 bits as
     ``sscan_i8_quant`` gives it) and residual, the sum s (want_residual, by default when a
-    residual is given; residual_dtype: its type without one, default x's).  ``out`` may supply
-    tensors by name; out["residual"] may be residual itself."""
+    residual is given; residual_dtype: its type without one, default x's), and nothing else.
+    ``out`` may supply tensors by name; those that are not wanted are neither written nor
+    returned; out["residual"] may be residual itself."""
     rows, dim = _tokens(x, "x")
     dt = _float(x, "x")
     shape, dtype = x.shape, x.dtype
@@ -126,8 +127,8 @@ def sscan_rms_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residu
         want_residual = residual is not None
     px, sx = _rows(x, "x", dtype, shape)
     pres, pw = _at(residual, "residual", residual_dtype, shape), _at(weight, "weight", _F32, (dim,))
-    out = dict(out) if out else {}
-    get = out.get
+    get = out.get if out else {}.get
+    out = {}                          # a given tensor that is not written has no place in it
     y = py = kept = pk = codes = pc = scales = psc = None
     sc = dim
     if want_y:
@@ -154,8 +155,10 @@ def sscan_rms_bwd(s: torch.Tensor, weight: Optional[torch.Tensor], dy: torch.Ten
     """Backward pass of ``sscan_rms_fwd``, given dy and, optionally, dresidual, the gradient
     of the sum s from what follows (of s's type).  s: the sum that the forward kept, or x
     itself without a residual.  Returns a dict with dx (dy's type), dresidual (the same
-    gradient in s's type) and dweight (by default when a weight is given); ``out`` may supply
-    tensors by name; dx also as columns of a wider tensor, out["dresidual"] as dresidual itself."""
+    gradient in s's type, want_dresidual) and dweight (by default when a weight is given), and
+    nothing else; ``out`` may supply tensors by name, of which those that are not wanted are
+    neither written nor returned; dx also as columns of a wider tensor, out["dresidual"] as
+    dresidual itself."""
     rows, dim = _tokens(dy, "dy")
     dt = _float(dy, "dy")
     shape, dtype, kept = dy.shape, dy.dtype, s.dtype
@@ -165,23 +168,27 @@ def sscan_rms_bwd(s: torch.Tensor, weight: Optional[torch.Tensor], dy: torch.Ten
         want_dweight = weight is not None
     ps, ss = _rows(s, "s", kept, shape)
     pw, pdy, pdk = _at(weight, "weight", _F32, (dim,)), _at(dy, "dy", dtype, shape), _at(dresidual, "dresidual", kept, shape)
-    out = dict(out) if out else {}
+    get = out.get if out else {}.get
+    out = {}                          # a given tensor that is not written has no place in it
     dx = dres = dw = ws = None
     pdx, sdx = None, dim
     if want_dx:
-        dx = out.get("dx")
+        dx = get("dx")
         if dx is None:
-            dx = out["dx"] = torch.empty_like(dy)
+            dx = torch.empty_like(dy)
+        out["dx"] = dx
         pdx, sdx = _rows(dx, "dx", dtype, shape)
     if want_dresidual:
-        dres = out.get("dresidual")
+        dres = get("dresidual")
         if dres is None:
-            dres = out["dresidual"] = torch.empty(shape, dtype=kept, device=dy.device)
+            dres = torch.empty(shape, dtype=kept, device=dy.device)
+        out["dresidual"] = dres
     pws = nws = None
     if want_dweight:
-        dw = out.get("dweight")
+        dw = get("dweight")
         if dw is None:
-            dw = out["dweight"] = torch.empty(dim, dtype=_F32, device=dy.device)
+            dw = torch.empty(dim, dtype=_F32, device=dy.device)
+        out["dweight"] = dw
         ws, pws, nws = _scratch(workspace, _lib.sscan_rms_bwd_workspace_size(rows, dim), dy.device)
     _together(dy, s, weight, dresidual, dx, dres, dw, ws)
     _run(dy, _lib.sscan_rms_bwd, rows, dim, dt, _DTYPES[kept], ps, ss, pw, eps, pdy, pdk, pdx, sdx,

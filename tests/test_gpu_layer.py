@@ -590,3 +590,25 @@ def test_rows_without_channels_have_scales(ss, dtype, lead):
         assert codes.shape == x.shape and bool((scales == 2.0 ** -126).all())
         same(ss.sscan_i8_matmul(codes, scales, w, ws, bias=bias, dtype=F32), bias.expand(*lead, 9), "product")
     assert bool((ws == 2.0 ** -126).all())
+
+
+def test_norm_returns_only_what_it_wrote(ss):
+    """Tensors that are supplied for what is not wanted are left alone and not returned."""
+    x, w = normal(1, 9, 40), normal(2, 40)
+    f32 = lambda *s: torch.full(s, 7.0, device="cuda")
+    room = dict(y=f32(9, 40), residual=f32(9, 40), codes=torch.full((9, 40), 7, dtype=torch.int8, device="cuda"), scales=f32(9))
+    for kw, names in ((dict(), {"y"}), (dict(want_y=False, want_codes=True), {"codes", "scales"}),
+                      (dict(want_y=False, want_residual=True), {"residual"}), (dict(residual=x), {"y", "residual"})):
+        given = {k: v.clone() for k, v in room.items()}
+        got = ss.sscan_rms_fwd(x, w, out=given, **kw)
+        assert set(got) == names and set(given) == set(room)
+        for k in room:
+            assert (got[k] is given[k]) if k in names else bool((given[k] == 7).all()), k
+    room = dict(dx=f32(9, 40), dresidual=f32(9, 40), dweight=f32(40))
+    for kw, names in ((dict(), {"dx", "dweight"}), (dict(want_dx=False, want_dresidual=True, want_dweight=False), {"dresidual"}),
+                      (dict(want_dweight=False), {"dx"})):
+        given = {k: v.clone() for k, v in room.items()}
+        got = ss.sscan_rms_bwd(x, w, x, out=given, **kw)
+        assert set(got) == names and set(given) == set(room)
+        for k in room:
+            assert (got[k] is given[k]) if k in names else bool((given[k] == 7).all()), k
