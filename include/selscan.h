@@ -557,7 +557,7 @@ sscan_status sscan_rms_fwd(int64_t rows, int64_t dim, int dtype, int residual_dt
                            const void* residual, const float* weight, float eps, void* y, void* residual_out,
                            int8_t* codes, int64_t codes_stride, float* scales, void* stream);
 
-/* Workspace bytes of sscan_rms_bwd. */
+/* Workspace bytes of sscan_rms_bwd; no less for more rows or channels. */
 size_t sscan_rms_bwd_workspace_size(int64_t rows, int64_t dim);
 
 /*
@@ -649,7 +649,7 @@ sscan_status sscan_dwconv_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_
                               const float* initial_state, const int32_t* offsets, int64_t num_seqs, void* y,
                               float* last_state, void* stream);
 
-/* Workspace bytes of sscan_dwconv_bwd. */
+/* Workspace bytes of sscan_dwconv_bwd; no less when any of the sizes grows. */
 size_t sscan_dwconv_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t dconv);
 
 /*

@@ -471,6 +471,8 @@ __global__ __launch_bounds__(64) void dwconv_step_kernel(ConvStepParams p, int64
 
 namespace {
 
+constexpr int kConvFull = 4096;   // waves that keep memory busy
+
 // Tokens of a wave's block, workgroups along the tokens and channels, workgroups in all.
 struct ConvPlan {
   int tokens, nblk, nct;
@@ -485,7 +487,7 @@ ConvPlan plan_of(int64_t batch, int64_t L, int64_t dim, int V) {
   ConvPlan q;
   q.nct = static_cast<int>((dim + 64 * V - 1) / (64 * V));
   for (q.tokens = 64; q.tokens > 16; q.tokens /= 2)
-    if (batch * ((L + q.tokens - 1) / q.tokens) * q.nct >= 4096) break;
+    if (batch * ((L + q.tokens - 1) / q.tokens) * q.nct >= kConvFull) break;
   q.nblk = static_cast<int>((L + kConvWaves * q.tokens - 1) / (kConvWaves * q.tokens));
   q.main = batch * q.nblk * q.nct;
   return q;
@@ -540,11 +542,16 @@ hipError_t by_type(int taps, bool bf16, F&& f) {
 
 }  // namespace
 
+// The most that plan_of can ask for any call up to these sizes, in either type, so that a buffer for
+// the longest batch serves the shorter ones.  Blocks of 64 tokens: a set of sums for each 256.  Shorter
+// blocks: one for at least 64 tokens, and fewer than kConvFull / nct sets, since blocks of twice the
+// length were fewer than kConvFull waves; with dim <= nct 64 V that is kConvFull 64 V numbers of each
+// parameter, V at most 4.
 size_t dwconv_bwd_workspace_bytes(int64_t batch, int64_t L, int64_t dim, int taps) {
   if (batch <= 0 || L <= 0 || dim <= 0) return 0;
-  // of the type with the more workgroups along the tokens
-  const int64_t a = plan_of(batch, L, dim, lane_channels(dim, 2)).nblk, b = plan_of(batch, L, dim, lane_channels(dim, 4)).nblk;
-  return static_cast<size_t>(batch) * (a > b ? a : b) * dim * (taps + 1) * 4;
+  const int64_t least = batch * ((L + 255) / 256) * dim, most = batch * ((L + 63) / 64) * dim, bound = kConvFull * 64 * 4;
+  const int64_t shorter = most < bound ? most : bound;
+  return static_cast<size_t>(least > shorter ? least : shorter) * (taps + 1) * 4;
 }
 
 hipError_t launch_dwconv_fwd(const ConvParams& p, int taps, bool bf16, hipStream_t s) {

@@ -497,8 +497,11 @@ hipError_t bwd(const RmsBwdParams& p, hipStream_t s) {
 
 }  // namespace
 
+// As many sums as workgroups of a row each would leave, which is no less for more rows or channels:
+// a buffer for the longest batch serves the shorter ones, whose plan may take four times the
+// workgroups (2048 channels: 256 at 1024 rows, 512 at 1023).
 size_t rms_bwd_workspace_bytes(int64_t rows, int64_t dim) {
-  return rows > 0 && dim > 0 ? static_cast<size_t>(groups_of(rows, dim)) * dim * 4 : 0;
+  return rows > 0 && dim > 0 ? static_cast<size_t>(rows < kRmsGroups ? rows : kRmsGroups) * dim * 4 : 0;
 }
 
 hipError_t launch_rms_fwd(const RmsFwdParams& p, bool bf16, bool kept_bf16, hipStream_t s) {

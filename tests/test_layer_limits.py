@@ -47,3 +47,34 @@ def test_convolution_step(lib):  # noqa: F811
     accepts(lib, conv_step, batch=MOST, dim=64, pool=MOST, y=None)
     refuses(lib, conv_step, batch=MOST + 1, dim=64, pool=MOST + 1)
     refuses(lib, conv_step, batch=1, dim=2 ** 28, pool=2 ** 20)
+
+
+def never_shrinks(size, fixed, values, at):
+    """size(*fixed) with its argument `at` going through `values` in order."""
+    last = 0
+    for v in values:
+        args = list(fixed)
+        args[at] = v
+        now = size(*args)
+        assert now >= last, (args, now, last)
+        last = now
+
+
+COUNTS = sorted({1, 2, 3, 5, 7} | {2 ** k + d for k in range(4, 16) for d in (-1, 0, 1)})
+
+
+def test_workspaces_serve_smaller_calls(lib):  # noqa: F811
+    """A buffer for the longest batch serves every shorter one: sizes do not shrink as any count grows."""
+    norm, conv = lib.sscan_rms_bwd_workspace_size, lib.sscan_dwconv_bwd_workspace_size
+    for dim in (1, 64, 96, 512, 513, 1535, 2048, 2049, 2560, 8193, 32768):
+        never_shrinks(norm, (0, dim), COUNTS, 0)
+    for rows in (1, 511, 1023, 1024, 4096, 70000):
+        never_shrinks(norm, (rows, 0), [d for d in COUNTS if d <= 32768], 1)
+    for dim in (1, 3, 4, 130, 257, 1535, 2048, 2560, 10240):
+        for batch in (1, 3, 8, 64):
+            never_shrinks(conv, (batch, 0, dim, 4), COUNTS, 1)
+        for seqlen in (1, 33, 65, 700, 4096):
+            never_shrinks(conv, (0, seqlen, dim, 4), COUNTS, 0)
+    for batch, seqlen in ((1, 1), (1, 4094), (1, 16411), (8, 4032), (8, 4096), (300, 64)):
+        never_shrinks(conv, (batch, seqlen, 0, 4), COUNTS, 2)
+        never_shrinks(conv, (batch, seqlen, 2048, 0), (1, 2, 3, 4), 3)
