@@ -53,25 +53,33 @@ __device__ __forceinline__ void bounds(const int32_t* offsets, int nseq, int L, 
   q.hi = to > L ? L : to;
   if (q.hi <= t) q.hi = kNone, q.lo = kNone;
 }
-__device__ __forceinline__ Sequence sequence_of(const int32_t* offsets, int nseq, int L, int64_t b, int t) {
-  if (!offsets) return {b, 0, L};
-  int lo = 0, hi = nseq;                             // the last s with offsets[s] <= t, or 0
+// The last s from `lo` on with offsets[s] <= t, or lo.
+__device__ __forceinline__ int last_begun(const int32_t* offsets, int lo, int nseq, int t) {
+  int hi = nseq;
   while (hi - lo > 1) {
     const int mid = lo + (hi - lo) / 2;
     if (offsets[mid] <= t) lo = mid;
     else hi = mid;
   }
-  Sequence q{lo, 0, 0};
+  return lo;
+}
+__device__ __forceinline__ Sequence sequence_of(const int32_t* offsets, int nseq, int L, int64_t b, int t) {
+  if (!offsets) return {b, 0, L};
+  Sequence q{last_begun(offsets, 0, nseq, t), 0, 0};
   bounds(offsets, nseq, L, t, q);
   return q;
 }
-// The sequence that begins at t, where one ended.
+// The sequence that begins at t, where one ended: the next, or one after empty ones, of which there
+// may be any number.
 __device__ __forceinline__ void follow(const int32_t* offsets, int nseq, int L, int t, Sequence& q) {
   if (!offsets) {
     q.lo = q.hi = kNone;
     return;
   }
-  while (q.s + 1 < nseq && offsets[q.s + 1] <= t) ++q.s;
+  int s = static_cast<int>(q.s);
+  if (s + 1 < nseq && offsets[s + 1] <= t) ++s;
+  if (s + 1 < nseq && offsets[s + 1] <= t) s = last_begun(offsets, s + 1, nseq, t);
+  q.s = s;
   bounds(offsets, nseq, L, t, q);
 }
 

@@ -460,3 +460,33 @@ def test_example_serves_prefill_and_decode_alike(block):
     torch.manual_seed(3)
     first, last, worst = block.main(steps=2, depth=3, tell=lambda *a: None)
     assert np.isfinite([first, last]).all() and worst <= 0.05
+
+
+def test_convolution_past_many_empty_requests(ss):  # noqa: F811
+    """A million empty requests between two others: the second is found at once, wherever a block of
+    tokens meets it.  With the empty ones in front, which the search at a block's first token passes,
+    the same calls take some 0.1 ms; one after another the empty ones took 80 ns each, 84 ms a pass."""
+    L, D, many = 200, 72, 1 << 20
+    x, dy, w, b = normal(1, 1, L, D), normal(2, 1, L, D), normal(3, D, 4), normal(4, D)
+    two = torch.tensor([0, 103, 190], dtype=torch.int32, device="cuda")
+    fill = lambda v: torch.full((many,), v, dtype=torch.int32, device="cuda")
+    middle, front = torch.cat([two[:2], fill(103), two[2:]]), torch.cat([fill(0), two])
+
+    def both(off):
+        y = ss.sscan_dwconv_fwd(x, w, b, offsets=off)
+        return y, ss.sscan_dwconv_bwd(x, w, dy, b, offsets=off, want_dinitial_state=False)
+
+    want = both(two)
+    took = []
+    for off in (middle, front):
+        y, g = both(off)
+        same(y, want[0], "y")
+        for k in g:
+            same(g[k], want[1][k], k)
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        both(off)
+        end.record()
+        torch.cuda.synchronize()
+        took.append(begin.elapsed_time(end))
+    assert took[0] <= 10 * took[1] + 10, took
