@@ -45,8 +45,9 @@ def rms_bwd(s, dy, weight=None, dresidual=None, eps=1e-5):
     return ds, (dy * s * r).reshape(-1, s.shape[-1]).sum(0)
 
 
-def rms_bwd_error(s, dy, weight=None, dresidual=None, eps=1e-5):
-    """(of ds, of dweight).  The mean's own error is relative to its terms' magnitudes."""
+def rms_bwd_error(s, dy, weight=None, dresidual=None, eps=1e-5, depth=None):
+    """(of ds, of dweight).  The mean's own error is relative to its terms' magnitudes.  depth: the
+    additions that a term of dweight passes through, at most as many as there are rows."""
     s, dy, w, dres = f64(s, dy, weight, dresidual)
     n = chain(s.shape[-1])
     g = dy if w is None else dy * w
@@ -56,7 +57,7 @@ def rms_bwd_error(s, dy, weight=None, dresidual=None, eps=1e-5):
     if dres is not None:
         ds = ds + U * np.abs(dres)
     terms = np.abs(dy * s * r).reshape(-1, s.shape[-1])
-    return ds + U * np.abs(ds), U * terms.sum(0) * (terms.shape[0] + n / 2 + 8)
+    return ds + U * np.abs(ds), U * terms.sum(0) * ((terms.shape[0] if depth is None else depth) + n / 2 + 8)
 
 
 def i8_rows(x):
@@ -118,15 +119,16 @@ def conv_fwd(x, w, b=None, silu=True, initial_state=None, offsets=None):
     return y, np.stack(last)
 
 
-def conv_bwd(x, w, dy, b=None, silu=True, initial_state=None, offsets=None, dlast_state=None):
-    """Gradients as a dict, and under "error" bounds of the kernels' arithmetic for each."""
+def conv_bwd(x, w, dy, b=None, silu=True, initial_state=None, offsets=None, dlast_state=None, depth=None):
+    """Gradients as a dict, and under "error" bounds of the kernels' arithmetic for each.  depth: the
+    additions that a term of a parameter's gradient passes through, at most as many as there are tokens."""
     x, w, dy, b, h0, dlast = f64(x, w, dy, b, initial_state, dlast_state)
     dim, K = w.shape
     seqs = sequences(x.shape, offsets)
     out = dict(dx=np.zeros_like(x), dconv_w=np.zeros((dim, K)), dconv_b=np.zeros(dim),
                dinitial_state=np.zeros((len(seqs), dim, K - 1)))
     err = {k: np.zeros_like(v) for k, v in out.items()}
-    tokens = x.shape[0] * x.shape[1] + 1
+    tokens = x.shape[0] * x.shape[1] + 1 if depth is None else depth
     for n, (row, lo, hi) in enumerate(seqs):
         T = hi - lo
         line = _line(x, h0, n, row, lo, hi, dim, K)

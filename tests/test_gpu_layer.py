@@ -612,3 +612,29 @@ def test_norm_returns_only_what_it_wrote(ss):
         assert set(got) == names and set(given) == set(room)
         for k in room:
             assert (got[k] is given[k]) if k in names else bool((given[k] == 7).all()), k
+
+
+@pytest.mark.parametrize("rows,dim", [(1024, 513), (1024, 2048), (1027, 1535), (2051, 1025), (2051, 1537), (4094, 1535), (4094, 2048)])
+@pytest.mark.parametrize("dtype,rtype", TYPES)
+def test_norm_backward_of_one_wave_a_row(ss, rows, dim, dtype, rtype):
+    """From 1024 rows on a wave holds rows of up to 2048 channels, in two to four words of a lane here.
+    A term of dweight passes through its wave's rows (in at most 512 workgroups of 4), 4 waves, a 16th of
+    the workgroups, 16 waves, and a rounding or two of its own."""
+    s, dy, dk, w = (normal(1, rows, dim, dtype=rtype), normal(2, rows, dim, dtype=dtype), normal(3, rows, dim, dtype=rtype),
+                    normal(4, dim))
+    groups = min(512, -(-rows // 4))
+    depth = -(-rows // (4 * groups)) + 3 + -(-groups // 16) + 15 + 2
+    need = ss.rms_bwd_workspace_size(rows, dim)
+    room = torch.full((need + 4096,), 90, dtype=torch.uint8, device="cuda")
+    g = ss.sscan_rms_bwd(s, w, dy, dresidual=dk, want_dresidual=True, workspace=room)
+    assert bool((room[need:] == 90).all())
+    ds, dw = layer.rms_bwd(host(s), host(dy), host(w), host(dk))
+    eds, edw = layer.rms_bwd_error(host(s), host(dy), host(w), host(dk), depth=depth)
+    close(g["dx"], ds, eds, "dx")
+    close(g["dresidual"], ds, eds, "dresidual")
+    close(g["dweight"], dw, edw, "dweight")
+    g = ss.sscan_rms_bwd(s, None, dy, want_dweight=True)
+    ds, dw = layer.rms_bwd(host(s), host(dy))
+    eds, edw = layer.rms_bwd_error(host(s), host(dy), depth=depth)
+    close(g["dx"], ds, eds, "dx alone")
+    close(g["dweight"], dw, edw, "dweight without weight")

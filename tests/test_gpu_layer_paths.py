@@ -490,3 +490,53 @@ def test_convolution_past_many_empty_requests(ss):  # noqa: F811
         torch.cuda.synchronize()
         took.append(begin.elapsed_time(end))
     assert took[0] <= 10 * took[1] + 10, took
+
+
+@pytest.mark.parametrize("K,silu", [(4, True), (3, False)])
+@pytest.mark.parametrize("dtype,batch,seqlen,dim,block", [
+    (F32, 1, 16411, 1535, 32), (F32, 1, 26201, 1535, 64), (BF16, 1, 16411, 2560, 32), (BF16, 1, 26201, 2560, 64),
+    (F32, 8, 1030, 2051, 32), (F32, 8, 2050, 2051, 64), (BF16, 8, 2047, 2050, 32), (BF16, 8, 4093, 2050, 64)])
+def test_convolution_in_longer_blocks(ss, dtype, batch, seqlen, dim, block, K, silu):  # noqa: F811
+    """Where at least 4096 waves have work, a wave has 32 or 64 tokens; dense, and packed requests that end
+    around the borders of blocks, with states, infinities and NaN in the padding.  Channels are
+    independent: some of every part of a row are compared.  A term of a parameter's gradient passes through
+    its wave's tokens, 4 waves, a 16th of the workgroups along the tokens, 16 waves, and a rounding
+    or two of its own."""
+    r = np.random.default_rng(seqlen)
+    off = None
+    if batch == 1:
+        around = [c for k in range(32, 400, 32) for c in (k - 3, k, k + 1)]
+        off = np.array([0, 0, 0, *sorted({1, 2, 6, *around, *r.integers(400, seqlen - 41, 60)}), seqlen - 41, seqlen - 41], np.int32)
+    seqs = batch if off is None else len(off) - 1
+    x, dy = filled(batch * seqlen, dim, seed=1, dtype=dtype).view(batch, seqlen, dim), \
+        filled(batch * seqlen, dim, seed=2, dtype=dtype).view(batch, seqlen, dim)
+    w, b = normal(3, dim, K), normal(4, dim)
+    h0, dlast = filled(seqs, dim, K - 1, seed=5, dtype=F32), filled(seqs, dim, K - 1, seed=6, dtype=F32)
+    doff = None
+    if off is not None:
+        doff = torch.from_numpy(off).cuda()
+        x[0, off[-1]:], dy[0, off[-1]:] = float("nan"), float("inf")
+    y, last = ss.sscan_dwconv_fwd(x, w, b, silu=silu, initial_state=h0, offsets=doff, return_last_state=True)
+    need = ss.dwconv_bwd_workspace_size(batch, seqlen, dim, K)
+    room = torch.full((need + 4096,), 90, dtype=torch.uint8, device="cuda")
+    g = ss.sscan_dwconv_bwd(x, w, dy, b, silu=silu, initial_state=h0, offsets=doff, dlast_state=dlast, workspace=room)
+    assert bool((room[need:] == 90).all())
+    cols = sorted({0, 1, 2, 3, 63, 64, 127, 128, 129, 255, 256, 257, dim // 2, *range(dim - 5, dim), *r.integers(0, dim, 16).tolist()})
+    pick = lambda t: host(t[:, :, cols])
+    args = (pick(x), host(w[cols]))
+    kw = dict(silu=silu, initial_state=host(h0[:, cols]), offsets=off)
+    want, wlast = layer.conv_fwd(*args, b=host(b[cols]), **kw)
+    inside = np.array(args[0])
+    if off is not None:
+        inside[:, off[-1]:] = 0                     # (the bound is formed of all tokens)
+    close(y[:, :, cols], want, layer.conv_fwd_error(inside, args[1], host(b[cols]), **kw), "y")
+    np.testing.assert_array_equal(host(last[:, cols]), wlast)
+    depth = block + 3 + -(-batch * -(-seqlen // (4 * block)) // 16) + 15 + 2
+    ref = layer.conv_bwd(*args, pick(dy), b=host(b[cols]), dlast_state=host(dlast[:, cols]), depth=depth, **kw)
+    close(g["dx"][:, :, cols], ref["dx"], ref["error"]["dx"], "dx")
+    for k in ("dconv_w", "dconv_b"):
+        close(g[k][cols], ref[k], ref["error"][k], k)
+    close(g["dinitial_state"][:, cols], ref["dinitial_state"], ref["error"]["dinitial_state"], "dinitial_state")
+    if off is not None:
+        assert not bool(y[0, off[-1]:].any()) and not bool(g["dx"][0, off[-1]:].any())
+    assert all(bool(t.isfinite().all()) for t in (y, last, *g.values()))

@@ -135,3 +135,18 @@ def test_the_norm_before_8_bits_loses_no_more_than_half_a_step():
     y, _ = layer.rms_fwd(r.normal(size=(5, 64)), r.normal(size=64))
     codes, scales = layer.i8_rows(y)
     assert (np.abs(codes * scales[:, None] - y) <= scales[:, None] * (0.5 + 2e-5)).all()
+
+
+def test_bounds_by_depth_are_below_one_row_or_token():
+    """With the additions that a kernel's sums really go through, the bound of a parameter's gradient is
+    below the share of one average row of 4094, or token of 26201, so that one left out would show."""
+    r = np.random.default_rng(3)
+    s, dy, w = r.standard_normal((4094, 40)), r.standard_normal((4094, 40)), r.standard_normal(40)
+    _, rr = layer.rms_fwd(s)
+    _, bound = layer.rms_bwd_error(s, dy, w, depth=54)
+    assert (bound < 0.1 * np.abs(dy * s * rr).mean(0)).all()
+    x, dy, w = r.standard_normal((1, 26201, 8)), r.standard_normal((1, 26201, 8)), r.standard_normal((8, 4))
+    err = layer.conv_bwd(x, w, dy, silu=False, depth=91)["error"]
+    assert (err["dconv_b"] < 0.25 * np.abs(dy).mean((0, 1))).all()
+    for k in range(4):
+        assert (err["dconv_w"][:, k] < 0.25 * np.abs(dy[0, 3 - k:] * x[0, :26201 - 3 + k]).mean(0)).all()
