@@ -618,7 +618,8 @@ sscan_status sscan_i8_quant(int64_t rows, int64_t dim, int dtype, const void* x,
  *   bias        : [n] (float32), NULL: zero
  *   out         : [m, n] (dtype), row stride out_stride
  * Any strides and alignment work; rows at multiples of 16 bytes with k a multiple of 128 are
- * read fastest.  k is at most SSCAN_I8_MAX_K, m and n at most 2^31 - 1.  With k == 0 the sums are zero.
+ * read fastest.  k is at most SSCAN_I8_MAX_K, m and n at most 2^31 - 1, and ceil(m / 16) ceil(n / 16)
+ * at most 2^31 - 1 as well.  With k == 0 the sums are zero.
  */
 sscan_status sscan_i8_matmul(int64_t m, int64_t n, int64_t k, const int8_t* a, int64_t a_stride,
                              const float* a_scales, const int8_t* b, int64_t b_stride, const float* b_scales,

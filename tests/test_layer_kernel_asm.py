@@ -8,7 +8,7 @@ from test_glr_kernel_asm import scratch
 from test_kernel_asm import _compile_asm, _hipcc
 
 # kernels of the source, and for name patterns the scratch they may use: the norm's backward
-# over rows of 16385 to 32768 channels holds 32 of two inputs in each of 1024 lanes
+# over rows of 24577 to 32768 channels holds 32 of two inputs in each of 1024 lanes
 SOURCES = {
     "sscan_rms.hip": (84, {r"rms_bwd_kernel\w*Li1024ELi4E": 64}),
     "sscan_i8_matmul.hip": (14, {}),
