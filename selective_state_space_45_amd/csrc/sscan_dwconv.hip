@@ -9,7 +9,9 @@
 // a group inside one sequence without a test or a move, any other by a loop over its tokens (with
 // the tests in every token the forward of 8 x 4096 x 2048 bf16 took 66 us, now 51; the backward
 // 132, now 108).  At 5 TB/s their reads and writes take 54 and 81 us; the backward issues about
-// 130 vector instructions for each 4 channels of a token and wave, some 60 us of them.
+// 130 vector instructions for each 4 channels of a token and wave, some 60 us of them.  Rows of fewer
+// than 256 bf16 channels leave lanes repeating the last word: 524288 x 64 forward 57 us of 27, backward 132
+// of 40 (131072 x 256: 26 and 48).
 #include "sscan_layer.h"
 
 namespace sscan {

@@ -6,8 +6,13 @@
 // holds row l % 16, bytes 16 (l / 16) .. + 15 of 64).  The order of k is the same on both
 // sides and otherwise free, since the sums are whole numbers.
 //
-// Large products are bound by power: the matrix units alone, on random codes, reach 4100
-// TOP/s with this instruction and 3450 with v_mfma_i32_32x32x32_i8, on zeros 4850 and 4970.
+// The matrix units alone, on random codes, reach 4100 TOP/s with this instruction (at 1.95 GHz) and
+// 3450 with v_mfma_i32_32x32x32_i8, on zeros 4850 and 4970: power sets the clock.  Large products stay
+// below that for two reasons.  32768 x 4096 x k takes 50 us and 0.77 us for each 64 of k (k = 512,
+// 1024, 2048, 4096: 98, 153, 248, 446 us).  The 50 us do not grow with k: all workgroups come to
+// their outputs together, 268 MB or 54 us of memory, while the matrix units stand still.  And in
+// 64 of k they are busy for 1024 of 1180 to 1290 cycles, at 1.8 GHz.  (On zeros, at 2.35 GHz, 2048 takes
+// 224 us.)
 #include "sscan_layer.h"
 
 namespace sscan {
@@ -456,7 +461,8 @@ int64_t tiles_of(const MatmulParams& p, int side) {
 }
 
 // The tile's side.  Small tiles while the compute units hold them all at once, two each: what a
-// depth of k takes then is latency, which grows with the tile (256 x 2560 x 5120, in 160 tiles
+// depth of k takes then is latency, which grows with the tile (one set of inputs again and
+// again, which stays in L2; three in turn take 21 us for the first: 256 x 2560 x 5120, in 160 tiles
 // of 64 x 64 15 us, in 40 of 128 x 128 28, in 10 of 256 x 256 55; but 256 x 10240 x 2560, in 640 of
 // 64 x 64 21 us, in 160 of 128 x 128 17; 2048 x 4096 x 2048, 512 tiles of 128 x 128 22 us, 128 of
 // 256 x 256 28).  Otherwise the largest, which reads least (4096 x 2560 x

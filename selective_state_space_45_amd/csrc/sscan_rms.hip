@@ -308,8 +308,10 @@ __global__ __launch_bounds__(block_of(LANES)) void rms_fwd_kernel(RmsFwdParams p
 
 // Rows as in the forward; each workgroup sums its rows' part of dweight in registers.  1024 lanes of
 // 4 words (rows of 24577 to 32768 channels) spill 56 to 60 bytes a lane.
-// Measured: 32768 x 2048 bf16 with a float32 stream 205 us of 161 at 5 TB/s (the forward 147 of
-// 161: part of what it reads and writes stays cached), 4094 x 1535 float32 30 of 25.
+// Measured: 32768 x 2048 bf16 with a float32 stream 205 us of 215 at 5 TB/s (the forward 147 of
+// 161: part of what both read and write stays cached), 4094 x 1535 float32 30 of 25.  Rows of few
+// channels leave lanes of their wave idle: 131072 x 256 bf16 90 of 40 (the forward 30 of 27), 524288 x 64
+// 336 of 40 (108 of 27), 65536 x 512 36 of 40.
 template <typename Tin, typename Tres, int LANES, int WORDS>
 __global__ __launch_bounds__(block_of(LANES)) void rms_bwd_kernel(RmsBwdParams p) {
   constexpr int kRows = block_of(LANES) / LANES;
